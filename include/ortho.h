@@ -22,6 +22,11 @@
  *                  neuron (row) before the update (declared below).
  *   dion2_step     Dion2: the rows of largest norm orthonormalised and applied,
  *                  with error feedback (declared below).
+ *   fp8_quantize, fp8_matmul, rms_norm_fp8, rms_norm_backward
+ *                  the linear layer whose weight the steps update, in 8 bits:
+ *                  its products (the weight gradient G among them), the norm
+ *                  before it and the conversion of its operands (declared
+ *                  below, after the steps).
  *   newton_schulz  Muon's Newton-Schulz orthogonalisation, the full-rank
  *                  comparison path.  Same talk, passage contrasting SGD with an
  *                  orthonormal update (take U V^T of the SVD) and the passage on
@@ -61,7 +66,12 @@ extern "C" {
 
 #define ORTHO_ABI_VERSION 1
 
-typedef enum { ORTHO_F32 = 0, ORTHO_BF16 = 1 } ortho_dtype;
+typedef enum {
+  ORTHO_F32 = 0,
+  ORTHO_BF16 = 1,
+  ORTHO_E4M3 = 2,   /* 8-bit codes: OCP e4m3, largest value 448, no infinities */
+  ORTHO_E8M0 = 3    /* 8-bit scales: byte b stands for 2^(b - 127), 255 for NaN */
+} ortho_dtype;
 
 /* A row-major device matrix view.  `data` must be 16-byte aligned for the
  * vectorised loads; other alignments and ragged sizes are handled element by
@@ -82,7 +92,8 @@ typedef enum {
   ORTHO_E_RANK = 4,       /* r outside [1, min(m, n)] or r != Q.cols */
   ORTHO_E_LAYOUT = 5,     /* ld < cols, or a size too large to index */
   ORTHO_E_WORKSPACE = 6,  /* ws is NULL or ws_bytes is below the required size */
-  ORTHO_E_PARAM = 7,      /* mu outside [0,1], non-finite lr/scale/abc, steps < 0, batch < 1 */
+  ORTHO_E_PARAM = 7,      /* mu outside [0,1], non-finite lr/scale/abc, steps < 0, batch < 1,
+                             eps < 0 or non-finite, block_rows other than 1 and 128 */
   ORTHO_E_HIP = 8,        /* a HIP launch failed (no device, invalid stream, ...) */
   ORTHO_E_SCRATCH = 9     /* dion_step_noalloc: the problem needs more than
                              ORTHO_NOALLOC_SCRATCH_BYTES of workspace */
@@ -269,6 +280,102 @@ size_t ortho_dion2_workspace_size(int64_t m, int64_t n, int32_t k);
 ortho_status dion2_step(ortho_mat X, ortho_mat G, ortho_mat M, int32_t k, int32_t steps,
                         const float* abc, float mu, float lr, float scale, int32_t* selected,
                         void* ws, size_t ws_bytes, void* stream);
+
+/* ---- 8-bit matrices with a scale for each block of 128 --------------------
+ *
+ * The matrices that the steps above update are the weights W (out x in) of
+ * linear layers.  Between two steps a training program forms the layer's
+ * products; with T tokens (rows of x, y and dy)
+ *     y = x W^T          fp8_matmul(x, W)
+ *     dx = dy W          fp8_matmul(dy, W^T)
+ *     G = dy^T x         fp8_matmul(dy^T, x^T), the gradient that a step reads
+ * Both operands of fp8_matmul have the contraction index along their rows, and
+ * fp8_quantize writes a matrix by rows, transposed, or both at once.
+ *
+ * An 8-bit R x C matrix is two ortho_mat: the codes (R x C, ORTHO_E4M3) and the
+ * scales, one for each block of 1 x 128 or 128 x 128 elements (R or ceil(R/128)
+ * rows, ceil(C/128) columns; the last block may be shorter), ORTHO_F32 or
+ * ORTHO_E8M0.  Element = code * scale.  Power-of-two scales (ORTHO_E8M0) are
+ * applied by the matrix instructions themselves and make every scaling exact;
+ * fp32 scales use a block's whole 8-bit range.
+ *
+ * Rows of codes that start at multiples of 16 bytes (data and ld) are read and
+ * written fastest; any other layout is accepted. */
+
+/* X (m x n, ORTHO_F32 or ORTHO_BF16) as 8-bit codes and scales.
+ *   block_rows  1 (blocks of 1 x 128: activations, gradients) or 128 (blocks of
+ *               128 x 128: weights), else ORTHO_E_PARAM.
+ *   Q, S    NULL, or the codes (m x n) and scales of X.
+ *   QT, ST  NULL, or the codes (n x m) and scales of X^T, whose blocks lie along
+ *           X's columns; S and ST share a dtype.  At least one pair is given.
+ * With a the largest finite |x| of a block (1 / s, where it is not exact, is
+ * rounded to fp32 once):
+ *     ORTHO_F32   s = max(a / 448, 2^-126), code = x * (1 / s) to nearest even
+ *     ORTHO_E8M0  s = the smallest power of two >= 2^-126 with a <= 448 s
+ * and s = 1 for a = 0.  Infinite and NaN elements get the NaN code and do not
+ * enter a, so they spoil no other element. */
+ortho_status fp8_quantize(ortho_mat X, int32_t block_rows, const ortho_mat* Q, const ortho_mat* S,
+                          const ortho_mat* QT, const ortho_mat* ST, void* stream);
+
+/* The root-mean-square norm in front of a linear layer, with the residual's
+ * addition and the result in 8 bits (1 x 128 blocks):
+ *     r = X + Res, rounded to X's dtype
+ *     y = r / sqrt(mean(r^2) + eps) * W        row by row, in fp32
+ *     Q, S = the codes and scales of y (as fp8_quantize)
+ *   X     m x n, ORTHO_F32 or ORTHO_BF16; n <= 65536.
+ *   Res   NULL (r = X), or m x n of X's dtype.
+ *   W     1 x n, ORTHO_F32 or X's dtype.
+ *   eps   >= 0 and finite, else ORTHO_E_PARAM.
+ *   Sum   NULL, or m x n of X's dtype: receives r (the next residual, and what
+ *         rms_norm_backward takes as X).  May be the same memory as X or Res.
+ *   Y     NULL, or m x n of X's dtype: receives y, e.g. to be quantised along
+ *         the tokens for the weight gradient.
+ *   Q, S  m x n ORTHO_E4M3, and m x ceil(n / 128). */
+ortho_status rms_norm_fp8(ortho_mat X, const ortho_mat* Res, ortho_mat W, float eps,
+                          const ortho_mat* Sum, const ortho_mat* Y, ortho_mat Q, ortho_mat S,
+                          void* stream);
+
+/* Bytes of device workspace for rms_norm_backward on m x n.  Returns 0 for
+ * invalid sizes.  256-byte alignment required. */
+size_t ortho_rms_norm_backward_workspace_size(int64_t m, int64_t n);
+
+/* Gradient of rms_norm_fp8's y (8-bit rounding passed straight through).  With
+ * t = 1 / sqrt(mean(X^2) + eps), u = X t and h = dY W (row by row, fp32):
+ *     dX = t (h - u mean(h u)) (+ dSum)
+ *     dW = sum over the rows of dY u
+ *   dY    m x n, the gradient of y, X's dtype.
+ *   X     m x n, what was normalised (rms_norm_fp8's Sum).
+ *   W, eps  as in the forward call.
+ *   dSum  NULL, or m x n of X's dtype: the gradient that reaches Sum along the
+ *         residual, added to dX.
+ *   dX    m x n of X's dtype: the gradient of X and of Res.  May be the same
+ *         memory as dY, X or dSum.
+ *   dW    1 x n, ORTHO_F32, overwritten; the rows are added in a fixed order.
+ *   ws    >= ortho_rms_norm_backward_workspace_size(m, n) bytes. */
+ortho_status rms_norm_backward(ortho_mat dY, ortho_mat X, ortho_mat W, float eps,
+                               const ortho_mat* dSum, ortho_mat dX, ortho_mat dW, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace for fp8_matmul with A m x k and B n x k.  Returns 0
+ * for invalid sizes.  256-byte alignment required. */
+size_t ortho_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
+
+/* C = A B^T (+ Add) of 8-bit matrices.
+ *   A, SA  m x k codes, and their scales: m rows of them (1 x 128 blocks) or
+ *          ceil(m / 128) (128 x 128 blocks), ceil(k / 128) columns.
+ *   B, SB  n x k codes, and their scales likewise; SB has SA's dtype.
+ *   C      m x n, ORTHO_F32 or ORTHO_BF16 (rounded to nearest even).
+ *   Add    NULL, or m x n, ORTHO_F32 or ORTHO_BF16, added in fp32 before C is
+ *          rounded (a residual, or a gradient being accumulated).  May be C.
+ *   ws     >= ortho_fp8_matmul_workspace_size(m, n, k) bytes.
+ * Products are accumulated in fp32, in an order that depends on the sizes and
+ * layouts alone.  With an ORTHO_F32 C every product counts in full.  With an
+ * ORTHO_BF16 C the 8-bit matrix instruction is used, which cuts each product
+ * below 2^-13 of the largest of its group of eight neighbours along k (about
+ * 1e-5 of the result, against the 2^-9 of C's rounding).  A NaN code or scale reaches the elements of C that it enters into,
+ * and no others. */
+ortho_status fp8_matmul(ortho_mat A, ortho_mat SA, ortho_mat B, ortho_mat SB, ortho_mat C,
+                        const ortho_mat* Add, void* ws, size_t ws_bytes, void* stream);
 
 /* Static English description of a status code. */
 const char* ortho_status_str(int32_t status);

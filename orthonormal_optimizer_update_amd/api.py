@@ -16,7 +16,8 @@ from typing import Optional, Sequence
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libortho.so")
 
-ORTHO_F32, ORTHO_BF16 = 0, 1
+ORTHO_F32, ORTHO_BF16, ORTHO_E4M3, ORTHO_E8M0 = 0, 1, 2, 3
+FP8_BLOCK = 128
 ORTHO_E_SCRATCH = 9
 NOALLOC_SCRATCH_BYTES = 64 << 20
 DEV_CHOL_SHIFT, DEV_ZERO_COLUMN = 1, 2
@@ -76,6 +77,21 @@ _SIGS = {
     "dion2_step": (ctypes.c_int, [OrthoMat, OrthoMat, OrthoMat, ctypes.c_int32, ctypes.c_int32,
                                   ctypes.POINTER(ctypes.c_float), ctypes.c_float, ctypes.c_float,
                                   ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                  ctypes.c_void_p]),
+    "fp8_quantize": (ctypes.c_int, [OrthoMat, ctypes.c_int32, ctypes.POINTER(OrthoMat),
+                                    ctypes.POINTER(OrthoMat), ctypes.POINTER(OrthoMat),
+                                    ctypes.POINTER(OrthoMat), ctypes.c_void_p]),
+    "rms_norm_fp8": (ctypes.c_int, [OrthoMat, ctypes.POINTER(OrthoMat), OrthoMat, ctypes.c_float,
+                                    ctypes.POINTER(OrthoMat), ctypes.POINTER(OrthoMat), OrthoMat,
+                                    OrthoMat, ctypes.c_void_p]),
+    "ortho_rms_norm_backward_workspace_size": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
+    "rms_norm_backward": (ctypes.c_int, [OrthoMat, OrthoMat, OrthoMat, ctypes.c_float,
+                                         ctypes.POINTER(OrthoMat), OrthoMat, OrthoMat,
+                                         ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "ortho_fp8_matmul_workspace_size": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64,
+                                                          ctypes.c_int64]),
+    "fp8_matmul": (ctypes.c_int, [OrthoMat, OrthoMat, OrthoMat, OrthoMat, OrthoMat,
+                                  ctypes.POINTER(OrthoMat), ctypes.c_void_p, ctypes.c_size_t,
                                   ctypes.c_void_p]),
     "ortho_status_str": (ctypes.c_char_p, [ctypes.c_int32]),
     "ortho_abi_version": (ctypes.c_int32, []),
@@ -308,3 +324,146 @@ def dion2_step(X, G, M, k: int, mu: float, lr: float, scale: float = 1.0, steps:
     st = lib().dion2_step(mat(X), mat(G), mat(M), k, steps, _abc(abc), mu, lr, scale,
                           _ptr(selected), _ptr(ws), ws.numel(), _stream_ptr(X.device))
     _check("dion2_step", st)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit matrices: e4m3 codes with a scale for each block of 128
+# ---------------------------------------------------------------------------
+
+_DTYPES = None
+
+
+def _mats(*tensors):
+    """Descriptors of 2-D tensors on one GPU (None stays None), which may hold
+    8-bit codes and scales."""
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float32: ORTHO_F32, torch.bfloat16: ORTHO_BF16,
+                   torch.float8_e4m3fn: ORTHO_E4M3, torch.float8_e8m0fnu: ORTHO_E8M0}
+    out, device = [], tensors[0].device
+    if device.type != "cuda":
+        raise ValueError(f"expected tensors on a GPU, got {device}")
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if t.device != device:
+            raise ValueError(f"expected every tensor on {device}, got {t.device}")
+        if t.dim() != 2:
+            raise ValueError("expected a 2-D tensor")
+        rows, cols = t.shape
+        ld, step = t.stride()
+        if cols > 1 and step != 1:
+            raise ValueError("expected unit stride along columns")
+        if rows > 1 and ld < cols:
+            raise ValueError("expected rows that do not overlap")
+        dt = _DTYPES.get(t.dtype)
+        if dt is None:
+            raise ValueError(f"unsupported dtype {t.dtype}")
+        out.append(OrthoMat(t.data_ptr(), rows, cols, ld if rows > 1 else cols, dt))
+    return out
+
+
+def _ref(m):
+    return None if m is None else ctypes.byref(m)
+
+
+def _call(fn: str, device, *args):
+    """The library call on `device`'s current stream, with `device` current."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        status = getattr(lib(), fn)(*args, _stream_ptr(device))
+    else:
+        with torch.cuda.device(device):
+            status = getattr(lib(), fn)(*args, _stream_ptr(device))
+    _check(fn, status)
+
+
+def _blocks(n: int) -> int:
+    return -(-n // FP8_BLOCK)
+
+
+def fp8_codes(rows: int, cols: int, device):
+    """Uninitialised e4m3 codes whose rows start at multiples of 16 bytes, the
+    layout that the kernels read and write fastest."""
+    import torch
+    return torch.empty(rows, -(-cols // 16) * 16, dtype=torch.float8_e4m3fn, device=device)[:, :cols]
+
+
+def fp8_scales(rows: int, cols: int, device, block_rows: int = 1, scale_dtype=None):
+    """Uninitialised scales of a rows x cols matrix: one for each block of
+    block_rows x 128, float32 (default) or float8_e8m0fnu."""
+    import torch
+    return torch.empty(-(-rows // block_rows), _blocks(cols), device=device,
+                       dtype=torch.float32 if scale_dtype is None else scale_dtype)
+
+
+def fp8_quantize(X, Q=None, S=None, QT=None, ST=None, block_rows: int = 1, scale_dtype=None,
+                 transposed: bool = False):
+    """X as e4m3 codes and block scales, by rows (Q, S) and transposed (QT, ST);
+    see ``fp8_quantize`` in ortho.h.  Without any output given, Q and S are
+    allocated, and with ``transposed`` QT and ST too.  Returns (Q, S, QT, ST),
+    None for what is not written."""
+    if Q is None and S is None and QT is None and ST is None:
+        m, n = X.shape
+        Q = fp8_codes(m, n, X.device)
+        S = fp8_scales(m, n, X.device, block_rows, scale_dtype)
+        if transposed:
+            QT = fp8_codes(n, m, X.device)
+            ST = fp8_scales(n, m, X.device, block_rows, scale_dtype)
+    x, q, s, qt, st = _mats(X, Q, S, QT, ST)
+    _call("fp8_quantize", X.device, x, block_rows, _ref(q), _ref(s), _ref(qt), _ref(st))
+    return Q, S, QT, ST
+
+
+def rms_norm_fp8(X, W, Q=None, S=None, eps: float = 1e-6, residual=None, sum_out=None, y_out=None,
+                 scale_dtype=None):
+    """RMS norm of X + residual times W as e4m3 codes and scales; see
+    ``rms_norm_fp8`` in ortho.h.  ``sum_out`` receives the sum, ``y_out`` the
+    result before its rounding to 8 bits.  Returns (Q, S)."""
+    if Q is None:
+        Q = fp8_codes(X.size(0), X.size(1), X.device)
+    if S is None:
+        S = fp8_scales(X.size(0), X.size(1), X.device, 1, scale_dtype)
+    x, res, w, total, y, q, s = _mats(X, residual, W, sum_out, y_out, Q, S)
+    _call("rms_norm_fp8", X.device, x, _ref(res), w, eps, _ref(total), _ref(y), q, s)
+    return Q, S
+
+
+def rms_norm_backward_workspace_size(m: int, n: int) -> int:
+    return int(lib().ortho_rms_norm_backward_workspace_size(m, n))
+
+
+def rms_norm_backward(dY, X, W, dX=None, dW=None, eps: float = 1e-6, dsum=None, ws=None):
+    """Gradient of ``rms_norm_fp8`` (see ortho.h): returns (dX, dW), dX with
+    ``dsum`` added when given, dW 1 x n float32."""
+    import torch
+    if dX is None:
+        dX = torch.empty_like(X, memory_format=torch.contiguous_format)
+    if dW is None:
+        dW = torch.empty(1, X.size(1), dtype=torch.float32, device=X.device)
+    if ws is None:
+        ws = workspace(rms_norm_backward_workspace_size(X.size(0), X.size(1)), X.device)
+    dy, x, w, ds, dx, dw = _mats(dY, X, W, dsum, dX, dW)
+    _call("rms_norm_backward", X.device, dy, x, w, eps, _ref(ds), dx, dw, _ptr(ws), ws.numel())
+    return dX, dW
+
+
+def fp8_matmul_workspace_size(m: int, n: int, k: int) -> int:
+    return int(lib().ortho_fp8_matmul_workspace_size(m, n, k))
+
+
+def fp8_matmul(A, SA, B, SB, out=None, add=None, ws=None, out_dtype=None):
+    """A B^T (+ add) of 8-bit matrices (codes A, B; scales SA, SB); see
+    ``fp8_matmul`` in ortho.h.  ``out`` is allocated when None, of ``out_dtype``
+    (default bfloat16).  Returns out."""
+    import torch
+    if out is None:
+        out = torch.empty(A.size(0), B.size(0), device=A.device,
+                          dtype=torch.bfloat16 if out_dtype is None else out_dtype)
+    if ws is None:
+        ws = workspace(fp8_matmul_workspace_size(A.size(0), B.size(0), A.size(1)), A.device)
+    a, sa, b, sb, c, ad = _mats(A, SA, B, SB, out, add)
+    _call("fp8_matmul", A.device, a, sa, b, sb, c, _ref(ad), _ptr(ws), ws.numel())
+    return out

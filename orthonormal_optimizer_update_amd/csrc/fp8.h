@@ -1,0 +1,210 @@
+// 8-bit matrices with a scale for each block of 128: device helpers and the
+// launchers' argument blocks (internal to libortho.so).  gfx950 only.
+//
+// A code is an OCP e4m3 byte (1 sign, 4 exponent, 3 mantissa bits; largest
+// value 448, one NaN, no infinities).  The scales of an R x C matrix hold one
+// value for each block of 1 x 128 or 128 x 128 elements (the last block of a
+// row or column may be shorter), as fp32 or as e8m0 (byte b stands for
+// 2^(b - 127), 255 for NaN).  Element = code * scale.
+#pragma once
+
+#include "common.h"
+
+namespace ortho {
+
+constexpr int kFp8Block = 128;
+constexpr float kFp8Top = 448.f;
+
+// Scales as a kernel sees them: the row of scales that covers matrix row i is
+// i >> shift (shift 0: a row of its own, 7: shared by 128 rows).
+struct ScaleArg {
+  const void* p;
+  int64_t ld;
+  int shift;
+};
+
+struct QuantArgs {
+  const void* x;
+  int64_t ldx;
+  int vec;                  // X's rows start at multiples of 16 bytes
+  uint8_t *q, *qt;          // codes by rows (m x n) and transposed (n x m); either may be null
+  int64_t ldq, ldqt;
+  int qvec, qtvec;          // rows of 16-byte multiples
+  void *s, *st;
+  int64_t lds, ldst;
+  int m, n;
+};
+hipError_t launch_fp8_quantize(const QuantArgs& a, bool bf, bool e8m0, bool tiles, hipStream_t s);
+
+struct NormArgs {
+  const void *x, *res, *w;
+  int64_t ldx, ldres;
+  void *sum, *y;
+  int64_t ldsum, ldy;
+  uint8_t* q;
+  int64_t ldq;
+  void* s;
+  int64_t lds;
+  float eps;
+  int m, n;
+  int vec;                  // x, res, sum, y rows of 16-byte multiples
+  int qvec;                 // q rows of 8-byte multiples
+  int w_bf;                 // W is bf16
+};
+hipError_t launch_rms_norm_fp8(const NormArgs& a, bool bf, bool e8m0, hipStream_t s);
+
+struct NormGradArgs {
+  const void *dy, *x, *w, *dsum;
+  int64_t lddy, ldx, lddsum;
+  void* dx;
+  int64_t lddx;
+  float* dw;
+  float* part;              // groups x n partial sums of dw
+  float eps;
+  int m, n, groups;
+  int vec;
+  int w_bf;
+};
+hipError_t launch_rms_norm_backward(const NormGradArgs& a, bool bf, hipStream_t s);
+
+struct Fp8GemmArgs {
+  const uint8_t *a, *b;     // M x K and N x K codes
+  int64_t lda, ldb;
+  ScaleArg sa, sb;
+  void* c;
+  const void* add;
+  int64_t ldc, ldadd;
+  int add_bf;
+  int cvec;                 // C (and Add) take four columns per access
+  int M, N, K;
+};
+hipError_t launch_fp8_matmul(const Fp8GemmArgs& a, bool c_bf, bool e8m0, hipStream_t s);
+
+// Scale of a block whose largest finite magnitude is `top`, and the factor
+// that takes the block's elements to codes.  fp32: top / 448, not below 2^-126
+// so that the factor 1 / scale is finite; the factor is rounded once.  e8m0:
+// the smallest power of two with top <= 448 * scale, so both are exact.  A
+// block of zeros (or without a finite element) has scale 1.
+template <bool kE8m0>
+__device__ __forceinline__ void block_scale(float top, float& scale, float& factor) {
+  if constexpr (kE8m0) {
+    // top = f 2^e with f in [0.5, 1): 448 = 0.875 * 2^9
+    int e;
+    const float f = __builtin_frexpf(top, &e);
+    e = e - 9 + (f > 0.875f ? 1 : 0);
+    e = e < -126 ? -126 : e;
+    e = top == 0.f ? 0 : e;
+    scale = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+    factor = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  } else {
+    float s = top / kFp8Top;
+    s = s < 0x1p-126f ? 0x1p-126f : s;
+    scale = top == 0.f ? 1.f : s;
+    factor = 1.f / scale;
+  }
+}
+
+template <bool kE8m0>
+__device__ __forceinline__ void store_scale(void* p, int64_t idx, float scale) {
+  if constexpr (kE8m0)
+    static_cast<uint8_t*>(p)[idx] = static_cast<uint8_t>(__float_as_uint(scale) >> 23);
+  else
+    static_cast<float*>(p)[idx] = scale;
+}
+
+template <bool kE8m0>
+__device__ __forceinline__ float load_scale(const void* p, int64_t idx) {
+  if constexpr (kE8m0) {
+    const uint32_t b = static_cast<const uint8_t*>(p)[idx];
+    return __uint_as_float(b == 0 ? 0x00400000u : (b == 255 ? 0x7fc00000u : b << 23));
+  } else {
+    return static_cast<const float*>(p)[idx];
+  }
+}
+
+// |x| if finite, else 0: what a block's scale is taken from.
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = __builtin_fabsf(x);
+  return a < __builtin_inff() ? a : 0.f;
+}
+
+// Four fp32 values as four e4m3 codes, round to nearest even; infinities and
+// NaN give the NaN code.
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  int u = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, u, true));
+}
+
+// Eight consecutive elements from column c of a row of `limit` columns.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int c, int limit, bool vec, float (&v)[8]);
+template <>
+__device__ __forceinline__ void load8<uint16_t>(const uint16_t* row, int c, int limit, bool vec,
+                                                float (&v)[8]) {
+  if (vec && c + 8 <= limit) {
+    const uint4 u = *reinterpret_cast<const uint4*>(row + c);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = c + j < limit ? bf16_bits_to_f32(row[c + j]) : 0.f;
+}
+template <>
+__device__ __forceinline__ void load8<float>(const float* row, int c, int limit, bool vec,
+                                             float (&v)[8]) {
+  if (vec && c + 8 <= limit) {
+    const float4 u = *reinterpret_cast<const float4*>(row + c);
+    const float4 w = *reinterpret_cast<const float4*>(row + c + 4);
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+    v[4] = w.x; v[5] = w.y; v[6] = w.z; v[7] = w.w;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = c + j < limit ? row[c + j] : 0.f;
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* row, int c, int limit, bool vec, const float (&v)[8]);
+template <>
+__device__ __forceinline__ void store8<uint16_t>(uint16_t* row, int c, int limit, bool vec,
+                                                 const float (&v)[8]) {
+  if (vec && c + 8 <= limit) {
+    const uint2 lo = pack_bf16x4(floatx4{v[0], v[1], v[2], v[3]});
+    const uint2 hi = pack_bf16x4(floatx4{v[4], v[5], v[6], v[7]});
+    *reinterpret_cast<uint4*>(row + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j < limit) row[c + j] = to_bf16_bits(v[j]);
+}
+template <>
+__device__ __forceinline__ void store8<float>(float* row, int c, int limit, bool vec,
+                                              const float (&v)[8]) {
+  if (vec && c + 8 <= limit) {
+    *reinterpret_cast<float4*>(row + c) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(row + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j < limit) row[c + j] = v[j];
+}
+
+// Eight codes to column c of a row of `limit` columns.
+__device__ __forceinline__ void store_codes8(uint8_t* row, int c, int limit, bool vec, uint2 u) {
+  if (vec && c + 8 <= limit) {
+    *reinterpret_cast<uint2*>(row + c) = u;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j < limit) row[c + j] = static_cast<uint8_t>((j < 4 ? u.x : u.y) >> (8 * (j & 3)));
+}
+
+}  // namespace ortho

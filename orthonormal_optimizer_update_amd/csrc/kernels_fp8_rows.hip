@@ -1,0 +1,352 @@
+// Conversion to 8-bit codes with block scales, and the RMS norm around it: the
+// residual's addition, the 8-bit output and the gradient.  All are bound by
+// HBM traffic: each element is read once, held in registers, and written once
+// per output.
+#include <type_traits>
+
+#include "fp8.h"
+
+namespace ortho {
+
+namespace {
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Largest value over the 16 lanes that hold one block of 128 (8 per lane).
+__device__ __forceinline__ float max16(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  return v;
+}
+
+__device__ __forceinline__ float top8(const float (&v)[8]) {
+  float t = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) t = fmaxf(t, finite_abs(v[j]));
+  return t;
+}
+
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float f) {
+  return make_uint2(pack_e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f),
+                    pack_e4m3x4(v[4] * f, v[5] * f, v[6] * f, v[7] * f));
+}
+
+// Codes by rows with a scale per 1 x 128 block: 16 lanes per block.
+template <typename T, bool kE8m0>
+__global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
+  const int nb = (a.n + kFp8Block - 1) / kFp8Block;
+  const int64_t blk = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  if (blk >= (int64_t)a.m * nb) return;
+  const int row = static_cast<int>(blk / nb), b = static_cast<int>(blk % nb);
+  const int c = b * kFp8Block + (threadIdx.x & 15) * 8;
+  float v[8];
+  load8<T>(static_cast<const T*>(a.x) + row * a.ldx, c, a.n, a.vec, v);
+  float scale, f;
+  block_scale<kE8m0>(max16(top8(v)), scale, f);
+  store_codes8(a.q + row * a.ldq, c, a.n, a.qvec, codes8(v, f));
+  if ((threadIdx.x & 15) == 0) store_scale<kE8m0>(a.s, row * a.lds + b, scale);
+}
+
+// A 128 x 128 tile per workgroup, 8 x 8 elements per thread (columns of 16
+// threads, rows of 16 groups): codes by rows, transposed, or both, from one
+// read.  kTiles: one scale for the tile; otherwise one per row for the codes
+// by rows and one per column for the transposed ones.
+template <typename T, bool kE8m0, bool kTiles>
+__global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
+  constexpr int kPitch = 128 + 16;   // bytes per LDS row of transposed codes
+  __shared__ __attribute__((aligned(16))) uint8_t tile[128 * kPitch];
+  __shared__ float red[4][128];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int nbn = (a.n + 127) / 128;
+  const int tn = blockIdx.x % nbn, tm = blockIdx.x / nbn;
+  const int cl = (t & 15) * 8, rl = (t >> 4) * 8;
+  const int c = tn * 128 + cl, r0 = tm * 128 + rl;
+  float v[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (r0 + i < a.m) {
+      load8<T>(static_cast<const T*>(a.x) + (r0 + i) * a.ldx, c, a.n, a.vec, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    }
+  }
+  float fr[8], fc[8];   // factors by row and by column
+  if constexpr (kTiles) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, top8(v[i]));
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    if (lane == 0) red[0][wave] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    float scale, f;
+    block_scale<kE8m0>(top, scale, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) fr[i] = fc[i] = f;
+    if (t == 0) {
+      if (a.q) store_scale<kE8m0>(a.s, tm * a.lds + tn, scale);
+      if (a.qt) store_scale<kE8m0>(a.st, tn * a.ldst + tm, scale);
+    }
+  } else {
+    if (a.q) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float scale;
+        block_scale<kE8m0>(max16(top8(v[i])), scale, fr[i]);
+        if ((t & 15) == 0 && r0 + i < a.m) store_scale<kE8m0>(a.s, (r0 + i) * a.lds + tn, scale);
+      }
+    }
+    if (a.qt) {
+      float top[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        top[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top[j] = fmaxf(top[j], finite_abs(v[i][j]));
+        top[j] = fmaxf(top[j], __shfl_xor(top[j], 16, 64));
+        top[j] = fmaxf(top[j], __shfl_xor(top[j], 32, 64));
+        if (lane < 16) red[wave][cl + j] = top[j];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float scale;
+        block_scale<kE8m0>(fmaxf(fmaxf(red[0][cl + j], red[1][cl + j]),
+                                 fmaxf(red[2][cl + j], red[3][cl + j])), scale, fc[j]);
+        if (t < 16 && c + j < a.n) store_scale<kE8m0>(a.st, (c + j) * a.ldst + tm, scale);
+      }
+    }
+  }
+  if (a.q) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (r0 + i < a.m) store_codes8(a.q + (r0 + i) * a.ldq, c, a.n, a.qvec, codes8(v[i], fr[i]));
+  }
+  if (a.qt) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float col[8] = {v[0][j], v[1][j], v[2][j], v[3][j], v[4][j], v[5][j], v[6][j], v[7][j]};
+      *reinterpret_cast<uint2*>(tile + (cl + j) * kPitch + rl) = codes8(col, fc[j]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int cc = (t >> 3) + 32 * i, k = (t & 7) * 16;   // column of X, offset along its rows
+      if (tn * 128 + cc >= a.n) continue;
+      const uint4 u = *reinterpret_cast<const uint4*>(tile + cc * kPitch + k);
+      uint8_t* dst = a.qt + (tn * 128 + cc) * a.ldqt;
+      const int m0 = tm * 128 + k;
+      if (a.qtvec && m0 + 16 <= a.m) {
+        *reinterpret_cast<uint4*>(dst + m0) = u;
+      } else {
+        store_codes8(dst, m0, a.m, false, make_uint2(u.x, u.y));
+        store_codes8(dst, m0 + 8, a.m, false, make_uint2(u.z, u.w));
+      }
+    }
+  }
+}
+
+// Sum over the workgroup in a fixed order; every thread gets the total.
+template <int kThreads>
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  if constexpr (kThreads == 64) return v;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float total = 0.f;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) total += red[w];
+  return total;
+}
+
+__device__ __forceinline__ void load_w8(const void* w, int w_bf, int c, int n, float (&v)[8]) {
+  if (w_bf) load8<uint16_t>(static_cast<const uint16_t*>(w), c, n, false, v);
+  else load8<float>(static_cast<const float*>(w), c, n, false, v);
+}
+
+// One row per workgroup, 8 kC elements per thread.
+//   r = round(x + res), t = 1 / sqrt(mean r^2 + eps), y = r t w
+// The sum is rounded to its storage type first and the rounded one is
+// normalised, so that the gradient, which sees only the stored sum, is that of
+// what was computed.
+template <typename T, bool kE8m0, int kThreads, int kC>
+__global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
+  __shared__ float red[kThreads / 64];
+  const int64_t row = blockIdx.x;
+  const int t = threadIdx.x;
+  float v[kC][8];
+  float sq = 0.f;
+#pragma unroll
+  for (int i = 0; i < kC; ++i) {
+    const int c = (i * kThreads + t) * 8;
+    load8<T>(static_cast<const T*>(a.x) + row * a.ldx, c, a.n, a.vec, v[i]);
+    if (a.res) {
+      float r[8];
+      load8<T>(static_cast<const T*>(a.res) + row * a.ldres, c, a.n, a.vec, r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[i][j] += r[j];
+        if constexpr (sizeof(T) == 2) v[i][j] = static_cast<float>(to_bf16(v[i][j]));
+      }
+    }
+    if (a.sum) store8<T>(static_cast<T*>(a.sum) + row * a.ldsum, c, a.n, a.vec, v[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sq += v[i][j] * v[i][j];
+  }
+  const float rs = 1.f / __builtin_sqrtf(block_sum<kThreads>(sq, red) / a.n + a.eps);
+#pragma unroll
+  for (int i = 0; i < kC; ++i) {
+    const int c = (i * kThreads + t) * 8;
+    if (c - (t & 15) * 8 >= a.n) continue;   // whole block past the row's end
+    float w[8];
+    load_w8(a.w, a.w_bf, c, a.n, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rs * w[j];
+    if (a.y) store8<T>(static_cast<T*>(a.y) + row * a.ldy, c, a.n, a.vec, v[i]);
+    float scale, f;
+    block_scale<kE8m0>(max16(top8(v[i])), scale, f);
+    store_codes8(a.q + row * a.ldq, c, a.n, a.qvec, codes8(v[i], f));
+    if ((t & 15) == 0) store_scale<kE8m0>(a.s, row * a.lds + c / kFp8Block, scale);
+  }
+}
+
+// Gradient of the norm.  With h = dy w, u = x t:
+//   dx = t (h - u mean(h u)) (+ dsum),  dw = sum over rows of dy u
+// Workgroup g takes the rows g, g + groups, ... and keeps its part of dw in
+// registers; the parts are added in a fixed order by a second launch.
+template <typename T, int kThreads, int kC>
+__global__ __launch_bounds__(kThreads) void rms_norm_grad_kernel(NormGradArgs a) {
+  __shared__ float red[2][kThreads / 64];
+  const int t = threadIdx.x;
+  float dw[kC][8];
+#pragma unroll
+  for (int i = 0; i < kC; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+  for (int64_t row = blockIdx.x; row < a.m; row += a.groups) {
+    float x[kC][8], g[kC][8];
+    float sq = 0.f, dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      const int c = (i * kThreads + t) * 8;
+      float w[8];
+      load8<T>(static_cast<const T*>(a.x) + row * a.ldx, c, a.n, a.vec, x[i]);
+      load8<T>(static_cast<const T*>(a.dy) + row * a.lddy, c, a.n, a.vec, g[i]);
+      load_w8(a.w, a.w_bf, c, a.n, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sq += x[i][j] * x[i][j];
+        dot += x[i][j] * (g[i][j] * w[j]);
+      }
+    }
+    sq = block_sum<kThreads>(sq, red[0]);
+    dot = block_sum<kThreads>(dot, red[1]);
+    const float rs = 1.f / __builtin_sqrtf(sq / a.n + a.eps);
+    const float mean = dot * rs / a.n;   // mean(h u)
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      const int c = (i * kThreads + t) * 8;
+      if (c >= a.n) continue;
+      float w[8], d[8], o[8];
+      load_w8(a.w, a.w_bf, c, a.n, w);
+      if (a.dsum) load8<T>(static_cast<const T*>(a.dsum) + row * a.lddsum, c, a.n, a.vec, d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float u = x[i][j] * rs;
+        dw[i][j] += g[i][j] * u;
+        o[j] = rs * (g[i][j] * w[j] - u * mean);
+        if (a.dsum) o[j] += d[j];
+      }
+      store8<T>(static_cast<T*>(a.dx) + row * a.lddx, c, a.n, a.vec, o);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kC; ++i) {
+    const int c = (i * kThreads + t) * 8;
+    store8<float>(a.part + (int64_t)blockIdx.x * a.n, c, a.n, false, dw[i]);
+  }
+}
+
+__global__ __launch_bounds__(256) void rms_norm_dw_kernel(NormGradArgs a) {
+  __shared__ float red[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  float sum = 0.f;
+  if (c < a.n)
+    for (int g = wave; g < a.groups; g += 4) sum += a.part[(int64_t)g * a.n + c];
+  red[wave][lane] = sum;
+  __syncthreads();
+  if (wave == 0 && c < a.n)
+    a.dw[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+}
+
+// f(threads, elements per thread / 8) at the smallest workgroup that holds a
+// row of n elements; n <= 65536.
+template <class F>
+hipError_t by_width(int n, F f) {
+  if (n <= 512) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+  else if (n <= 1024) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+  else if (n <= 2048) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+  else if (n <= 4096) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+  else if (n <= 8192) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+  else if (n <= 16384) f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+  else if (n <= 32768) f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+  else if (n <= 65536) f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 8>{});
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+template <typename T, bool kE8m0>
+hipError_t quantize(const QuantArgs& a, bool tiles, hipStream_t s) {
+  if (!tiles && a.qt == nullptr) {
+    const int64_t blocks = cdiv((int64_t)a.m * cdiv(a.n, kFp8Block), 16);
+    hipLaunchKernelGGL((quant_rows_kernel<T, kE8m0>), dim3(static_cast<uint32_t>(blocks)), dim3(256),
+                       0, s, a);
+    return hipGetLastError();
+  }
+  const dim3 grid(static_cast<uint32_t>(cdiv(a.n, 128) * cdiv(a.m, 128)));
+  if (tiles) hipLaunchKernelGGL((quant_tile_kernel<T, kE8m0, true>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((quant_tile_kernel<T, kE8m0, false>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename T, bool kE8m0>
+hipError_t norm(const NormArgs& a, hipStream_t s) {
+  return by_width(a.n, [&](auto th, auto c) {
+    hipLaunchKernelGGL((rms_norm_fp8_kernel<T, kE8m0, decltype(th)::value, decltype(c)::value>),
+                       dim3(a.m), dim3(decltype(th)::value), 0, s, a);
+  });
+}
+
+template <typename T>
+hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
+  hipError_t e = by_width(a.n, [&](auto th, auto c) {
+    hipLaunchKernelGGL((rms_norm_grad_kernel<T, decltype(th)::value, decltype(c)::value>),
+                       dim3(a.groups), dim3(decltype(th)::value), 0, s, a);
+  });
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(rms_norm_dw_kernel, dim3(static_cast<uint32_t>(cdiv(a.n, 64))), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp8_quantize(const QuantArgs& a, bool bf, bool e8m0, bool tiles, hipStream_t s) {
+  if (bf) return e8m0 ? quantize<uint16_t, true>(a, tiles, s) : quantize<uint16_t, false>(a, tiles, s);
+  return e8m0 ? quantize<float, true>(a, tiles, s) : quantize<float, false>(a, tiles, s);
+}
+
+hipError_t launch_rms_norm_fp8(const NormArgs& a, bool bf, bool e8m0, hipStream_t s) {
+  if (bf) return e8m0 ? norm<uint16_t, true>(a, s) : norm<uint16_t, false>(a, s);
+  return e8m0 ? norm<float, true>(a, s) : norm<float, false>(a, s);
+}
+
+hipError_t launch_rms_norm_backward(const NormGradArgs& a, bool bf, hipStream_t s) {
+  return bf ? norm_grad<uint16_t>(a, s) : norm_grad<float>(a, s);
+}
+
+}  // namespace ortho

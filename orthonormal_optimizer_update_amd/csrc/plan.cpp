@@ -435,4 +435,137 @@ ortho_status validate_muon(int32_t batch, const ortho_mat* X, const ortho_mat* G
   return ORTHO_OK;
 }
 
+namespace {
+
+// A matrix of one of the dtypes in `allowed` (a mask of 1 << dtype).
+ortho_status check_any(const ortho_mat& a, unsigned allowed) {
+  if (a.data == nullptr) return ORTHO_E_NULL;
+  if (a.rows < 1 || a.cols < 1 || a.rows > kMaxDim || a.cols > kMaxDim) return ORTHO_E_SHAPE;
+  if (a.ld < a.cols || a.ld > (int64_t{1} << 40)) return ORTHO_E_LAYOUT;
+  if (a.dtype < 0 || a.dtype > 31 || !(allowed >> a.dtype & 1u)) return ORTHO_E_DTYPE;
+  return ORTHO_OK;
+}
+
+constexpr unsigned kReal = 1u << ORTHO_F32 | 1u << ORTHO_BF16;
+constexpr unsigned kCodes = 1u << ORTHO_E4M3;
+constexpr unsigned kScales = 1u << ORTHO_F32 | 1u << ORTHO_E8M0;
+
+bool shape_is(const ortho_mat& a, int64_t rows, int64_t cols) {
+  return a.rows == rows && a.cols == cols;
+}
+
+// Optional matrix of a required dtype and shape.
+ortho_status check_like(const ortho_mat* a, int32_t dtype, int64_t rows, int64_t cols) {
+  if (a == nullptr) return ORTHO_OK;
+  const ortho_status st = check_any(*a, 1u << dtype);
+  if (st != ORTHO_OK) return st;
+  return shape_is(*a, rows, cols) ? ORTHO_OK : ORTHO_E_SHAPE;
+}
+
+// Codes of a rows x cols matrix and the scales of its br x 128 blocks.
+ortho_status check_codes(const ortho_mat& q, const ortho_mat& s, int64_t rows, int64_t cols,
+                         int64_t br) {
+  ortho_status st;
+  if ((st = check_any(q, kCodes)) != ORTHO_OK) return st;
+  if ((st = check_any(s, kScales)) != ORTHO_OK) return st;
+  if (!shape_is(q, rows, cols)) return ORTHO_E_SHAPE;
+  return shape_is(s, cdiv(rows, br), cdiv(cols, kFp8BlockSize)) ? ORTHO_OK : ORTHO_E_SHAPE;
+}
+
+ortho_status check_norm_weight(const ortho_mat& W, const ortho_mat& X, float eps) {
+  const ortho_status st = check_any(W, kReal);
+  if (st != ORTHO_OK) return st;
+  if (W.dtype != ORTHO_F32 && W.dtype != X.dtype) return ORTHO_E_DTYPE;
+  if (!shape_is(W, 1, X.cols) || X.cols > kNormMaxCols) return ORTHO_E_SHAPE;
+  return finite(eps) && eps >= 0.f ? ORTHO_OK : ORTHO_E_PARAM;
+}
+
+ortho_status check_ws(const void* ws, size_t have, size_t need) {
+  if (ws == nullptr || have < need) return ORTHO_E_WORKSPACE;
+  return reinterpret_cast<uintptr_t>(ws) % kWsAlign != 0 ? ORTHO_E_WORKSPACE : ORTHO_OK;
+}
+
+// Workgroups of a launch are counted in 31 bits.
+constexpr int64_t kMaxGrid = (int64_t{1} << 31) - 1;
+
+}  // namespace
+
+bool plan_fp8_matmul(int64_t m, int64_t n, int64_t k, Fp8MatmulPlan* p) {
+  if (m < 1 || n < 1 || k < 1 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return false;
+  if (cdiv(m, 128) * cdiv(n, 128) > kMaxGrid) return false;
+  p->total_bytes = kWsAlign;
+  return true;
+}
+
+bool plan_norm_grad(int64_t m, int64_t n, NormGradPlan* p) {
+  if (m < 1 || n < 1 || m > kMaxDim || n > kNormMaxCols) return false;
+  p->groups = static_cast<int>(m < 512 ? m : 512);
+  p->total_bytes = align_up(static_cast<size_t>(p->groups) * static_cast<size_t>(n) * 4);
+  return true;
+}
+
+ortho_status validate_fp8_quantize(const ortho_mat& X, int32_t block_rows, const ortho_mat* Q,
+                                   const ortho_mat* S, const ortho_mat* QT, const ortho_mat* ST) {
+  if (block_rows != 1 && block_rows != kFp8BlockSize) return ORTHO_E_PARAM;
+  ortho_status st;
+  if ((st = check_any(X, kReal)) != ORTHO_OK) return st;
+  if ((Q == nullptr) != (S == nullptr) || (QT == nullptr) != (ST == nullptr)) return ORTHO_E_NULL;
+  if (Q == nullptr && QT == nullptr) return ORTHO_E_NULL;
+  if (Q && (st = check_codes(*Q, *S, X.rows, X.cols, block_rows)) != ORTHO_OK) return st;
+  if (QT && (st = check_codes(*QT, *ST, X.cols, X.rows, block_rows)) != ORTHO_OK) return st;
+  if (S && ST && S->dtype != ST->dtype) return ORTHO_E_DTYPE;
+  if (X.rows * cdiv(X.cols, kFp8BlockSize) > kMaxGrid) return ORTHO_E_SHAPE;
+  return ORTHO_OK;
+}
+
+ortho_status validate_rms_norm_fp8(const ortho_mat& X, const ortho_mat* Res, const ortho_mat& W,
+                                   float eps, const ortho_mat* Sum, const ortho_mat* Y,
+                                   const ortho_mat& Q, const ortho_mat& S) {
+  ortho_status st;
+  if ((st = check_any(X, kReal)) != ORTHO_OK) return st;
+  if ((st = check_norm_weight(W, X, eps)) != ORTHO_OK) return st;
+  for (const ortho_mat* t : {Res, Sum, Y})
+    if ((st = check_like(t, X.dtype, X.rows, X.cols)) != ORTHO_OK) return st;
+  return check_codes(Q, S, X.rows, X.cols, 1);
+}
+
+ortho_status validate_rms_norm_backward(const ortho_mat& dY, const ortho_mat& X, const ortho_mat& W,
+                                        float eps, const ortho_mat* dSum, const ortho_mat& dX,
+                                        const ortho_mat& dW, const void* ws, size_t ws_bytes) {
+  ortho_status st;
+  if ((st = check_any(X, kReal)) != ORTHO_OK) return st;
+  if ((st = check_norm_weight(W, X, eps)) != ORTHO_OK) return st;
+  for (const ortho_mat* t : {&dY, dSum, &dX})
+    if ((st = check_like(t, X.dtype, X.rows, X.cols)) != ORTHO_OK) return st;
+  if ((st = check_like(&dW, ORTHO_F32, 1, X.cols)) != ORTHO_OK) return st;
+  NormGradPlan plan;
+  if (!plan_norm_grad(X.rows, X.cols, &plan)) return ORTHO_E_SHAPE;
+  return check_ws(ws, ws_bytes, plan.total_bytes);
+}
+
+ortho_status validate_fp8_matmul(const ortho_mat& A, const ortho_mat& SA, const ortho_mat& B,
+                                 const ortho_mat& SB, const ortho_mat& C, const ortho_mat* Add,
+                                 const void* ws, size_t ws_bytes) {
+  ortho_status st;
+  if ((st = check_any(A, kCodes)) != ORTHO_OK) return st;
+  if ((st = check_any(B, kCodes)) != ORTHO_OK) return st;
+  if ((st = check_any(C, kReal)) != ORTHO_OK) return st;
+  if (B.cols != A.cols || !shape_is(C, A.rows, B.rows)) return ORTHO_E_SHAPE;
+  // one row of scales per matrix row, or one for 128 of them
+  if ((st = check_codes(A, SA, A.rows, A.cols, SA.rows == A.rows ? 1 : kFp8BlockSize)) != ORTHO_OK)
+    return st;
+  if ((st = check_codes(B, SB, B.rows, B.cols, SB.rows == B.rows ? 1 : kFp8BlockSize)) != ORTHO_OK)
+    return st;
+  if (SA.dtype != SB.dtype) return ORTHO_E_DTYPE;
+  if (Add) {
+    if ((st = check_any(*Add, kReal)) != ORTHO_OK) return st;
+    if (!shape_is(*Add, C.rows, C.cols)) return ORTHO_E_SHAPE;
+    // in place only where each element is read by the thread that writes it
+    if (Add->data == C.data && (Add->dtype != C.dtype || Add->ld != C.ld)) return ORTHO_E_LAYOUT;
+  }
+  Fp8MatmulPlan plan;
+  if (!plan_fp8_matmul(A.rows, B.rows, A.cols, &plan)) return ORTHO_E_SHAPE;
+  return check_ws(ws, ws_bytes, plan.total_bytes);
+}
+
 }  // namespace ortho

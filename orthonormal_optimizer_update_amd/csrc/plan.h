@@ -153,4 +153,33 @@ ortho_status validate_muon(int32_t batch, const ortho_mat* X, const ortho_mat* G
                            int32_t steps, const float* abc, float mu, float lr, float scale,
                            const void* ws, size_t ws_bytes, bool row_norm = false);
 
+// 8-bit operators (fp8_quantize, rms_norm_fp8, rms_norm_backward, fp8_matmul).
+constexpr int64_t kFp8BlockSize = 128;
+// Longest row of the norms: it stays in one workgroup's registers.
+constexpr int64_t kNormMaxCols = 65536;
+
+struct Fp8MatmulPlan {
+  size_t total_bytes;
+};
+bool plan_fp8_matmul(int64_t m, int64_t n, int64_t k, Fp8MatmulPlan* out);
+
+// dw partial sums: one row of n floats per workgroup of the norm's gradient.
+struct NormGradPlan {
+  int groups;
+  size_t total_bytes;
+};
+bool plan_norm_grad(int64_t m, int64_t n, NormGradPlan* out);
+
+ortho_status validate_fp8_quantize(const ortho_mat& X, int32_t block_rows, const ortho_mat* Q,
+                                   const ortho_mat* S, const ortho_mat* QT, const ortho_mat* ST);
+ortho_status validate_rms_norm_fp8(const ortho_mat& X, const ortho_mat* Res, const ortho_mat& W,
+                                   float eps, const ortho_mat* Sum, const ortho_mat* Y,
+                                   const ortho_mat& Q, const ortho_mat& S);
+ortho_status validate_rms_norm_backward(const ortho_mat& dY, const ortho_mat& X, const ortho_mat& W,
+                                        float eps, const ortho_mat* dSum, const ortho_mat& dX,
+                                        const ortho_mat& dW, const void* ws, size_t ws_bytes);
+ortho_status validate_fp8_matmul(const ortho_mat& A, const ortho_mat& SA, const ortho_mat& B,
+                                 const ortho_mat& SB, const ortho_mat& C, const ortho_mat* Add,
+                                 const void* ws, size_t ws_bytes);
+
 }  // namespace ortho

@@ -1,0 +1,493 @@
+"""The 8-bit operators through the public binding against their definitions in
+64 bits (fp8_ref.py).
+
+Tolerances count roundings: u = 2^-24 is half a step of fp32 relative to the
+value, 2^-8 of bf16, 2^-4 of e4m3."""
+
+import pytest
+import torch
+
+import fp8_ref as ref
+from orthonormal_optimizer_update_amd import api
+from parity_util import note
+
+pytestmark = pytest.mark.gpu
+
+U32, UBF = 2.0 ** -24, 2.0 ** -8
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+SCALES = {"f32": torch.float32, "e8m0": torch.float8_e8m0fnu}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    api.lib()
+    torch.cuda.set_device(0)
+
+
+def half(t):
+    return UBF if t == torch.bfloat16 else U32
+
+
+def normal(seed, rows, cols, dtype="f32", std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(rows, cols, generator=g) * std).to(TYPES[dtype])
+
+
+def padded(t, extra=0, offset=0):
+    """t on the GPU inside a larger buffer: rows `extra` elements apart, the
+    first element `offset` elements in; returns (view, buffer)."""
+    rows, cols = t.shape
+    buf = torch.zeros(rows * (cols + extra) + offset + extra, dtype=t.dtype).view(torch.uint8)
+    buf.fill_(0x7f)    # NaN codes, NaN-like numbers: what is out of range must not count
+    buf = buf.view(t.dtype).to("cuda")
+    view = buf[offset:offset + rows * (cols + extra)].view(rows, cols + extra)[:, :cols]
+    if t.element_size() == 1:
+        view.view(torch.uint8).copy_(t.cuda().view(torch.uint8))
+    else:
+        view.copy_(t)
+    return view, buf
+
+
+def untouched(view, buf):
+    """Whether everything of buf outside the view still holds the fill."""
+    flat = buf.view(torch.uint8).clone()
+    esz = view.element_size()
+    start = (view.data_ptr() - buf.data_ptr())
+    for r in range(view.size(0)):
+        b = start + r * view.stride(0) * esz
+        flat[b:b + view.size(1) * esz] = 0x7f
+    return bool((flat == 0x7f).all())
+
+
+def check_codes(x, q, s, block_rows):
+    """q, s against x's definition (x: host tensor)."""
+    x = x.double()
+    m, n = x.shape
+    top = ref.block_tops(x, block_rows)
+    sv = ref.scale_values(s)
+    if s.dtype == torch.float32:
+        # a / 448 rounded once
+        want = ref.f32_scale(top)
+        assert torch.all((sv - want).abs() <= U32 * want)
+    else:
+        assert torch.equal(sv, ref.e8m0_scale(top))
+    qv = ref.e4m3_values(q)
+    ok = torch.isfinite(x)
+    assert torch.equal(torch.isnan(qv), ~ok)
+    v = torch.where(ok, x, torch.zeros_like(x)) / ref.expand(sv, m, n, block_rows)
+    qv = torch.where(ok, qv, torch.zeros_like(qv))
+    if s.dtype == torch.float32:
+        # half a step of e4m3, around the value moved by two fp32 roundings
+        # (1 / s and the product)
+        slack = 2.01 * U32 * v.abs()
+        assert torch.all((qv - v).abs() <= torch.maximum(ref.half_step(v), ref.half_step(qv)) + slack)
+    else:
+        assert torch.equal(qv, ref.nearest_e4m3(v))
+
+
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n", [(1, 1), (1, 128), (3, 129), (128, 128), (129, 257), (200, 1000),
+                                 (384, 640), (5, 4096), (1031, 72)])
+def test_quantize(m, n, dtype, scale):
+    x = normal(m * 7 + n, m, n, dtype, 0.02)
+    for br in (1, 128):
+        note(f"fp8_quantize {m}x{n} {dtype} {scale} block_rows={br}")
+        Q, S, QT, ST = api.fp8_quantize(x.cuda(), block_rows=br, scale_dtype=SCALES[scale],
+                                        transposed=True)
+        torch.cuda.synchronize()
+        check_codes(x, Q, S, br)
+        check_codes(x.t().contiguous(), QT, ST, br)
+        # one orientation alone gives the same
+        Q1, S1, none, none2 = api.fp8_quantize(x.cuda(), block_rows=br, scale_dtype=SCALES[scale])
+        assert none is None and none2 is None
+        qt = api.fp8_codes(n, m, "cuda")
+        st = api.fp8_scales(n, m, "cuda", br, SCALES[scale])
+        api.fp8_quantize(x.cuda(), QT=qt, ST=st, block_rows=br)
+        torch.cuda.synchronize()
+        for a, b in ((Q, Q1), (S, S1), (QT, qt), (ST, st)):
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("m,n,extra,offset", [(130, 200, 8, 8), (130, 200, 3, 1), (65, 128, 16, 0),
+                                              (17, 300, 1, 5)])
+def test_quantize_strides(m, n, extra, offset):
+    """Rows at any element, outputs at any byte, nothing written outside."""
+    x = normal(3, m, n, "bf16")
+    X, _ = padded(x, extra, offset)
+    for br in (1, 128):
+        outs = []
+        for rows, cols in ((m, n), (n, m)):
+            outs.append(padded(torch.zeros(rows, cols).to(torch.float8_e4m3fn), extra, offset))
+            outs.append(padded(torch.zeros(ref.cdiv(rows, br), ref.cdiv(cols, 128)), extra, offset))
+        note(f"fp8_quantize strided {m}x{n} +{extra} @{offset} block_rows={br}")
+        api.fp8_quantize(X, *[v for v, _ in outs], block_rows=br)
+        torch.cuda.synchronize()
+        check_codes(x, outs[0][0], outs[1][0], br)
+        check_codes(x.t().contiguous(), outs[2][0], outs[3][0], br)
+        assert all(untouched(v, b) for v, b in outs)
+
+
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("br", [1, 128])
+def test_quantize_special_values(br, scale):
+    """Zero blocks, infinities, NaN, subnormals, the largest values, and tops on
+    either side of 448 times a power of two."""
+    x = normal(5, 256, 640)
+    x[0] = 0.0
+    x[1, :128] = 0.0
+    x[2, 5], x[2, 300], x[3, 7] = float("inf"), float("-inf"), float("nan")
+    x[4] = float("nan")
+    x[5] = float("inf")
+    x[6] *= 1e-42
+    x[7, :128] = 1e-45
+    x[8, 0] = torch.finfo(torch.float32).max
+    x[9] = 448.0
+    x[10] = torch.nextafter(torch.tensor(448.0), torch.tensor(1e9))
+    x[11] = 2.0 ** -126 * 448.0
+    x[12] = 2.0 ** -130
+    x[13] = -0.0
+    x[128:, 128:256] = 0.0
+    x[128:, 256:384] = float("nan")
+    note(f"fp8_quantize special values block_rows={br} {scale}")
+    Q, S, QT, ST = api.fp8_quantize(x.cuda(), block_rows=br, scale_dtype=SCALES[scale], transposed=True)
+    torch.cuda.synchronize()
+    check_codes(x, Q, S, br)
+    check_codes(x.t().contiguous(), QT, ST, br)
+    b = x.to(torch.bfloat16)
+    Q, S, QT, ST = api.fp8_quantize(b.cuda(), block_rows=br, scale_dtype=SCALES[scale], transposed=True)
+    torch.cuda.synchronize()
+    check_codes(b, Q, S, br)
+    check_codes(b.t().contiguous(), QT, ST, br)
+
+
+def test_quantize_every_bf16_rounding():
+    """Every finite bf16 of one binade range against every rounding of e4m3:
+    with a block's top at 448 the power-of-two scale is 1 and the codes are the
+    roundings of the values themselves."""
+    bits = torch.arange(0, 1 << 16, dtype=torch.int32).to(torch.int16)
+    v = bits.view(torch.bfloat16)
+    v = v[torch.isfinite(v) & (v.abs() <= 448)]
+    v = torch.cat([v, torch.zeros(-v.numel() % 127, dtype=torch.bfloat16)]).view(-1, 127)
+    x = torch.cat([torch.full((v.size(0), 1), 448.0, dtype=torch.bfloat16), v], 1)
+    note("fp8_quantize every bf16")
+    Q, S, _, _ = api.fp8_quantize(x.cuda(), scale_dtype=torch.float8_e8m0fnu)
+    torch.cuda.synchronize()
+    assert torch.all(ref.scale_values(S) == 1.0)
+    assert torch.equal(ref.e4m3_values(Q), ref.nearest_e4m3(x.double()))
+
+
+# ---------------------------------------------------------------------------
+
+
+def codes_and_scales(seed, rows, cols, block_rows, scale, wide=False):
+    """Random codes over the whole range of the type and random scales."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g)
+    if wide:
+        x = x * torch.exp2(torch.randint(-8, 8, (rows, cols), generator=g).float())
+    q = x.clamp(-448, 448).to(torch.float8_e4m3fn)
+    shape = (ref.cdiv(rows, block_rows), ref.cdiv(cols, 128))
+    if scale == "f32":
+        s = torch.rand(shape, generator=g) * 0.02 + 1e-3
+    else:
+        s = torch.exp2(torch.randint(-12, 3, shape, generator=g).float()).to(torch.float8_e8m0fnu)
+    return q, s
+
+
+def matmul_reference(a, sa, bra, b, sb, brb):
+    """(product, sum of magnitudes) in 64 bits, on the GPU in float64."""
+    A = (ref.e4m3_values(a) * ref.expand(ref.scale_values(sa), *a.shape, bra)).cuda()
+    B = (ref.e4m3_values(b) * ref.expand(ref.scale_values(sb), *b.shape, brb)).cuda()
+    Bt, Babs = B.t().contiguous(), B.abs().t().contiguous()
+    return (A @ Bt).cpu(), (A.abs() @ Babs).cpu()
+
+
+def group_tops(a, sa, bra, b, sb, brb):
+    """Sum over the groups of eight consecutive k of the largest product."""
+    A = (ref.e4m3_values(a) * ref.expand(ref.scale_values(sa), *a.shape, bra)).abs().float().cuda()
+    B = (ref.e4m3_values(b) * ref.expand(ref.scale_values(sb), *b.shape, brb)).abs().float().cuda()
+    total = torch.zeros(a.size(0), b.size(0), dtype=torch.float64, device="cuda")
+    for k in range(0, a.size(1), 8):
+        top = torch.zeros(a.size(0), b.size(0), device="cuda")
+        for j in range(k, min(k + 8, a.size(1))):
+            top = torch.maximum(top, A[:, j:j + 1] * B[:, j:j + 1].t())
+        total += top
+    return total.cpu()
+
+
+def check_product(got, want, mags, K, add=None, tops=None):
+    """Each of the at most K + ceil(K / 128) additions and the scalings of a
+    block are off by at most one step of fp32 (2 u: the matrix instructions may
+    cut rather than round) of the magnitudes summed so far; then one rounding
+    of the output.
+
+    `tops`, for a bf16 result: the 8-bit matrix instruction keeps the terms of a
+    group of eight products down to 2^-13 of the power of two of the largest,
+    2^(E + F) with E, F the factors' exponents, and cuts below it.  Each of the
+    seven other terms thus loses less than 2^-13 times that power, which is at
+    most the largest product itself: 7 * 2^-13 of it for the group, and the sum
+    of that over the groups for the element."""
+    tol = 2 * U32 * (K + K / 128 + 6) * mags
+    if tops is not None:
+        tol = tol + 7 * 2.0 ** -13 * tops * (1 + 2.0 ** -20)
+    if add is not None:
+        want = want + add.double().cpu()
+        tol = tol + 2 * U32 * (mags + add.double().cpu().abs())
+    tol = tol * (1 + 2 ** -7) + half(got.dtype) * want.abs()
+    err = (got.double().cpu() - want).abs()
+    assert torch.all(err <= tol), float((err / tol.clamp(min=1e-300)).max())
+
+
+def upload(q):
+    v = api.fp8_codes(q.size(0), q.size(1), "cuda")
+    v.view(torch.uint8).copy_(q.cuda().view(torch.uint8))
+    return v
+
+
+MATMULS = [  # m, n, k
+    (1, 1, 1), (1, 128, 128), (1, 777, 1000), (2, 2048, 512), (5, 300, 4096), (16, 256, 2048),
+    (17, 1024, 384), (33, 130, 640), (64, 512, 1024), (100, 100, 100), (128, 128, 128),
+    (129, 257, 385), (200, 640, 130), (256, 256, 256), (300, 1000, 1111), (512, 768, 896),
+    (513, 511, 1025), (1000, 1537, 1111), (1024, 1024, 128), (260, 2052, 8200),
+]
+
+
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("m,n,k", MATMULS)
+def test_matmul(m, n, k, scale):
+    for bra, brb, out, with_add in ((1, 128, "bf16", False), (1, 1, "f32", True), (128, 128, "f32", False),
+                                    (128, 1, "bf16", True)):
+        a, sa = codes_and_scales(m + k, m, k, bra, scale)
+        b, sb = codes_and_scales(n + 2 * k, n, k, brb, scale, wide=True)
+        add = normal(9, m, n, out) if with_add else None
+        note(f"fp8_matmul {m}x{n}x{k} {scale} blocks {bra}/{brb} {out} add={with_add}")
+        c = api.fp8_matmul(upload(a), sa.cuda(), upload(b), sb.cuda(), out_dtype=TYPES[out],
+                           add=None if add is None else add.cuda())
+        torch.cuda.synchronize()
+        want, mags = matmul_reference(a, sa, bra, b, sb, brb)
+        tops = group_tops(a, sa, bra, b, sb, brb) if out == "bf16" else None
+        check_product(c, want, mags, k, add, tops)
+
+
+@pytest.mark.parametrize("m,n,k,extra,offset", [(5, 300, 260, 3, 1), (130, 200, 385, 16, 0),
+                                                (130, 200, 384, 16, 5), (300, 257, 511, 1, 0),
+                                                (20, 640, 1024, 16, 16), (260, 260, 200, 8, 0)])
+def test_matmul_strides(m, n, k, extra, offset):
+    """Codes at any byte, strided scales, outputs at any element, an Add of
+    another type; NaN codes around every operand and nothing written outside."""
+    a, sa = codes_and_scales(1, m, k, 1, "f32")
+    b, sb = codes_and_scales(2, n, k, 128, "f32")
+    add = normal(3, m, n, "bf16")
+    va, vb = padded(a, extra, offset)[0], padded(b, extra, offset)[0]
+    vsa, vsb = padded(sa, extra, offset)[0], padded(sb, extra, offset)[0]
+    vadd = padded(add, extra, offset)[0]
+    c, buf = padded(torch.zeros(m, n), extra, offset)
+    note(f"fp8_matmul strided {m}x{n}x{k} +{extra} @{offset}")
+    api.fp8_matmul(va, vsa, vb, vsb, c, add=vadd)
+    torch.cuda.synchronize()
+    want, mags = matmul_reference(a, sa, 1, b, sb, 128)
+    check_product(c, want, mags, k, add)
+    assert untouched(c, buf)
+
+
+def test_matmul_add_in_place_and_deterministic():
+    for m, n, k in ((3, 500, 1024), (300, 400, 2000)):
+        a, sa = codes_and_scales(1, m, k, 1, "e8m0")
+        b, sb = codes_and_scales(2, n, k, 1, "e8m0")
+        args = upload(a), sa.cuda(), upload(b), sb.cuda()
+        add = normal(4, m, n).cuda()
+        first = api.fp8_matmul(*args, add=add, out_dtype=torch.float32)
+        c = add.clone()
+        api.fp8_matmul(*args, c, add=c)
+        again = api.fp8_matmul(*args, add=add, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        assert torch.equal(first, c) and torch.equal(first, again)
+
+
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("m,n,k", [(4, 200, 300), (300, 300, 300), (70, 260, 1000)])
+def test_matmul_nan_reaches_only_its_row_and_column(m, n, k, scale):
+    a, sa = codes_and_scales(1, m, k, 1, scale)
+    b, sb = codes_and_scales(2, n, k, 1, scale)
+    a.view(torch.uint8)[1, k - 1] = 0x7f
+    b.view(torch.uint8)[150, 0] = 0xff
+    if scale == "f32":
+        sa[3, -1] = float("nan")
+    else:
+        sa.view(torch.uint8)[3, -1] = 255
+    note(f"fp8_matmul NaN {m}x{n}x{k} {scale}")
+    c = api.fp8_matmul(upload(a), sa.cuda(), upload(b), sb.cuda(), out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    bad = torch.isnan(c).cpu()
+    want = torch.zeros(m, n, dtype=torch.bool)
+    want[1], want[3], want[:, 150] = True, True, True
+    assert torch.equal(bad, want)
+
+
+def test_matmul_scale_extremes():
+    """The smallest and largest power-of-two scales, and fp32 scales across the
+    exponent range."""
+    for m in (3, 256):
+        n, k = 256, 256
+        a, sa = codes_and_scales(1, m, k, 1, "e8m0")
+        b, sb = codes_and_scales(2, n, k, 128, "e8m0")
+        sa.view(torch.uint8)[:, 0] = 1       # 2^-126
+        sb.view(torch.uint8)[:, 0] = 200     # 2^73
+        sa.view(torch.uint8)[:, 1] = 247     # 2^120
+        sb.view(torch.uint8)[:, 1] = 7       # 2^-120
+        note(f"fp8_matmul extreme scales m={m}")
+        c = api.fp8_matmul(upload(a), sa.cuda(), upload(b), sb.cuda(), out_dtype=torch.float32)
+        sf = ref.scale_values(sa).float().cuda()
+        tf = ref.scale_values(sb).float().cuda()
+        d = api.fp8_matmul(upload(a), sf, upload(b), tf, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        want, mags = matmul_reference(a, sa, 1, b, sb, 128)
+        check_product(c, want, mags, k)
+        check_product(d, want, mags, k)
+
+
+# ---------------------------------------------------------------------------
+
+
+def check_norm(x, res, w, eps, Q, S, total, y):
+    r = x.double()
+    if res is not None:
+        exact = x.double() + res.double()
+        r = exact.to(x.dtype).double() if x.dtype == torch.bfloat16 else exact.float().double()
+        if total is not None:
+            assert torch.equal(total.cpu().double(), r)
+    n = x.size(1)
+    want = ref.rms_norm(r, w, eps)
+    # sum of n squares, mean, + eps, square root, reciprocal, two products
+    tol = (n / 2 + 8) * U32 * want.abs()
+    if y is not None:
+        assert torch.all((y.cpu().double() - want).abs() <= tol + half(x.dtype) * want.abs())
+    sv, qv = ref.scale_values(S), ref.e4m3_values(Q)
+    top = ref.block_tops(want, 1)
+    if S.dtype == torch.float32:
+        s = ref.f32_scale(top)
+        assert torch.all((sv - s).abs() <= (n / 2 + 9) * U32 * s)
+    else:
+        s = ref.e8m0_scale(top)
+        near = (top / ref.TOP / s - 1).abs().minimum((2 * top / ref.TOP / s - 1).abs()) < (n / 2 + 9) * U32
+        assert torch.all((sv == s) | near)
+    v = want / ref.expand(sv, *want.shape, 1)
+    slack = (n / 2 + 12) * U32 * v.abs()
+    assert torch.all((qv - v).abs() <= torch.maximum(ref.half_step(v), ref.half_step(qv)) + slack)
+
+
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n", [(1, 1), (1, 4096), (3, 127), (37, 512), (5, 520), (8, 1000), (4, 2048),
+                                 (3, 2049), (2, 4100), (2, 8192), (2, 16384), (2, 17000), (1, 65536)])
+def test_norm(m, n, dtype, scale):
+    x, res = normal(1, m, n, dtype, 2.0), normal(2, m, n, dtype)
+    w = 1 + 0.1 * normal(3, 1, n)
+    note(f"rms_norm_fp8 {m}x{n} {dtype} {scale}")
+    total, y = torch.empty_like(x, device="cuda"), torch.empty_like(x, device="cuda")
+    Q, S = api.rms_norm_fp8(x.cuda(), w.cuda(), residual=res.cuda(), sum_out=total, y_out=y,
+                            scale_dtype=SCALES[scale])
+    torch.cuda.synchronize()
+    check_norm(x, res, w, 1e-6, Q, S, total, y)
+    # without the residual and the optional outputs; weight of X's type
+    wb = w.to(x.dtype)
+    Q, S = api.rms_norm_fp8(x.cuda(), wb.cuda(), eps=1e-5, scale_dtype=SCALES[scale])
+    torch.cuda.synchronize()
+    check_norm(x, None, wb, 1e-5, Q, S, None, None)
+
+
+@pytest.mark.parametrize("extra,offset", [(8, 8), (3, 1), (1, 0)])
+def test_norm_strides_and_in_place_sum(extra, offset):
+    m, n = 9, 300
+    x, res, w = normal(1, m, n, "bf16"), normal(2, m, n, "bf16"), normal(3, 1, n)
+    X, xb = padded(x, extra, offset)
+    R, _ = padded(res, extra, offset)
+    Y, yb = padded(torch.zeros(m, n, dtype=torch.bfloat16), extra, offset)
+    Q, qb = padded(torch.zeros(m, n).to(torch.float8_e4m3fn), extra, offset)
+    S, sb = padded(torch.zeros(m, 3), extra, offset)
+    note(f"rms_norm_fp8 strided +{extra} @{offset}")
+    api.rms_norm_fp8(X, w.cuda(), Q, S, residual=R, sum_out=X, y_out=Y)
+    torch.cuda.synchronize()
+    check_norm(x, res, w, 1e-6, Q, S, X, Y)
+    for v, b in ((X, xb), (Y, yb), (Q, qb), (S, sb)):
+        assert untouched(v, b)
+
+
+def test_norm_zero_and_non_finite_rows():
+    x, w = normal(1, 6, 384), torch.ones(1, 384)
+    x[1] = 0.0
+    x[2, 5] = float("nan")
+    x[3, 200] = float("inf")
+    x[4] *= 1e-30
+    note("rms_norm_fp8 zero and non-finite rows")
+    Q, S = api.rms_norm_fp8(x.cuda(), w.cuda())
+    torch.cuda.synchronize()
+    qv, sv = ref.e4m3_values(Q), ref.scale_values(S)
+    assert torch.all(qv[1] == 0) and torch.all(sv[1] == 1)
+    assert torch.all(torch.isnan(qv[2])) and torch.all(sv[2] == 1)
+    # an infinite element: its own result is NaN, the others are 0
+    assert torch.isnan(qv[3, 200]) and int(torch.isnan(qv[3]).sum()) == 1
+    assert torch.all(torch.nan_to_num(qv[3]) == 0)
+    keep = [0, 4, 5]
+    check_norm(x[keep], None, w, 1e-6, Q.view(torch.uint8)[keep].view(torch.float8_e4m3fn), S[keep], None, None)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n", [(1, 1), (1, 4096), (3, 127), (37, 2048), (600, 512), (8, 1000),
+                                 (1100, 260), (3, 4100), (2, 8192), (2, 17000), (2, 65536)])
+def test_norm_gradient(m, n, dtype):
+    x, dy, ds = normal(1, m, n, dtype, 2.0), normal(2, m, n, dtype, 1e-3), normal(3, m, n, dtype, 1e-3)
+    w = 1 + 0.1 * normal(4, 1, n)
+    for dsum, wt in ((ds, w), (None, w.to(x.dtype))):
+        note(f"rms_norm_backward {m}x{n} {dtype} dsum={dsum is not None}")
+        dx, dw = api.rms_norm_backward(dy.cuda(), x.cuda(), wt.cuda(),
+                                       dsum=None if dsum is None else dsum.cuda())
+        torch.cuda.synchronize()
+        wx, ww = ref.rms_norm_backward(dy, x, wt, 1e-6, dsum)
+        t = 1 / torch.sqrt(x.double().square().mean(1, keepdim=True) + 1e-6)
+        h, u = (dy.double() * wt.double()).abs(), x.double().abs() * t
+        mags = t * (h + u * (h * u).mean(1, keepdim=True)) + (0 if dsum is None else dsum.double().abs())
+        tol = 2 * (n + 12) * U32 * mags + half(x.dtype) * wx.abs()
+        assert torch.all((dx.cpu().double() - wx).abs() <= tol)
+        mw = (dy.double().abs() * u).sum(0, keepdim=True)
+        assert torch.all((dw.cpu().double() - ww).abs() <= (m + n / 2 + 10) * U32 * mw)
+
+
+def test_norm_gradient_is_the_forward_calls_difference():
+    """The gradient against central differences of the forward call's y (fp32:
+    the difference of step e is off by about e^2 and by u |L| / e)."""
+    m, n = 3, 256
+    x, dy, w = normal(1, m, n), normal(2, m, n), 1 + 0.1 * normal(3, 1, n)
+    dx, dw = api.rms_norm_backward(dy.cuda(), x.cuda(), w.cuda())
+
+    def loss(xx, ww):
+        y = torch.empty_like(xx, device="cuda")
+        api.rms_norm_fp8(xx.cuda(), ww.cuda(), y_out=y)
+        torch.cuda.synchronize()
+        return float((y.cpu().double() * dy.double()).sum())
+
+    e = 2.0 ** -6
+    for seed in range(4):
+        vx, vw = normal(10 + seed, m, n), normal(20 + seed, 1, n)
+        for num, ana in (((loss(x + e * vx, w) - loss(x - e * vx, w)) / (2 * e),
+                          float((dx.cpu().double() * vx.double()).sum())),
+                         ((loss(x, w + e * vw) - loss(x, w - e * vw)) / (2 * e),
+                          float((dw.cpu().double() * vw.double()).sum()))):
+            scale = float(dy.double().norm() * n ** 0.5)
+            assert abs(num - ana) <= 1e-3 * scale, (num, ana)
+
+
+def test_norm_gradient_in_place_and_strided():
+    m, n = 70, 300
+    x, dy, ds, w = (normal(1, m, n, "bf16"), normal(2, m, n, "bf16"), normal(3, m, n, "bf16"), normal(4, 1, n))
+    want, wdw = api.rms_norm_backward(dy.cuda(), x.cuda(), w.cuda(), dsum=ds.cuda())
+    for target in ("dy", "x", "dsum"):
+        t = {"dy": padded(dy, 3, 1), "x": padded(x, 8, 8), "dsum": padded(ds, 1, 0)}
+        note(f"rms_norm_backward into {target}")
+        v, buf = t[target]
+        _, dw = api.rms_norm_backward(t["dy"][0], t["x"][0], w.cuda(), dX=v, dsum=t["dsum"][0])
+        torch.cuda.synchronize()
+        assert torch.equal(v, want) and torch.equal(dw, wdw) and untouched(v, buf)
