@@ -138,6 +138,7 @@ ortho_status fp8_matmul(ortho_mat A, ortho_mat SA, ortho_mat B, ortho_mat SB, or
   a.M = static_cast<int>(A.rows);
   a.N = static_cast<int>(B.rows);
   a.K = static_cast<int>(A.cols);
+  a.dma = rows_at(&A, 16) && rows_at(&B, 16) && A.ld <= (1 << 22) && B.ld <= (1 << 22);
   return done(launch_fp8_matmul(a, C.dtype == ORTHO_BF16, SA.dtype == ORTHO_E8M0, as_stream(stream)));
 }
 

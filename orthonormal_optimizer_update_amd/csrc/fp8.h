@@ -77,6 +77,11 @@ struct Fp8GemmArgs {
   int add_bf;
   int cvec;                 // C (and Add) take four columns per access
   int M, N, K;
+  int dma;                  // A's and B's rows at multiples of 16 bytes, 256 of them within 2 GiB
+  // set by the launcher
+  int e8m0;
+  int splits, kchunk;       // splits of K, blocks of 128 in each
+  float* part;              // splits x M x N partial sums (splits > 1)
 };
 hipError_t launch_fp8_matmul(const Fp8GemmArgs& a, bool c_bf, bool e8m0, hipStream_t s);
 
