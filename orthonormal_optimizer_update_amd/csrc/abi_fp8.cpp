@@ -134,11 +134,13 @@ ortho_status fp8_matmul(ortho_mat A, ortho_mat SA, ortho_mat B, ortho_mat SB, or
   a.add = data_of(Add);
   a.ldadd = ld_of(Add);
   a.add_bf = Add && Add->dtype == ORTHO_BF16;
-  a.cvec = rows_at(&C, 4 * esz(C)) && (Add == nullptr || rows_at(Add, 4 * esz(*Add)));
+  a.cvec = rows_at(&C, 16) && rows_at(Add, 16);
   a.M = static_cast<int>(A.rows);
   a.N = static_cast<int>(B.rows);
   a.K = static_cast<int>(A.cols);
-  a.dma = rows_at(&A, 16) && rows_at(&B, 16) && A.ld <= (1 << 22) && B.ld <= (1 << 22);
+  constexpr int64_t kMaxLd = 1 << 22;   // 256 rows within 32-bit byte offsets, scales' rows too
+  a.dma = rows_at(&A, 16) && rows_at(&B, 16) && A.ld <= kMaxLd && B.ld <= kMaxLd &&
+          SA.ld <= kMaxLd / 4 && SB.ld <= kMaxLd / 4;
   return done(launch_fp8_matmul(a, C.dtype == ORTHO_BF16, SA.dtype == ORTHO_E8M0, as_stream(stream)));
 }
 

@@ -75,7 +75,7 @@ struct Fp8GemmArgs {
   const void* add;
   int64_t ldc, ldadd;
   int add_bf;
-  int cvec;                 // C (and Add) take four columns per access
+  int cvec;                 // C's (and Add's) rows at multiples of 16 bytes
   int M, N, K;
   int dma;                  // A's and B's rows at multiples of 16 bytes, 256 of them within 2 GiB
   // set by the launcher

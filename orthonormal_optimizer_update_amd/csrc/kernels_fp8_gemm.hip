@@ -37,7 +37,14 @@ __device__ __forceinline__ bf16x8 codes_to_bf16(int lo, int hi) {
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-__device__ __forceinline__ int swz(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
+// Position of a 16-byte chunk in the 128-byte LDS row `row` of a tile, such that
+// the 16 rows of a fragment hit 64 distinct banks: rows r .. r + 15 of A (and of
+// B for an fp32 C), rows 16 (i / 4) + i % 4 + 4 j of B for a bf16 C.
+template <bool kSpread>
+__device__ __forceinline__ int swz(int row, int chunk) {
+  if constexpr (kSpread) return chunk ^ (((row >> 1) & 1) | ((row >> 3) & 6));
+  return chunk ^ ((row >> 1) & 7);
+}
 
 // 16 bytes per lane from global memory into LDS at lds + 16 * lane.  lds must
 // be wave-uniform.  The compiler does not look inside the assembly for
@@ -48,6 +55,27 @@ __device__ __forceinline__ int swz(int row, int chunk) { return chunk ^ ((row >>
 __device__ __forceinline__ void dma16(unsigned voff, const uint8_t* sbase, unsigned lds) {
   asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :: "v"(voff), "s"(sbase), "s"(lds) : "memory");
+}
+
+// Four bytes, or one byte as a word, per lane into LDS at lds + 4 * lane.
+__device__ __forceinline__ void dma4(unsigned voff, const uint8_t* sbase, unsigned lds) {
+  asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :: "v"(voff), "s"(sbase), "s"(lds) : "memory");
+}
+__device__ __forceinline__ void dma1(unsigned voff, const uint8_t* sbase, unsigned lds) {
+  asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, %1"
+               :: "v"(voff), "s"(sbase), "s"(lds) : "memory");
+}
+
+// Waits until at most kOutstanding of the wave's copies are under way and its
+// LDS reads and writes are done, then for the workgroup.
+template <int kOutstanding>
+__device__ __forceinline__ void sync() {
+  static_assert(kOutstanding < 16, "");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(kOutstanding | 7 << 4);   // vmcnt, expcnt off, lgkmcnt 0
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 __device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
@@ -71,36 +99,46 @@ __device__ __forceinline__ uint4 load_codes16(const uint8_t* row, int k, int K) 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A BM x BN tile of C per workgroup, kWM x kWN waves of (16 kMI) x (16 kNJ).
-// The rows of B are the matrix instruction's rows and the rows of A its
-// columns, so a lane holds four consecutive columns of one row of C and needs
-// one scale of A per 16 rows; the scale of a 128 x 128 block of B is the same
-// for the whole wave.
+// A BM x BN tile of C per workgroup, kWM x kWN waves of (16 kMI) x 64.  The
+// rows of B are the matrix instruction's rows and the rows of A its columns, so
+// a lane holds four columns of one row of C per instruction and needs one scale
+// of A per 16 rows; the scale of a 128 x 128 block of B is the same for the
+// whole wave.  Which row of B is which row of instruction j is free: for a bf16
+// C, row 4 g + e is column 16 g + 4 j + e of the wave's 64, so that lane group
+// g ends up with 16 consecutive columns and stores them as two 16-byte pieces;
+// for an fp32 C it is column 16 j + 4 g + e, four 16-byte pieces of which the
+// lane groups' lie side by side.  C is written straight from the accumulators:
+// the LDS is free at once for the next workgroup, whose first copies overlap
+// the stores.
 //
-// A k tile is one block of 128: 128-byte LDS rows of eight 16-byte chunks,
-// chunk c of row r at c ^ ((r >> 1) & 7) so that 16 consecutive rows hit 64
-// distinct banks.  Two stages.  The barrier of a tile sits before its last row
-// of products, when the last fragments are in registers: the copies of the
-// tile after next and the next tile's first fragment reads go out under those
-// products, and a copy has a whole tile's time to arrive.  Copies go straight
-// from L2 into LDS (kDma; rows at multiples of 16 bytes) or through registers
-// (rows at any byte).
+// A k tile is one block of 128: 128-byte LDS rows of eight 16-byte chunks, two
+// stages.  B's fragments and the scales of a tile sit in registers from its
+// start and A's are read 16 rows at a time, so a stage empties in two steps,
+// each at a barrier, and each step's copies of the tile after next go out at
+// once, spread over the products that follow:
+//   barrier M, before the last products of the first half of A's rows:
+//     B, the scales and that half are free;  the second half has arrived
+//   barrier E, before the tile's last 16 rows of products:
+//     the second half is free;  the next tile's B, scales and first half have
+//     arrived, and its first fragments are read under those products
+// A copy thus has one and a half tiles' time to arrive, in two stages.  (With
+// one barrier per tile a copy has at most one, and the 256 x 256 tiles of
+// 8192^3 took 545 us.)  Copies go straight from L2 into LDS (kDma; rows at
+// multiples of 16 bytes), or through registers (rows at any byte).
 template <int kMode, bool kRowB, int kWM, int kWN, int kMI, int kNJ, bool kDma>
 __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs p) {
   constexpr int kThreads = kWM * kWN * 64, BM = kWM * kMI * 16, BN = kWN * kNJ * 16;
   constexpr int kStage = (BM + BN) * 128;
-  constexpr int kGroups = (BM + BN) / 8 / (kWM * kWN);   // 8-row copies per wave and tile
+  constexpr int kWaves = kWM * kWN;
   constexpr int kSlots = kMI * kNJ;
-  constexpr int kScaleRows = (BM + BN + kThreads - 1) / kThreads;
-  // The result leaves through LDS in kPasses passes of BM / kPasses rows.
-  constexpr int kPasses = BM * BN * 4 > 2 * kStage + BM * 16 ? 2 : 1;
-  constexpr int kOutRow = BN + 4;                         // floats; rows 16 bytes apart in banks
-  constexpr int kOutBytes = BM / kPasses * kOutRow * 4;
-  constexpr int kLds = kOutBytes > 2 * kStage ? kOutBytes : 2 * kStage;
-  static_assert(kSlots % 4 == 0 && kMI % kPasses == 0, "");
-  static_assert(kThreads <= BM + BN && (BM + BN) % kThreads == 0, "");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kLds];
-  __shared__ __attribute__((aligned(16))) float scales[2][BM + BN];
+  // 8-row copies per wave and tile: B's, the first half of A's rows, the second
+  constexpr int kCopyB = BN / 8 / kWaves, kCopyA = BM / 16 / kWaves, kCopies = kCopyB + 2 * kCopyA;
+  constexpr int kM = kMI / 2 - 1, kE = kMI - 1;   // groups of products behind the barriers
+  constexpr bool kBf = kMode != kExact;
+  static_assert(kSlots % 4 == 0 && kNJ == 4, "");
+  static_assert(kThreads == BM + BN && kCopyB * kWaves * 8 == BN && kCopyA * kWaves * 16 == BM, "");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
+  __shared__ __attribute__((aligned(16))) uint32_t scales[2][BM + BN];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = (wave / kWN) * (kMI * 16), wn = (wave % kWN) * (kNJ * 16);
@@ -123,17 +161,25 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   const int tail = p.K % kFp8Block;   // codes in the last tile, 0: all
   const int tail_kt = tail != 0 ? nkb - 1 : nkb;
 
-  // copies: group g of this wave is rows 8 (wave kGroups + g) .. + 7 of the
-  // stage (A's rows, then B's); lane = 8 * (row of the group) + chunk position
-  auto row_of = [&](int g) { return (wave * kGroups + g) * 8 + (lane >> 3); };
-  auto chunk_of = [&](int g) { return swz(row_of(g), lane & 7); };
+  // copy g of this wave: 8 rows of the stage (A's rows, then B's), lane = 8 *
+  // (row of the 8) + chunk position; g < kCopyB: B; then the halves of A (the
+  // first or second 8 kMI rows of every wave)
+  auto rows8 = [&](int g) {
+    if (g < kCopyB) return BM + (wave * kCopyB + g) * 8;
+    const int half = (g - kCopyB) / kCopyA, x = (wave * kCopyA + (g - kCopyB) % kCopyA) * 8;
+    return x / (8 * kMI) * (16 * kMI) + half * (8 * kMI) + x % (8 * kMI);
+  };
+  auto row_of = [&](int g) { return rows8(g) + (lane >> 3); };
+  auto place = [&](int r, int c) { return r < BM ? swz<false>(r, c) : swz<kBf>(r - BM, c); };
+  auto chunk_of = [&](int g) { return place(row_of(g), lane & 7); };
   auto matrix_row = [&](int r) { return r < BM ? min(m0 + r, p.M - 1) : min(n0 + r - BM, p.N - 1); };
-  unsigned voff[kGroups];
+  unsigned voff[kCopies];
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
+  for (int g = 0; g < kCopies; ++g) {
     const int r = row_of(g), mr = matrix_row(r);
     voff[g] = static_cast<unsigned>(r < BM ? (mr - m0) * p.lda : (mr - n0) * p.ldb) + chunk_of(g) * 16;
   }
+  const unsigned scales0 = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(lds_ptr_t)(&scales[0][0]));
   const unsigned lds0 = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(lds_ptr_t)(smem));
   const uint8_t* const a0 = uniform_ptr(p.a + (int64_t)m0 * p.lda);
   const uint8_t* const b0 = uniform_ptr(p.b + (int64_t)n0 * p.ldb);
@@ -141,27 +187,22 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   // whole is taken from column 0 instead, and patch_tail replaces it.
   auto tail_offsets = [&]() {
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
+    for (int g = 0; g < kCopies; ++g) {
       const int k = (nkb - 1) * 128 + chunk_of(g) * 16;
       voff[g] = voff[g] - chunk_of(g) * 16 + (k + 16 <= p.K ? k : 0);
     }
   };
   auto copy_group = [&](int g, int kt, int st) {
-    const int r8 = (wave * kGroups + g) * 8;
+    const int r8 = rows8(g);
     if constexpr (kDma) {
       const int64_t k0 = kt == tail_kt ? 0 : (int64_t)kt * 128;   // the last tile's offsets hold its k
-      dma16(voff[g], (r8 < BM ? a0 : b0) + k0, lds0 + st * kStage + r8 * 128);
+      dma16(voff[g], (g < kCopyB ? b0 : a0) + k0, lds0 + st * kStage + r8 * 128);
     } else {
       const int r = row_of(g), mr = matrix_row(r);
       const uint8_t* src = r < BM ? p.a + (int64_t)mr * p.lda : p.b + (int64_t)mr * p.ldb;
       *reinterpret_cast<uint4*>(smem + st * kStage + r8 * 128 + lane * 16) =
           load_codes16(src, kt * 128 + chunk_of(g) * 16, p.K);
     }
-  };
-  auto copy_tile = [&](int kt, int st) {
-    if (kDma && kt == tail_kt) tail_offsets();
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) copy_group(g, kt, st);
   };
   // The last tile's codes from the first chunk that is not whole on.
   auto patch_tail = [&](int st) {
@@ -171,30 +212,35 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
       if (c < (tail >> 4)) continue;
       const int mr = matrix_row(r);
       const uint8_t* src = r < BM ? p.a + (int64_t)mr * p.lda : p.b + (int64_t)mr * p.ldb;
-      *reinterpret_cast<uint4*>(smem + st * kStage + (r * 8 + swz(r, c)) * 16) =
+      *reinterpret_cast<uint4*>(smem + st * kStage + (r * 8 + place(r, c)) * 16) =
           load_codes16(src, (nkb - 1) * 128 + c * 16, p.K);
     }
   };
 
-  // scales of tile kt for the stage rows t, t + kThreads, ...
-  auto load_scales = [&](int kt, float (&s)[kScaleRows]) {
-    kt = min(kt, nkb - 1);
-#pragma unroll
-    for (int q = 0; q < kScaleRows; ++q) {
-      const int r = t + q * kThreads, mr = matrix_row(r);
-      const void* sp = r < BM ? p.sa.p : p.sb.p;
-      const int64_t at = (int64_t)(mr >> (r < BM ? p.sa.shift : p.sb.shift)) * (r < BM ? p.sa.ld : p.sb.ld) + kt;
-      if constexpr (kMode == kHardware)
-        s[q] = __uint_as_float(static_cast<const uint8_t*>(sp)[at]);
-      else if constexpr (kMode == kScaled)
-        s[q] = load_scale<false>(sp, at);
-      else
-        s[q] = p.e8m0 ? load_scale<true>(sp, at) : load_scale<false>(sp, at);
+  // scales: the wave's 64 rows of the stage, one per lane (bytes as words)
+  constexpr bool kByteOnly = kMode == kHardware;
+  const int scale_size = kByteOnly || (kMode == kExact && p.e8m0) ? 1 : 4;
+  const bool scales_a = wave * 64 < BM;
+  const int s_shift = scales_a ? p.sa.shift : p.sb.shift;
+  const int64_t s_ld = (scales_a ? p.sa.ld : p.sb.ld) * scale_size;
+  const int s_first = (scales_a ? m0 : n0) >> s_shift;
+  const uint8_t* const s0 =
+      uniform_ptr(static_cast<const uint8_t*>(scales_a ? p.sa.p : p.sb.p) + s_first * s_ld);
+  const int64_t s_off = ((matrix_row(wave * 64 + lane) >> s_shift) - s_first) * s_ld;
+  auto copy_scales = [&](int kt, int st) {
+    const uint8_t* base = s0 + (int64_t)kt * scale_size;
+    if constexpr (kDma) {
+      const unsigned at = scales0 + (st * (BM + BN) + wave * 64) * 4;
+      if (scale_size == 1) dma1(static_cast<unsigned>(s_off), base, at);
+      else dma4(static_cast<unsigned>(s_off), base, at);
+    } else {
+      scales[st][wave * 64 + lane] = scale_size == 1 ? base[s_off] : *reinterpret_cast<const uint32_t*>(base + s_off);
     }
   };
-  auto put_scales = [&](int buf, const float (&s)[kScaleRows]) {
-#pragma unroll
-    for (int q = 0; q < kScaleRows; ++q) scales[buf][t + q * kThreads] = s[q];
+  // a scale as it was copied -> its value
+  auto scale_value = [&](uint32_t u) {
+    if (kMode == kExact && p.e8m0) u = u == 0 ? 0x00400000u : (u == 255 ? 0x7fc00000u : u << 23);
+    return __uint_as_float(u);
   };
 
   floatx4 acc[kMI][kNJ];
@@ -203,19 +249,25 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
 #pragma unroll
     for (int j = 0; j < kNJ; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  // 16 rows of 128 codes (row: a multiple of 16): lane l takes chunks l / 16
-  // and l / 16 + 4 of row l % 16 (the order of k within a block is free, if
-  // both operands share it)
-  const int flo = ((lane & 15) * 8 + swz(lane & 15, lane >> 4)) * 16;
-  const int fhi = ((lane & 15) * 8 + swz(lane & 15, (lane >> 4) + 4)) * 16;
-  auto frag = [&](int off) {
-    const uint4 lo = *reinterpret_cast<const uint4*>(smem + flo + off);
-    const uint4 hi = *reinterpret_cast<const uint4*>(smem + fhi + off);
-    return intx8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+  // 16 rows of 128 codes: lane l takes chunks l / 16 and l / 16 + 4 of its row
+  // (the order of k within a block is free, if both operands share it)
+  auto chunks = [&](int row, int lo, int hi) {
+    const uint4 x = *reinterpret_cast<const uint4*>(smem + row + lo);
+    const uint4 y = *reinterpret_cast<const uint4*>(smem + row + hi);
+    return intx8{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
   };
+  const int l16 = lane & 15, lg = lane >> 4;
+  const int alo = (l16 * 8 + swz<false>(l16, lg)) * 16, ahi = (l16 * 8 + swz<false>(l16, lg + 4)) * 16;
+  const int brow = kBf ? l16 / 4 * 16 + l16 % 4 : l16;
+  constexpr int kBStep = kBf ? 4 : 16;   // rows of B between fragments
+  // rows 4 apart within 16 share a place (swz<true>), as rows 16 apart do (swz<false>)
+  const int blo = (brow * 8 + swz<kBf>(brow, lg)) * 16, bhi = (brow * 8 + swz<kBf>(brow, lg + 4)) * 16;
+  auto frag_a = [&](int off) { return chunks(off, alo, ahi); };
+  auto frag_b = [&](int off) { return chunks(off, blo, bhi); };
   const int offa = wm * 128, offb = (BM + wn) * 128;
-  const float* const my_sa = &scales[0][wm + (lane & 15)];
-  const float* const my_sb = &scales[0][BM + wn + (kMode == kHardware ? (lane & 15) : (kRowB ? (lane >> 4) * 4 : 0))];
+  const uint32_t* const my_sa = &scales[0][wm + l16];
+  const uint32_t* const my_sb =
+      &scales[0][BM + wn + (kMode == kHardware ? brow : (kRowB ? lg * (kBf ? 16 : 4) : 0))];
 
   intx8 fa[2], fb[kNJ];
   bf16x8 xa[4], xb[kNJ][4];              // kExact: the fragments as bf16
@@ -225,26 +277,30 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   floatx4 sb[kRowB ? kNJ : 1];
   int ea[kMI], eb[kNJ];                  // kHardware: scale bytes
 
-  float next_scales[kScaleRows];
-  {
-    float s[kScaleRows];
-    load_scales(kt_begin, s);
-    put_scales(0, s);
-    load_scales(kt_begin + 1, s);
-    put_scales(1, s);
+  // The copies of a tile, in this order (the waits count them): scales, B, the
+  // first half of A, the second half.
+  constexpr int kPerTile = 1 + kCopies;
+  auto first_copies = [&](int kt, int st) {
+    copy_scales(kt, st);
+#pragma unroll
+    for (int g = 0; g < kCopies; ++g) copy_group(g, kt, st);
+  };
+  if (kDma && kt_begin == tail_kt) tail_offsets();
+  first_copies(kt_begin, 0);
+  if (kt_begin + 1 < kt_end) {
+    if (kDma && kt_begin + 1 == tail_kt) tail_offsets();
+    first_copies(kt_begin + 1, 1);
+    sync<kPerTile>();
+  } else {
+    sync<0>();
   }
-  copy_tile(kt_begin, 0);
-  if (kt_begin + 1 < kt_end) copy_tile(kt_begin + 1, 1);
-  load_scales(kt_begin + 2, next_scales);
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
   if (kDma && kt_begin == tail_kt) {
     patch_tail(0);
     __syncthreads();
   }
-  fa[0] = frag(offa);
+  fa[0] = frag_a(offa);
 #pragma unroll
-  for (int j = 0; j < kNJ; ++j) fb[j] = frag(offb + j * 2048);
+  for (int j = 0; j < kNJ; ++j) fb[j] = frag_b(offb + j * kBStep * 128);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     sum[q] = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -254,35 +310,38 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   for (int kt = kt_begin; kt < kt_end; ++kt) {
     const int cur = (kt - kt_begin) & 1;
     const int here = cur * kStage, next = (cur ^ 1) * kStage;
+    const bool more = kt + 2 < kt_end;   // there is a tile after next
     // this tile's scales
     if constexpr (kMode == kHardware) {
 #pragma unroll
-      for (int i = 0; i < kMI; ++i) ea[i] = __float_as_int(my_sa[cur * (BM + BN) + i * 16]);
+      for (int i = 0; i < kMI; ++i) ea[i] = my_sa[cur * (BM + BN) + i * 16];
 #pragma unroll
-      for (int j = 0; j < kNJ; ++j) eb[j] = __float_as_int(my_sb[cur * (BM + BN) + j * 16]);
+      for (int j = 0; j < kNJ; ++j) eb[j] = my_sb[cur * (BM + BN) + j * kBStep];
     } else {
 #pragma unroll
-      for (int i = 0; i < kMI; ++i) sa[i] = my_sa[cur * (BM + BN) + i * 16];
+      for (int i = 0; i < kMI; ++i) sa[i] = scale_value(my_sa[cur * (BM + BN) + i * 16]);
 #pragma unroll
       for (int j = 0; j < (kRowB ? kNJ : 1); ++j) {
-        if constexpr (kRowB) sb[j] = *reinterpret_cast<const floatx4*>(my_sb + cur * (BM + BN) + j * 16);
-        else sb[j][0] = my_sb[cur * (BM + BN)];
+        if constexpr (kRowB) {
+          const uint4 u = *reinterpret_cast<const uint4*>(my_sb + cur * (BM + BN) + j * kBStep);
+          sb[j] = floatx4{scale_value(u.x), scale_value(u.y), scale_value(u.z), scale_value(u.w)};
+        } else {
+          sb[j][0] = scale_value(my_sb[cur * (BM + BN)]);
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < kMI; ++i) {
-      if (i == kMI - 1) {
-        // the tile's last fragments are in registers and the next tile has
-        // arrived: hand this stage to the tile after next
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0);
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (kDma && kt + 1 == tail_kt && kt + 1 < kt_end) {
+      if (i == kM || i == kE) {
+        // Since the copies that have to be here by now, one tile's worth was
+        // issued; near the end there are fewer, and the wait is for all.
+        if (more) sync<kPerTile>();
+        else sync<0>();
+        if (kDma && i == kE && kt + 1 == tail_kt && kt + 1 < kt_end) {
           patch_tail(cur ^ 1);
           __syncthreads();
         }
-        if (kDma && kt + 2 == tail_kt && kt + 2 < kt_end) tail_offsets();
+        if (kDma && i == kM && kt + 2 == tail_kt && more) tail_offsets();
       }
       if constexpr (kMode == kExact) {
 #pragma unroll
@@ -291,7 +350,7 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
 #pragma unroll
       for (int j = 0; j < kNJ; ++j) {
         const int slot = i * kNJ + j;
-        if (j == 0) fa[(i + 1) & 1] = frag(i + 1 < kMI ? here + offa + (i + 1) * 2048 : next + offa);
+        if (j == 0) fa[(i + 1) & 1] = frag_a(i + 1 < kMI ? here + offa + (i + 1) * 2048 : next + offa);
         if constexpr (kMode == kHardware) {
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i & 1], acc[i][j], 0, 0, 0,
                                                                        eb[j], 0, ea[i]);
@@ -326,18 +385,23 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
             factor[slot & 3][0] = sa[i] * sb[0][0];
           }
         }
-        if (i == kMI - 1) {
-          fb[j] = frag(next + offb + j * 2048);
-          if (kt + 2 < kt_end) {
+        if (i == kE) fb[j] = frag_b(next + offb + j * kBStep * 128);
+        // the copies behind barrier M, one every second or third slot, and
+        // those behind barrier E
+        if (more) {
+          constexpr int kStep = (kE - kM) * kNJ / (1 + kCopyB + kCopyA);
+          const int x = slot - kM * kNJ;
+          if (x >= 0 && x % kStep == 0 && x / kStep <= kCopyB + kCopyA) {
+            if (x == 0) copy_scales(kt + 2, cur);
+            else copy_group(x / kStep - 1, kt + 2, cur);
+          }
+          if (i == kE) {
 #pragma unroll
-            for (int g = j * kGroups / kNJ; g < (j + 1) * kGroups / kNJ; ++g) copy_group(g, kt + 2, cur);
+            for (int g = j * kCopyA / kNJ; g < (j + 1) * kCopyA / kNJ; ++g)
+              copy_group(kCopyB + kCopyA + g, kt + 2, cur);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
-      }
-      if (i == kMI - 1) {
-        put_scales(cur, next_scales);
-        load_scales(kt + 3, next_scales);
       }
     }
   }
@@ -351,58 +415,59 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
     }
   }
 
-  // The result through LDS, then whole rows, four columns per lane.
-  constexpr bool kBf = kMode != kExact;
-  constexpr int kIters = BM / kPasses * BN / 4 / kThreads;
-  float* const stage = reinterpret_cast<float*>(smem);
+  // Columns of piece j of a lane: four, next to those of piece j + 1 for bf16.
+  const bool whole = n0 + wn + 64 <= p.N && p.cvec;
 #pragma unroll
-  for (int pass = 0; pass < kPasses; ++pass) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMI / kPasses; ++i)
+  for (int i = 0; i < kMI; ++i) {
+    const int m = m0 + wm + i * 16 + l16;
+    if (m >= p.M) continue;
+    const int nl = n0 + wn + lg * (kBf ? 16 : 4);
+    if (p.part) {
+      float* o = p.part + ((int64_t)split * p.M + m) * p.N;
 #pragma unroll
       for (int j = 0; j < kNJ; ++j)
-        *reinterpret_cast<floatx4*>(stage + (wm / kPasses + i * 16 + (lane & 15)) * kOutRow + wn + j * 16 +
-                                    (lane >> 4) * 4) = acc[pass * (kMI / kPasses) + i][j];
-    __syncthreads();
-#pragma unroll 2
-    for (int q = 0; q < kIters; ++q) {
-      const int x = q * kThreads + t, r = x / (BN / 4), c = x % (BN / 4) * 4;
-      // LDS row r is row r / h * (kPasses h) + pass h + r % h of the tile, h = 16 kMI / kPasses
-      constexpr int h = kMI * 16 / kPasses;
-      const int m = m0 + r / h * (kMI * 16) + pass * h + r % h, n = n0 + c;
-      if (m >= p.M || n >= p.N) continue;
-      floatx4 v = *reinterpret_cast<const floatx4*>(stage + r * kOutRow + c);
-      if (p.part) {
-        float* o = p.part + ((int64_t)split * p.M + m) * p.N;
-        if (p.N % 4 == 0) {
-          *reinterpret_cast<floatx4*>(o + n) = v;
-        } else {
-          for (int e = 0; e < 4; ++e)
-            if (n + e < p.N) o[n + e] = v[e];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int n = nl + j * kBStep + e;
+          if (n < p.N) o[n] = acc[i][j][e];
         }
-        continue;
-      }
-      if (p.add) {
+      continue;
+    }
+    if (p.add) {
+#pragma unroll
+      for (int j = 0; j < kNJ; ++j) {
+        const int n = nl + j * kBStep;
         const float4 ad = p.add_bf ? load4<uint16_t>(static_cast<const uint16_t*>(p.add) + m * p.ldadd, n, p.N, p.cvec)
                                    : load4<float>(static_cast<const float*>(p.add) + m * p.ldadd, n, p.N, p.cvec);
-        v[0] += ad.x; v[1] += ad.y; v[2] += ad.z; v[3] += ad.w;
+        acc[i][j][0] += ad.x; acc[i][j][1] += ad.y; acc[i][j][2] += ad.z; acc[i][j][3] += ad.w;
       }
-      if constexpr (kBf) {
-        uint16_t* o = static_cast<uint16_t*>(p.c) + m * p.ldc;
-        if (p.cvec && n + 4 <= p.N) {
-          *reinterpret_cast<uint2*>(o + n) = pack_bf16x4(v);
+    }
+    if constexpr (kBf) {
+      uint16_t* o = static_cast<uint16_t*>(p.c) + m * p.ldc;
+#pragma unroll
+      for (int j = 0; j < kNJ; j += 2) {
+        const uint2 lo = pack_bf16x4(acc[i][j]), hi = pack_bf16x4(acc[i][j + 1]);
+        const int n = nl + j * 4;
+        if (whole) {
+          *reinterpret_cast<uint4*>(o + n) = make_uint4(lo.x, lo.y, hi.x, hi.y);
         } else {
-          for (int e = 0; e < 4; ++e)
-            if (n + e < p.N) o[n + e] = to_bf16_bits(v[e]);
+          const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < p.N) o[n + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
         }
-      } else {
-        float* o = static_cast<float*>(p.c) + m * p.ldc;
-        if (p.cvec && n + 4 <= p.N) {
-          *reinterpret_cast<floatx4*>(o + n) = v;
+      }
+    } else {
+      float* o = static_cast<float*>(p.c) + m * p.ldc;
+#pragma unroll
+      for (int j = 0; j < kNJ; ++j) {
+        const int n = nl + j * 16;
+        if (whole) {
+          *reinterpret_cast<floatx4*>(o + n) = acc[i][j];
         } else {
+#pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (n + e < p.N) o[n + e] = v[e];
+            if (n + e < p.N) o[n + e] = acc[i][j][e];
         }
       }
     }
