@@ -22,6 +22,9 @@ namespace ortho {
 
 namespace {
 
+// The kernel's lambdas share its state by reference: inlined, it stays in registers.
+#define ORTHO_INLINE __attribute__((always_inline))
+
 typedef int intx8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
@@ -71,13 +74,15 @@ __device__ __forceinline__ void dma1(unsigned voff, const uint8_t* sbase, unsign
 // LDS reads and writes are done, then for the workgroup.
 template <int kOutstanding>
 __device__ __forceinline__ void sync() {
-  static_assert(kOutstanding < 16, "");
+  static_assert(kOutstanding < 64, "");
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(kOutstanding | 7 << 4);   // vmcnt, expcnt off, lgkmcnt 0
+  // vmcnt kOutstanding, expcnt off, lgkmcnt 0
+  __builtin_amdgcn_s_waitcnt((kOutstanding & 15) | (kOutstanding >> 4) << 14 | 7 << 4);
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
+__device__ __forceinline__ unsigned uniform(unsigned x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
   const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
@@ -117,7 +122,7 @@ __device__ __forceinline__ uint4 load_codes16(const uint8_t* row, int k, int K) 
 // each at a barrier, and each step's copies of the tile after next go out at
 // once, spread over the products that follow:
 //   barrier M, before the last products of the first half of A's rows:
-//     B, the scales and that half are free;  the second half has arrived
+//     B and that half are free;  the second half has arrived
 //   barrier E, before the tile's last 16 rows of products:
 //     the second half is free;  the next tile's B, scales and first half have
 //     arrived, and its first fragments are read under those products
@@ -125,7 +130,7 @@ __device__ __forceinline__ uint4 load_codes16(const uint8_t* row, int k, int K) 
 // one barrier per tile a copy has at most one, and the 256 x 256 tiles of
 // 8192^3 took 545 us.)  Copies go straight from L2 into LDS (kDma; rows at
 // multiples of 16 bytes), or through registers (rows at any byte).
-template <int kMode, bool kRowB, int kWM, int kWN, int kMI, int kNJ, bool kDma>
+template <int kMode, bool kRowB, int kWM, int kWN, int kMI, int kNJ, bool kDma, bool kWhole>
 __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs p) {
   constexpr int kThreads = kWM * kWN * 64, BM = kWM * kMI * 16, BN = kWN * kNJ * 16;
   constexpr int kStage = (BM + BN) * 128;
@@ -138,65 +143,88 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   static_assert(kSlots % 4 == 0 && kNJ == 4, "");
   static_assert(kThreads == BM + BN && kCopyB * kWaves * 8 == BN && kCopyA * kWaves * 16 == BM, "");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
-  __shared__ __attribute__((aligned(16))) uint32_t scales[2][BM + BN];
+  __shared__ __attribute__((aligned(16))) uint32_t scales[3][BM + BN];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = (wave / kWN) * (kMI * 16), wn = (wave % kWN) * (kNJ * 16);
 
-  // Each XCD (workgroup id mod 8) gets a contiguous run of tiles, walked in
-  // groups of 4 tile rows, so that a run shares row blocks in that XCD's L2.
+  // Units of work: tiles of C times splits of K.  Each XCD (workgroup id mod 8)
+  // gets a contiguous run of them, walked in groups of 4 tile rows so that what
+  // runs together shares row blocks in that XCD's L2.
   const int tiles_n = (p.N + BN - 1) / BN, tiles_m = (p.M + BM - 1) / BM;
-  const int nwg = tiles_n * tiles_m;
-  int tile = blockIdx.x % nwg;
-  const int split = blockIdx.x / nwg;
-  {
-    const int xcd = tile & 7, each = nwg >> 3, rest = nwg & 7;
-    tile = xcd * each + min(xcd, rest) + (tile >> 3);
-  }
-  const int group = 4 * tiles_n, first_m = (tile / group) * 4, gsize = min(tiles_m - first_m, 4);
-  const int m0 = (first_m + (tile % group) % gsize) * BM, n0 = ((tile % group) / gsize) * BN;
+  const int tiles = tiles_n * tiles_m, units = tiles * p.splits;
+  const int xcd = blockIdx.x & 7, each = units >> 3, rest = units & 7;
+  const int run_first = xcd * each + min(xcd, rest), run_end = run_first + each + (xcd < rest ? 1 : 0);
+  const int run_step = static_cast<int>(gridDim.x) < units ? gridDim.x >> 3 : units;   // < units: kWhole only
+  auto place_unit = [&](int u, int& m, int& n, int& sp) ORTHO_INLINE {
+    sp = u / tiles;
+    const int tile = u - sp * tiles, group = 4 * tiles_n, g = tile / group;
+    const int gsize = min(tiles_m - g * 4, 4), in = tile - g * group, col = in / gsize;
+    m = (g * 4 + in - col * gsize) * BM;
+    n = col * BN;
+  };
+  int unit = run_first + (blockIdx.x >> 3), m0, n0, split;
+  place_unit(unit, m0, n0, split);
 
   const int nkb = (p.K + kFp8Block - 1) / kFp8Block;
-  const int kt_begin = split * p.kchunk, kt_end = min(kt_begin + p.kchunk, nkb);
-  const int tail = p.K % kFp8Block;   // codes in the last tile, 0: all
+  int kt_begin = split * p.kchunk, kt_end = min(kt_begin + p.kchunk, nkb);
+  const int tail = kWhole ? 0 : p.K % kFp8Block;   // codes in the last tile, 0: all
   const int tail_kt = tail != 0 ? nkb - 1 : nkb;
 
   // copy g of this wave: 8 rows of the stage (A's rows, then B's), lane = 8 *
   // (row of the 8) + chunk position; g < kCopyB: B; then the halves of A (the
   // first or second 8 kMI rows of every wave)
-  auto rows8 = [&](int g) {
+  auto rows8 = [&](int g) ORTHO_INLINE {
     if (g < kCopyB) return BM + (wave * kCopyB + g) * 8;
     const int half = (g - kCopyB) / kCopyA, x = (wave * kCopyA + (g - kCopyB) % kCopyA) * 8;
     return x / (8 * kMI) * (16 * kMI) + half * (8 * kMI) + x % (8 * kMI);
   };
-  auto row_of = [&](int g) { return rows8(g) + (lane >> 3); };
-  auto place = [&](int r, int c) { return r < BM ? swz<false>(r, c) : swz<kBf>(r - BM, c); };
-  auto chunk_of = [&](int g) { return place(row_of(g), lane & 7); };
-  auto matrix_row = [&](int r) { return r < BM ? min(m0 + r, p.M - 1) : min(n0 + r - BM, p.N - 1); };
-  unsigned voff[kCopies];
+  auto row_of = [&](int g) ORTHO_INLINE { return rows8(g) + (lane >> 3); };
+  auto place = [&](int r, int c) ORTHO_INLINE { return r < BM ? swz<false>(r, c) : swz<kBf>(r - BM, c); };
+  auto chunk_of = [&](int g) ORTHO_INLINE { return place(row_of(g), lane & 7); };
+  auto matrix_row = [&](int r) ORTHO_INLINE {
+    if (kWhole) return r < BM ? m0 + r : n0 + r - BM;
+    return r < BM ? min(m0 + r, p.M - 1) : min(n0 + r - BM, p.N - 1);
+  };
+  // What a lane adds to a copy's base address.  kWhole: its row of the 8, and
+  // the chunk that belongs at its position (the part of swz that depends on
+  // the 8 rows is uniform); otherwise rows past the matrix are the last row.
+  const int sub = lane >> 3;
+  const unsigned row_a = sub * static_cast<unsigned>(p.lda), row_b = sub * static_cast<unsigned>(p.ldb);
+  const unsigned chunk_a = swz<false>(sub, lane & 7) * 16, chunk_b = swz<kBf>(sub, lane & 7) * 16;
+  unsigned voff[kWhole ? 1 : kCopies];
+  if constexpr (!kWhole) {
 #pragma unroll
-  for (int g = 0; g < kCopies; ++g) {
-    const int r = row_of(g), mr = matrix_row(r);
-    voff[g] = static_cast<unsigned>(r < BM ? (mr - m0) * p.lda : (mr - n0) * p.ldb) + chunk_of(g) * 16;
+    for (int g = 0; g < kCopies; ++g) {
+      const int r = row_of(g), mr = matrix_row(r);
+      voff[g] = static_cast<unsigned>(r < BM ? (mr - m0) * p.lda : (mr - n0) * p.ldb) + chunk_of(g) * 16;
+    }
   }
   const unsigned scales0 = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(lds_ptr_t)(&scales[0][0]));
   const unsigned lds0 = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(lds_ptr_t)(smem));
-  const uint8_t* const a0 = uniform_ptr(p.a + (int64_t)m0 * p.lda);
-  const uint8_t* const b0 = uniform_ptr(p.b + (int64_t)n0 * p.ldb);
+  const uint8_t* a0 = uniform_ptr(p.a + (int64_t)m0 * p.lda);
+  const uint8_t* b0 = uniform_ptr(p.b + (int64_t)n0 * p.ldb);
   // Before the copies of the last tile, if it is short: a chunk that is not
   // whole is taken from column 0 instead, and patch_tail replaces it.
-  auto tail_offsets = [&]() {
+  auto tail_offsets = [&]() ORTHO_INLINE {
+    if constexpr (!kWhole)
 #pragma unroll
     for (int g = 0; g < kCopies; ++g) {
       const int k = (nkb - 1) * 128 + chunk_of(g) * 16;
       voff[g] = voff[g] - chunk_of(g) * 16 + (k + 16 <= p.K ? k : 0);
     }
   };
-  auto copy_group = [&](int g, int kt, int st) {
+  auto copy_group = [&](int g, int kt, int st) ORTHO_INLINE {
     const int r8 = rows8(g);
-    if constexpr (kDma) {
+    const bool is_a = g >= kCopyB;
+    const unsigned at = uniform(lds0 + st * kStage + r8 * 128);
+    if constexpr (kDma && kWhole) {
+      const unsigned key = is_a ? swz<false>(r8, 0) : swz<kBf>(r8 - BM, 0);
+      const uint8_t* base = (is_a ? a0 + r8 * p.lda : b0 + (r8 - BM) * p.ldb) + (int64_t)kt * 128;
+      dma16((is_a ? row_a : row_b) + ((is_a ? chunk_a : chunk_b) ^ (key * 16)), uniform_ptr(base), at);
+    } else if constexpr (kDma) {
       const int64_t k0 = kt == tail_kt ? 0 : (int64_t)kt * 128;   // the last tile's offsets hold its k
-      dma16(voff[g], (g < kCopyB ? b0 : a0) + k0, lds0 + st * kStage + r8 * 128);
+      dma16(voff[g], uniform_ptr((is_a ? a0 : b0) + k0), at);
     } else {
       const int r = row_of(g), mr = matrix_row(r);
       const uint8_t* src = r < BM ? p.a + (int64_t)mr * p.lda : p.b + (int64_t)mr * p.ldb;
@@ -205,7 +233,7 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
     }
   };
   // The last tile's codes from the first chunk that is not whole on.
-  auto patch_tail = [&](int st) {
+  auto patch_tail = [&](int st) ORTHO_INLINE {
 #pragma unroll 1
     for (int x = t; x < (BM + BN) * 8; x += kThreads) {
       const int r = x >> 3, c = x & 7;
@@ -224,34 +252,32 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   const int s_shift = scales_a ? p.sa.shift : p.sb.shift;
   const int64_t s_ld = (scales_a ? p.sa.ld : p.sb.ld) * scale_size;
   const int s_first = (scales_a ? m0 : n0) >> s_shift;
-  const uint8_t* const s0 =
+  const uint8_t* s0 =
       uniform_ptr(static_cast<const uint8_t*>(scales_a ? p.sa.p : p.sb.p) + s_first * s_ld);
-  const int64_t s_off = ((matrix_row(wave * 64 + lane) >> s_shift) - s_first) * s_ld;
-  auto copy_scales = [&](int kt, int st) {
+  const int s_row = (matrix_row(wave * 64 + lane) >> s_shift) - s_first;
+  auto copy_scales = [&](int kt, int st) ORTHO_INLINE {
     const uint8_t* base = s0 + (int64_t)kt * scale_size;
     if constexpr (kDma) {
-      const unsigned at = scales0 + (st * (BM + BN) + wave * 64) * 4;
-      if (scale_size == 1) dma1(static_cast<unsigned>(s_off), base, at);
-      else dma4(static_cast<unsigned>(s_off), base, at);
+      const unsigned at = uniform(scales0 + (st * (BM + BN) + wave * 64) * 4);
+      base = uniform_ptr(base);
+      if (scale_size == 1) dma1(s_row * static_cast<unsigned>(s_ld), base, at);
+      else dma4(s_row * static_cast<unsigned>(s_ld), base, at);
     } else {
-      scales[st][wave * 64 + lane] = scale_size == 1 ? base[s_off] : *reinterpret_cast<const uint32_t*>(base + s_off);
+      base += s_row * s_ld;
+      scales[st][wave * 64 + lane] = scale_size == 1 ? *base : *reinterpret_cast<const uint32_t*>(base);
     }
   };
   // a scale as it was copied -> its value
-  auto scale_value = [&](uint32_t u) {
+  auto scale_value = [&](uint32_t u) ORTHO_INLINE {
     if (kMode == kExact && p.e8m0) u = u == 0 ? 0x00400000u : (u == 255 ? 0x7fc00000u : u << 23);
     return __uint_as_float(u);
   };
 
   floatx4 acc[kMI][kNJ];
-#pragma unroll
-  for (int i = 0; i < kMI; ++i)
-#pragma unroll
-    for (int j = 0; j < kNJ; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
   // 16 rows of 128 codes: lane l takes chunks l / 16 and l / 16 + 4 of its row
   // (the order of k within a block is free, if both operands share it)
-  auto chunks = [&](int row, int lo, int hi) {
+  auto chunks = [&](int row, int lo, int hi) ORTHO_INLINE {
     const uint4 x = *reinterpret_cast<const uint4*>(smem + row + lo);
     const uint4 y = *reinterpret_cast<const uint4*>(smem + row + hi);
     return intx8{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
@@ -262,8 +288,8 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   constexpr int kBStep = kBf ? 4 : 16;   // rows of B between fragments
   // rows 4 apart within 16 share a place (swz<true>), as rows 16 apart do (swz<false>)
   const int blo = (brow * 8 + swz<kBf>(brow, lg)) * 16, bhi = (brow * 8 + swz<kBf>(brow, lg + 4)) * 16;
-  auto frag_a = [&](int off) { return chunks(off, alo, ahi); };
-  auto frag_b = [&](int off) { return chunks(off, blo, bhi); };
+  auto frag_a = [&](int off) ORTHO_INLINE { return chunks(off, alo, ahi); };
+  auto frag_b = [&](int off) ORTHO_INLINE { return chunks(off, blo, bhi); };
   const int offa = wm * 128, offb = (BM + wn) * 128;
   const uint32_t* const my_sa = &scales[0][wm + l16];
   const uint32_t* const my_sb =
@@ -273,23 +299,58 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   bf16x8 xa[4], xb[kNJ][4];              // kExact: the fragments as bf16
   floatx4 sum[4];                        // block sums of the last slots,
   floatx4 factor[4];                     // and what they are multiplied by
-  float sa[kMI];
-  floatx4 sb[kRowB ? kNJ : 1];
-  int ea[kMI], eb[kNJ];                  // kHardware: scale bytes
+  uint32_t sa[2];                        // scales as they were copied: A's of the
+  floatx4 sb[kRowB ? kNJ : 1];           // 16 rows at hand, B's of the tile
+  int eb[kNJ];                           // (kHardware: bytes)
+  auto load_sb = [&](int j, int buf) ORTHO_INLINE {
+    if constexpr (kMode == kHardware) {
+      eb[j] = my_sb[buf * (BM + BN) + j * kBStep];
+    } else if constexpr (kRowB) {
+      const uint4 u = *reinterpret_cast<const uint4*>(my_sb + buf * (BM + BN) + j * kBStep);
+      sb[j] = floatx4{scale_value(u.x), scale_value(u.y), scale_value(u.z), scale_value(u.w)};
+    } else {
+      if (j == kNJ - 1) sb[0][0] = scale_value(my_sb[buf * (BM + BN)]);
+    }
+  };
 
   // The copies of a tile, in this order (the waits count them): scales, B, the
   // first half of A, the second half.
   constexpr int kPerTile = 1 + kCopies;
-  auto first_copies = [&](int kt, int st) {
+  auto first_copies = [&](int kt, int st) ORTHO_INLINE {
     copy_scales(kt, st);
 #pragma unroll
     for (int g = 0; g < kCopies; ++g) copy_group(g, kt, st);
   };
+  // The k tile to be copied next, two on from the one being computed.  kWhole:
+  // the next unit's follow this one's, so that its first tiles arrive under
+  // this one's last products and stores.
+  int ahead = kt_begin, ahead_end = kt_end, ahead_unit = unit;
+  bool more = true;
+  auto advance = [&]() ORTHO_INLINE {
+    if (++ahead < ahead_end) return;
+    if constexpr (!kWhole) {
+      more = false;
+    } else {
+      ahead_unit += run_step;
+      more = ahead_unit < run_end;
+      if (!more) return;
+      int m, n, sp;
+      place_unit(ahead_unit, m, n, sp);
+      a0 = uniform_ptr(p.a + (int64_t)m * p.lda);
+      b0 = uniform_ptr(p.b + (int64_t)n * p.ldb);
+      s0 = uniform_ptr(static_cast<const uint8_t*>(scales_a ? p.sa.p : p.sb.p) +
+                       ((scales_a ? m : n) >> s_shift) * s_ld);
+      ahead = sp * p.kchunk;
+      ahead_end = min(ahead + p.kchunk, nkb);
+    }
+  };
   if (kDma && kt_begin == tail_kt) tail_offsets();
-  first_copies(kt_begin, 0);
-  if (kt_begin + 1 < kt_end) {
-    if (kDma && kt_begin + 1 == tail_kt) tail_offsets();
-    first_copies(kt_begin + 1, 1);
+  first_copies(ahead, 0);
+  advance();
+  if (more) {
+    if (kDma && ahead == tail_kt) tail_offsets();
+    first_copies(ahead, 1);
+    advance();
     sync<kPerTile>();
   } else {
     sync<0>();
@@ -299,49 +360,49 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
     __syncthreads();
   }
   fa[0] = frag_a(offa);
+  sa[0] = my_sa[0];
 #pragma unroll
-  for (int j = 0; j < kNJ; ++j) fb[j] = frag_b(offb + j * kBStep * 128);
+  for (int j = 0; j < kNJ; ++j) {
+    fb[j] = frag_b(offb + j * kBStep * 128);
+    load_sb(j, 0);
+  }
+  // kWhole: the stores of a unit count among the outstanding accesses like
+  // copies; the three waits after them are for copies issued before them.
+  constexpr int kStores = kMI * (kBf ? 2 : 4);
+  int stores_ahead = 0;
+  int cur = 0, cur3 = 0;   // stage, and buffer of scales, of the k tile being computed
+
+  for (;;) {
+#pragma unroll
+  for (int i = 0; i < kMI; ++i)
+#pragma unroll
+    for (int j = 0; j < kNJ; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     sum[q] = floatx4{0.f, 0.f, 0.f, 0.f};
     factor[q] = floatx4{0.f, 0.f, 0.f, 0.f};
   }
-
-  for (int kt = kt_begin; kt < kt_end; ++kt) {
-    const int cur = (kt - kt_begin) & 1;
+  for (int kt = kt_begin; kt < kt_end; ++kt, cur ^= 1, cur3 = cur3 == 2 ? 0 : cur3 + 1) {
     const int here = cur * kStage, next = (cur ^ 1) * kStage;
-    const bool more = kt + 2 < kt_end;   // there is a tile after next
-    // this tile's scales
-    if constexpr (kMode == kHardware) {
-#pragma unroll
-      for (int i = 0; i < kMI; ++i) ea[i] = my_sa[cur * (BM + BN) + i * 16];
-#pragma unroll
-      for (int j = 0; j < kNJ; ++j) eb[j] = my_sb[cur * (BM + BN) + j * kBStep];
-    } else {
-#pragma unroll
-      for (int i = 0; i < kMI; ++i) sa[i] = scale_value(my_sa[cur * (BM + BN) + i * 16]);
-#pragma unroll
-      for (int j = 0; j < (kRowB ? kNJ : 1); ++j) {
-        if constexpr (kRowB) {
-          const uint4 u = *reinterpret_cast<const uint4*>(my_sb + cur * (BM + BN) + j * kBStep);
-          sb[j] = floatx4{scale_value(u.x), scale_value(u.y), scale_value(u.z), scale_value(u.w)};
-        } else {
-          sb[j][0] = scale_value(my_sb[cur * (BM + BN)]);
-        }
-      }
-    }
+    const int next3 = cur3 == 2 ? 0 : cur3 + 1, ahead3 = next3 == 2 ? 0 : next3 + 1;
 #pragma unroll
     for (int i = 0; i < kMI; ++i) {
       if (i == kM || i == kE) {
         // Since the copies that have to be here by now, one tile's worth was
         // issued; near the end there are fewer, and the wait is for all.
-        if (more) sync<kPerTile>();
-        else sync<0>();
+        if (!more) {
+          sync<0>();
+        } else if (kWhole && stores_ahead > 0) {
+          --stores_ahead;
+          sync<kPerTile + kStores>();
+        } else {
+          sync<kPerTile>();
+        }
         if (kDma && i == kE && kt + 1 == tail_kt && kt + 1 < kt_end) {
           patch_tail(cur ^ 1);
           __syncthreads();
         }
-        if (kDma && i == kM && kt + 2 == tail_kt && more) tail_offsets();
+        if (kDma && i == kM && more && ahead == tail_kt) tail_offsets();
       }
       if constexpr (kMode == kExact) {
 #pragma unroll
@@ -350,10 +411,13 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
 #pragma unroll
       for (int j = 0; j < kNJ; ++j) {
         const int slot = i * kNJ + j;
-        if (j == 0) fa[(i + 1) & 1] = frag_a(i + 1 < kMI ? here + offa + (i + 1) * 2048 : next + offa);
+        if (j == 0) {
+          fa[(i + 1) & 1] = frag_a(i + 1 < kMI ? here + offa + (i + 1) * 2048 : next + offa);
+          sa[(i + 1) & 1] = i + 1 < kMI ? my_sa[cur3 * (BM + BN) + (i + 1) * 16] : my_sa[next3 * (BM + BN)];
+        }
         if constexpr (kMode == kHardware) {
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i & 1], acc[i][j], 0, 0, 0,
-                                                                       eb[j], 0, ea[i]);
+                                                                       eb[j], 0, sa[i & 1]);
           const int ds = (slot + kSlots - 4) % kSlots;   // keeps the products in this order
           asm volatile("" : "+v"(acc[ds / kNJ][ds % kNJ]));
         } else {
@@ -380,25 +444,29 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
           sum[slot & 3] = s;
           if constexpr (kRowB) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) factor[slot & 3][e] = sa[i] * sb[j][e];
+            for (int e = 0; e < 4; ++e) factor[slot & 3][e] = scale_value(sa[i & 1]) * sb[j][e];
           } else {
-            factor[slot & 3][0] = sa[i] * sb[0][0];
+            factor[slot & 3][0] = scale_value(sa[i & 1]) * sb[0][0];
           }
         }
-        if (i == kE) fb[j] = frag_b(next + offb + j * kBStep * 128);
+        if (i == kE) {
+          fb[j] = frag_b(next + offb + j * kBStep * 128);
+          load_sb(j, next3);
+        }
         // the copies behind barrier M, one every second or third slot, and
         // those behind barrier E
         if (more) {
           constexpr int kStep = (kE - kM) * kNJ / (1 + kCopyB + kCopyA);
           const int x = slot - kM * kNJ;
           if (x >= 0 && x % kStep == 0 && x / kStep <= kCopyB + kCopyA) {
-            if (x == 0) copy_scales(kt + 2, cur);
-            else copy_group(x / kStep - 1, kt + 2, cur);
+            if (x == 0) copy_scales(ahead, ahead3);
+            else copy_group(x / kStep - 1, ahead, cur);
           }
           if (i == kE) {
 #pragma unroll
             for (int g = j * kCopyA / kNJ; g < (j + 1) * kCopyA / kNJ; ++g)
-              copy_group(kCopyB + kCopyA + g, kt + 2, cur);
+              copy_group(kCopyB + kCopyA + g, ahead, cur);
+            if (j == kNJ - 1) advance();
           }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -416,13 +484,13 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   }
 
   // Columns of piece j of a lane: four, next to those of piece j + 1 for bf16.
-  const bool whole = n0 + wn + 64 <= p.N && p.cvec;
+  const bool whole = kWhole || (n0 + wn + 64 <= p.N && p.cvec);
 #pragma unroll
   for (int i = 0; i < kMI; ++i) {
     const int m = m0 + wm + i * 16 + l16;
-    if (m >= p.M) continue;
+    if (!kWhole && m >= p.M) continue;
     const int nl = n0 + wn + lg * (kBf ? 16 : 4);
-    if (p.part) {
+    if (!kWhole && p.part) {
       float* o = p.part + ((int64_t)split * p.M + m) * p.N;
 #pragma unroll
       for (int j = 0; j < kNJ; ++j)
@@ -472,22 +540,42 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
       }
     }
   }
+  if constexpr (kWhole) {
+    stores_ahead = p.add ? 0 : 3;   // with Add its loads were waited for, and with them all before
+    unit += run_step;
+    if (unit >= run_end) return;
+    place_unit(unit, m0, n0, split);
+    kt_begin = split * p.kchunk;
+    kt_end = min(kt_begin + p.kchunk, nkb);
+  } else {
+    return;
+  }
+  }
 }
 
-template <int kMode, bool kRowB, int kWM, int kWN, int kMI, int kNJ, bool kDma>
+constexpr int kResident = 256;   // workgroups of eight waves that the chip holds at once
+
+template <int kMode, bool kRowB, int kWM, int kWN, int kMI, int kNJ, bool kDma, bool kWhole>
 void launch(const Fp8GemmArgs& a, hipStream_t s) {
   constexpr int BM = kWM * kMI * 16, BN = kWN * kNJ * 16;
-  const int64_t tiles = (int64_t)((a.N + BN - 1) / BN) * ((a.M + BM - 1) / BM);
-  hipLaunchKernelGGL((fp8_gemm_kernel<kMode, kRowB, kWM, kWN, kMI, kNJ, kDma>),
-                     dim3(static_cast<uint32_t>(tiles * a.splits)), dim3(kWM * kWN * 64), 0, s, a);
+  const int64_t units = (int64_t)((a.N + BN - 1) / BN) * ((a.M + BM - 1) / BM) * a.splits;
+  const int64_t grid = kWhole && units > kResident ? kResident : units;
+  hipLaunchKernelGGL((fp8_gemm_kernel<kMode, kRowB, kWM, kWN, kMI, kNJ, kDma, kWhole>),
+                     dim3(static_cast<uint32_t>(grid)), dim3(kWM * kWN * 64), 0, s, a);
 }
 
 template <int kMode, bool kRowB>
 void by_tile(const Fp8GemmArgs& a, hipStream_t s) {
   const bool dma = a.dma && a.K >= 16;
-  if (!dma) launch<kMode, kRowB, 2, 2, 4, 4, false>(a, s);
-  else if (kMode != kExact && (int64_t)a.M * a.N >= 256 * 256 * 128) launch<kMode, kRowB, 2, 4, 8, 4, true>(a, s);
-  else launch<kMode, kRowB, 2, 2, 4, 4, true>(a, s);
+  const bool whole = a.M % 256 == 0 && a.N % 256 == 0 && a.K % kFp8Block == 0 && a.cvec;
+  if (!dma) return launch<kMode, kRowB, 2, 2, 4, 4, false, false>(a, s);
+  if constexpr (kMode != kExact) {
+    if ((int64_t)a.M * a.N >= 256 * 256 * 128) {
+      if (whole) return launch<kMode, kRowB, 2, 4, 8, 4, true, true>(a, s);
+      return launch<kMode, kRowB, 2, 4, 8, 4, true, false>(a, s);
+    }
+  }
+  launch<kMode, kRowB, 2, 2, 4, 4, true, false>(a, s);
 }
 
 }  // namespace
