@@ -83,6 +83,8 @@ struct Fp8GemmArgs {
   int splits, kchunk;       // splits of K, blocks of 128 in each
   float* part;              // splits x M x N partial sums (splits > 1)
 };
+hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s);    // bf16 C
+hipError_t launch_fp8_exact(const Fp8GemmArgs& a, hipStream_t s);   // fp32 C
 hipError_t launch_fp8_matmul(const Fp8GemmArgs& a, bool c_bf, bool e8m0, hipStream_t s);
 
 // Scale of a block whose largest finite magnitude is `top`, and the factor

@@ -1,0 +1,89 @@
+// What the kernels of the 8-bit product share: matrix operand types, copies into
+// LDS, LDS places, conversion to bf16.
+#pragma once
+
+#include "fp8.h"
+
+namespace ortho {
+
+// The kernel's lambdas share its state by reference: inlined, it stays in registers.
+#define ORTHO_INLINE __attribute__((always_inline))
+
+typedef int intx8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+// Eight codes as eight bf16 (exact; the NaN code gives NaN).
+__device__ __forceinline__ bf16x8 codes_to_bf16(int lo, int hi) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Position of a 16-byte chunk in the 128-byte LDS row `row` of a tile, such that
+// the 16 rows of a fragment hit 64 distinct banks: rows r .. r + 15 of A (and of
+// B for an fp32 C), rows 16 (i / 4) + i % 4 + 4 j of B for a bf16 C.
+template <bool kSpread>
+__device__ __forceinline__ int swz(int row, int chunk) {
+  if constexpr (kSpread) return chunk ^ (((row >> 1) & 1) | ((row >> 3) & 6));
+  return chunk ^ ((row >> 1) & 7);
+}
+
+// 16 bytes per lane from global memory into LDS at lds + 16 * lane.  lds must
+// be wave-uniform.  The compiler does not look inside the assembly for
+// hazards, so it carries its own wait states: five before anything in it (a
+// vector instruction that wrote an SGPR the load reads needs five before a
+// vector memory instruction), and one between the M0 write and the load.  The
+// caller waits (vmcnt) before the LDS is read.
+__device__ __forceinline__ void dma16(unsigned voff, const uint8_t* sbase, unsigned lds) {
+  asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(voff), "s"(sbase), "s"(lds) : "memory");
+}
+
+// Four bytes, or one byte as a word, per lane into LDS at lds + 4 * lane.
+__device__ __forceinline__ void dma4(unsigned voff, const uint8_t* sbase, unsigned lds) {
+  asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :: "v"(voff), "s"(sbase), "s"(lds) : "memory");
+}
+__device__ __forceinline__ void dma1(unsigned voff, const uint8_t* sbase, unsigned lds) {
+  asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, %1"
+               :: "v"(voff), "s"(sbase), "s"(lds) : "memory");
+}
+
+// Waits until at most kOutstanding of the wave's copies are under way and its
+// LDS reads and writes are done, then for the workgroup.
+template <int kOutstanding>
+__device__ __forceinline__ void sync() {
+  static_assert(kOutstanding < 64, "");
+  asm volatile("" ::: "memory");
+  // vmcnt kOutstanding, expcnt off, lgkmcnt 0
+  __builtin_amdgcn_s_waitcnt((kOutstanding & 15) | (kOutstanding >> 4) << 14 | 7 << 4);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ unsigned uniform(unsigned x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return reinterpret_cast<const uint8_t*>((static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+// 16 codes from column k of a row; zero codes from column K on.  Any byte.
+__device__ __forceinline__ uint4 load_codes16(const uint8_t* row, int k, int K) {
+  uint4 u = make_uint4(0, 0, 0, 0);
+  if (k + 16 <= K) {
+    __builtin_memcpy(&u, row + k, 16);
+    return u;
+  }
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (k + j < K) w[j >> 2] |= static_cast<uint32_t>(row[k + j]) << (8 * (j & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+}  // namespace ortho

@@ -16,103 +16,22 @@
 // accumulates across blocks by itself.  With fp32 scales, and with the bf16
 // instruction, a block's sum starts at zero and joins the accumulators with
 // one fused multiply-add per element.
-#include "fp8.h"
+#include "fp8_gemm.h"
 
 namespace ortho {
 
 namespace {
 
-// The kernel's lambdas share its state by reference: inlined, it stays in registers.
-#define ORTHO_INLINE __attribute__((always_inline))
-
-typedef int intx8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
-
-enum { kScaled = 0, kHardware = 1, kExact = 2 };
-
-// Eight codes as eight bf16 (exact; the NaN code gives NaN).
-__device__ __forceinline__ bf16x8 codes_to_bf16(int lo, int hi) {
-  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false);
-  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
-  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false);
-  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
-  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
-// Position of a 16-byte chunk in the 128-byte LDS row `row` of a tile, such that
-// the 16 rows of a fragment hit 64 distinct banks: rows r .. r + 15 of A (and of
-// B for an fp32 C), rows 16 (i / 4) + i % 4 + 4 j of B for a bf16 C.
-template <bool kSpread>
-__device__ __forceinline__ int swz(int row, int chunk) {
-  if constexpr (kSpread) return chunk ^ (((row >> 1) & 1) | ((row >> 3) & 6));
-  return chunk ^ ((row >> 1) & 7);
-}
-
-// 16 bytes per lane from global memory into LDS at lds + 16 * lane.  lds must
-// be wave-uniform.  The compiler does not look inside the assembly for
-// hazards, so it carries its own wait states: five before anything in it (a
-// vector instruction that wrote an SGPR the load reads needs five before a
-// vector memory instruction), and one between the M0 write and the load.  The
-// caller waits (vmcnt) before the LDS is read.
-__device__ __forceinline__ void dma16(unsigned voff, const uint8_t* sbase, unsigned lds) {
-  asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :: "v"(voff), "s"(sbase), "s"(lds) : "memory");
-}
-
-// Four bytes, or one byte as a word, per lane into LDS at lds + 4 * lane.
-__device__ __forceinline__ void dma4(unsigned voff, const uint8_t* sbase, unsigned lds) {
-  asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
-               :: "v"(voff), "s"(sbase), "s"(lds) : "memory");
-}
-__device__ __forceinline__ void dma1(unsigned voff, const uint8_t* sbase, unsigned lds) {
-  asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, %1"
-               :: "v"(voff), "s"(sbase), "s"(lds) : "memory");
-}
-
-// Waits until at most kOutstanding of the wave's copies are under way and its
-// LDS reads and writes are done, then for the workgroup.
-template <int kOutstanding>
-__device__ __forceinline__ void sync() {
-  static_assert(kOutstanding < 64, "");
-  asm volatile("" ::: "memory");
-  // vmcnt kOutstanding, expcnt off, lgkmcnt 0
-  __builtin_amdgcn_s_waitcnt((kOutstanding & 15) | (kOutstanding >> 4) << 14 | 7 << 4);
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
-__device__ __forceinline__ unsigned uniform(unsigned x) { return __builtin_amdgcn_readfirstlane(x); }
-__device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
-  const uint64_t v = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
-  return reinterpret_cast<const uint8_t*>((static_cast<uint64_t>(hi) << 32) | lo);
-}
-
-// 16 codes from column k of a row; zero codes from column K on.  Any byte.
-__device__ __forceinline__ uint4 load_codes16(const uint8_t* row, int k, int K) {
-  uint4 u = make_uint4(0, 0, 0, 0);
-  if (k + 16 <= K) {
-    __builtin_memcpy(&u, row + k, 16);
-    return u;
-  }
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (k + j < K) w[j >> 2] |= static_cast<uint32_t>(row[k + j]) << (8 * (j & 3));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
+enum { kScaled = 0, kHardware = 1 };
 
 // A BM x BN tile of C per workgroup, kWM x kWN waves of (16 kMI) x 64.  The
 // rows of B are the matrix instruction's rows and the rows of A its columns, so
 // a lane holds four columns of one row of C per instruction and needs one scale
 // of A per 16 rows; the scale of a 128 x 128 block of B is the same for the
-// whole wave.  Which row of B is which row of instruction j is free: for a bf16
-// C, row 4 g + e is column 16 g + 4 j + e of the wave's 64, so that lane group
-// g ends up with 16 consecutive columns and stores them as two 16-byte pieces;
-// for an fp32 C it is column 16 j + 4 g + e, four 16-byte pieces of which the
-// lane groups' lie side by side.  C is written straight from the accumulators:
+// whole wave.  Which row of B is which row of instruction j is free: row
+// 4 g + e is column 16 g + 4 j + e of the wave's 64, so that lane group g ends
+// up with 16 consecutive columns and stores them as two 16-byte pieces.  C is
+// written straight from the accumulators:
 // the LDS is free at once for the next workgroup, whose first copies overlap
 // the stores.
 //
@@ -139,7 +58,6 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   // 8-row copies per wave and tile: B's, the first half of A's rows, the second
   constexpr int kCopyB = BN / 8 / kWaves, kCopyA = BM / 16 / kWaves, kCopies = kCopyB + 2 * kCopyA;
   constexpr int kM = kMI / 2 - 1, kE = kMI - 1;   // groups of products behind the barriers
-  constexpr bool kBf = kMode != kExact;
   static_assert(kSlots % 4 == 0 && kNJ == 4, "");
   static_assert(kThreads == BM + BN && kCopyB * kWaves * 8 == BN && kCopyA * kWaves * 16 == BM, "");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
@@ -180,7 +98,7 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
     return x / (8 * kMI) * (16 * kMI) + half * (8 * kMI) + x % (8 * kMI);
   };
   auto row_of = [&](int g) ORTHO_INLINE { return rows8(g) + (lane >> 3); };
-  auto place = [&](int r, int c) ORTHO_INLINE { return r < BM ? swz<false>(r, c) : swz<kBf>(r - BM, c); };
+  auto place = [&](int r, int c) ORTHO_INLINE { return r < BM ? swz<false>(r, c) : swz<true>(r - BM, c); };
   auto chunk_of = [&](int g) ORTHO_INLINE { return place(row_of(g), lane & 7); };
   auto matrix_row = [&](int r) ORTHO_INLINE {
     if (kWhole) return r < BM ? m0 + r : n0 + r - BM;
@@ -191,7 +109,7 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   // the 8 rows is uniform); otherwise rows past the matrix are the last row.
   const int sub = lane >> 3;
   const unsigned row_a = sub * static_cast<unsigned>(p.lda), row_b = sub * static_cast<unsigned>(p.ldb);
-  const unsigned chunk_a = swz<false>(sub, lane & 7) * 16, chunk_b = swz<kBf>(sub, lane & 7) * 16;
+  const unsigned chunk_a = swz<false>(sub, lane & 7) * 16, chunk_b = swz<true>(sub, lane & 7) * 16;
   unsigned voff[kWhole ? 1 : kCopies];
   if constexpr (!kWhole) {
 #pragma unroll
@@ -219,7 +137,7 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
     const bool is_a = g >= kCopyB;
     const unsigned at = uniform(lds0 + st * kStage + r8 * 128);
     if constexpr (kDma && kWhole) {
-      const unsigned key = is_a ? swz<false>(r8, 0) : swz<kBf>(r8 - BM, 0);
+      const unsigned key = is_a ? swz<false>(r8, 0) : swz<true>(r8 - BM, 0);
       const uint8_t* base = (is_a ? a0 + r8 * p.lda : b0 + (r8 - BM) * p.ldb) + (int64_t)kt * 128;
       dma16((is_a ? row_a : row_b) + ((is_a ? chunk_a : chunk_b) ^ (key * 16)), uniform_ptr(base), at);
     } else if constexpr (kDma) {
@@ -247,7 +165,7 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
 
   // scales: the wave's 64 rows of the stage, one per lane (bytes as words)
   constexpr bool kByteOnly = kMode == kHardware;
-  const int scale_size = kByteOnly || (kMode == kExact && p.e8m0) ? 1 : 4;
+  constexpr int scale_size = kByteOnly ? 1 : 4;
   const bool scales_a = wave * 64 < BM;
   const int s_shift = scales_a ? p.sa.shift : p.sb.shift;
   const int64_t s_ld = (scales_a ? p.sa.ld : p.sb.ld) * scale_size;
@@ -267,11 +185,6 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
       scales[st][wave * 64 + lane] = scale_size == 1 ? *base : *reinterpret_cast<const uint32_t*>(base);
     }
   };
-  // a scale as it was copied -> its value
-  auto scale_value = [&](uint32_t u) ORTHO_INLINE {
-    if (kMode == kExact && p.e8m0) u = u == 0 ? 0x00400000u : (u == 255 ? 0x7fc00000u : u << 23);
-    return __uint_as_float(u);
-  };
 
   floatx4 acc[kMI][kNJ];
 
@@ -284,19 +197,17 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   };
   const int l16 = lane & 15, lg = lane >> 4;
   const int alo = (l16 * 8 + swz<false>(l16, lg)) * 16, ahi = (l16 * 8 + swz<false>(l16, lg + 4)) * 16;
-  const int brow = kBf ? l16 / 4 * 16 + l16 % 4 : l16;
-  constexpr int kBStep = kBf ? 4 : 16;   // rows of B between fragments
-  // rows 4 apart within 16 share a place (swz<true>), as rows 16 apart do (swz<false>)
-  const int blo = (brow * 8 + swz<kBf>(brow, lg)) * 16, bhi = (brow * 8 + swz<kBf>(brow, lg + 4)) * 16;
+  const int brow = l16 / 4 * 16 + l16 % 4;
+  constexpr int kBStep = 4;   // rows of B between fragments (rows 4 apart within 16 share a place)
+  const int blo = (brow * 8 + swz<true>(brow, lg)) * 16, bhi = (brow * 8 + swz<true>(brow, lg + 4)) * 16;
   auto frag_a = [&](int off) ORTHO_INLINE { return chunks(off, alo, ahi); };
   auto frag_b = [&](int off) ORTHO_INLINE { return chunks(off, blo, bhi); };
   const int offa = wm * 128, offb = (BM + wn) * 128;
   const uint32_t* const my_sa = &scales[0][wm + l16];
   const uint32_t* const my_sb =
-      &scales[0][BM + wn + (kMode == kHardware ? brow : (kRowB ? lg * (kBf ? 16 : 4) : 0))];
+      &scales[0][BM + wn + (kMode == kHardware ? brow : (kRowB ? lg * 16 : 0))];
 
   intx8 fa[2], fb[kNJ];
-  bf16x8 xa[4], xb[kNJ][4];              // kExact: the fragments as bf16
   floatx4 sum[4];                        // block sums of the last slots,
   floatx4 factor[4];                     // and what they are multiplied by
   uint32_t sa[2];                        // scales as they were copied: A's of the
@@ -307,9 +218,9 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
       eb[j] = my_sb[buf * (BM + BN) + j * kBStep];
     } else if constexpr (kRowB) {
       const uint4 u = *reinterpret_cast<const uint4*>(my_sb + buf * (BM + BN) + j * kBStep);
-      sb[j] = floatx4{scale_value(u.x), scale_value(u.y), scale_value(u.z), scale_value(u.w)};
+      sb[j] = floatx4{__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
     } else {
-      if (j == kNJ - 1) sb[0][0] = scale_value(my_sb[buf * (BM + BN)]);
+      if (j == kNJ - 1) sb[0][0] = __uint_as_float(my_sb[buf * (BM + BN)]);
     }
   };
 
@@ -368,7 +279,7 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   }
   // kWhole: the stores of a unit count among the outstanding accesses like
   // copies; the three waits after them are for copies issued before them.
-  constexpr int kStores = kMI * (kBf ? 2 : 4);
+  constexpr int kStores = kMI * 2;
   int stores_ahead = 0;
   int cur = 0, cur3 = 0;   // stage, and buffer of scales, of the k tile being computed
 
@@ -404,10 +315,6 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
         }
         if (kDma && i == kM && more && ahead == tail_kt) tail_offsets();
       }
-      if constexpr (kMode == kExact) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) xa[q] = codes_to_bf16(fa[i & 1][2 * q], fa[i & 1][2 * q + 1]);
-      }
 #pragma unroll
       for (int j = 0; j < kNJ; ++j) {
         const int slot = i * kNJ + j;
@@ -422,17 +329,7 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
           asm volatile("" : "+v"(acc[ds / kNJ][ds % kNJ]));
         } else {
           floatx4 s = {0.f, 0.f, 0.f, 0.f};
-          if constexpr (kMode == kScaled) {
-            s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i & 1], s, 0, 0, 0, 0, 0, 0);
-          } else {
-            if (i == 0) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) xb[j][q] = codes_to_bf16(fb[j][2 * q], fb[j][2 * q + 1]);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[j][q], xa[q], s, 0, 0, 0);
-          }
+          s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i & 1], s, 0, 0, 0, 0, 0, 0);
           // the sum of two slots ago joins its accumulators (pinned here: left
           // alone, the compiler gathers the additions at the tile's end and
           // keeps every sum alive until then)
@@ -444,9 +341,9 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
           sum[slot & 3] = s;
           if constexpr (kRowB) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) factor[slot & 3][e] = scale_value(sa[i & 1]) * sb[j][e];
+            for (int e = 0; e < 4; ++e) factor[slot & 3][e] = __uint_as_float(sa[i & 1]) * sb[j][e];
           } else {
-            factor[slot & 3][0] = scale_value(sa[i & 1]) * sb[0][0];
+            factor[slot & 3][0] = __uint_as_float(sa[i & 1]) * sb[0][0];
           }
         }
         if (i == kE) {
@@ -489,7 +386,7 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   for (int i = 0; i < kMI; ++i) {
     const int m = m0 + wm + i * 16 + l16;
     if (!kWhole && m >= p.M) continue;
-    const int nl = n0 + wn + lg * (kBf ? 16 : 4);
+    const int nl = n0 + wn + lg * 16;
     if (!kWhole && p.part) {
       float* o = p.part + ((int64_t)split * p.M + m) * p.N;
 #pragma unroll
@@ -510,33 +407,18 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
         acc[i][j][0] += ad.x; acc[i][j][1] += ad.y; acc[i][j][2] += ad.z; acc[i][j][3] += ad.w;
       }
     }
-    if constexpr (kBf) {
-      uint16_t* o = static_cast<uint16_t*>(p.c) + m * p.ldc;
+    uint16_t* o = static_cast<uint16_t*>(p.c) + m * p.ldc;
 #pragma unroll
-      for (int j = 0; j < kNJ; j += 2) {
-        const uint2 lo = pack_bf16x4(acc[i][j]), hi = pack_bf16x4(acc[i][j + 1]);
-        const int n = nl + j * 4;
-        if (whole) {
-          *reinterpret_cast<uint4*>(o + n) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-        } else {
-          const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
+    for (int j = 0; j < kNJ; j += 2) {
+      const uint2 lo = pack_bf16x4(acc[i][j]), hi = pack_bf16x4(acc[i][j + 1]);
+      const int n = nl + j * 4;
+      if (whole) {
+        *reinterpret_cast<uint4*>(o + n) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      } else {
+        const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (n + e < p.N) o[n + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
-        }
-      }
-    } else {
-      float* o = static_cast<float*>(p.c) + m * p.ldc;
-#pragma unroll
-      for (int j = 0; j < kNJ; ++j) {
-        const int n = nl + j * 16;
-        if (whole) {
-          *reinterpret_cast<floatx4*>(o + n) = acc[i][j];
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n + e < p.N) o[n + e] = acc[i][j][e];
-        }
+        for (int e = 0; e < 8; ++e)
+          if (n + e < p.N) o[n + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
       }
     }
   }
@@ -566,19 +448,23 @@ void launch(const Fp8GemmArgs& a, hipStream_t s) {
 
 template <int kMode, bool kRowB>
 void by_tile(const Fp8GemmArgs& a, hipStream_t s) {
-  const bool dma = a.dma && a.K >= 16;
   const bool whole = a.M % 256 == 0 && a.N % 256 == 0 && a.K % kFp8Block == 0 && a.cvec;
-  if (!dma) return launch<kMode, kRowB, 2, 2, 4, 4, false, false>(a, s);
-  if constexpr (kMode != kExact) {
-    if ((int64_t)a.M * a.N >= 256 * 256 * 128) {
-      if (whole) return launch<kMode, kRowB, 2, 4, 8, 4, true, true>(a, s);
-      return launch<kMode, kRowB, 2, 4, 8, 4, true, false>(a, s);
-    }
+  if (!a.dma || a.K < 16) return launch<kMode, kRowB, 2, 2, 4, 4, false, false>(a, s);
+  if ((int64_t)a.M * a.N >= 256 * 256 * 128) {
+    if (whole) return launch<kMode, kRowB, 2, 4, 8, 4, true, true>(a, s);
+    return launch<kMode, kRowB, 2, 4, 8, 4, true, false>(a, s);
   }
   launch<kMode, kRowB, 2, 2, 4, 4, true, false>(a, s);
 }
 
 }  // namespace
+
+hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s) {
+  if (a.e8m0) by_tile<kHardware, false>(a, s);
+  else if (a.sb.shift == 0) by_tile<kScaled, true>(a, s);
+  else by_tile<kScaled, false>(a, s);
+  return hipGetLastError();
+}
 
 hipError_t launch_fp8_matmul(const Fp8GemmArgs& a0, bool c_bf, bool e8m0, hipStream_t s) {
   Fp8GemmArgs a = a0;
@@ -586,17 +472,7 @@ hipError_t launch_fp8_matmul(const Fp8GemmArgs& a0, bool c_bf, bool e8m0, hipStr
   a.splits = 1;
   a.part = nullptr;
   a.kchunk = (a.K + kFp8Block - 1) / kFp8Block;
-  const bool row_b = a.sb.shift == 0;
-  if (!c_bf) {
-    if (row_b) by_tile<kExact, true>(a, s);
-    else by_tile<kExact, false>(a, s);
-  } else if (e8m0) {
-    by_tile<kHardware, false>(a, s);
-  } else {
-    if (row_b) by_tile<kScaled, true>(a, s);
-    else by_tile<kScaled, false>(a, s);
-  }
-  return hipGetLastError();
+  return c_bf ? launch_fp8_gemm(a, s) : launch_fp8_exact(a, s);
 }
 
 }  // namespace ortho

@@ -272,6 +272,32 @@ def test_matmul(m, n, k, scale):
         check_product(c, want, mags, k, add, tops)
 
 
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("m,n,k", [
+    (4352, 4096, 384),    # whole 256 x 256 tiles, more than there are CUs
+    (4096, 4352, 128),    # the same with one block of k
+    (2048, 4096, 640),    # whole tiles, fewer than there are CUs
+    (3000, 2900, 300),    # large and ragged
+    (16384, 520, 272),
+])
+def test_matmul_large(m, n, k, scale):
+    """The large tiles, and their walk over several of C; references summed in
+    float64 on the GPU."""
+    for bra, brb, with_add in ((1, 128, False), (1, 1, True)):
+        a, sa = codes_and_scales(m + k, m, k, bra, scale)
+        b, sb = codes_and_scales(n + 2 * k, n, k, brb, scale)
+        add = normal(9, m, n, "bf16") if with_add else None
+        note(f"fp8_matmul {m}x{n}x{k} {scale} blocks {bra}/{brb} bf16 add={with_add}")
+        args = upload(a), sa.cuda(), upload(b), sb.cuda()
+        c = api.fp8_matmul(*args, add=None if add is None else add.cuda())
+        torch.cuda.synchronize()
+        want, mags = matmul_reference(a, sa, bra, b, sb, brb)
+        check_product(c, want, mags, k, add, group_tops(a, sa, bra, b, sb, brb))
+        again = api.fp8_matmul(*args, add=None if add is None else add.cuda())
+        torch.cuda.synchronize()
+        assert torch.equal(c, again)
+
+
 @pytest.mark.parametrize("m,n,k,extra,offset", [(5, 300, 260, 3, 1), (130, 200, 385, 16, 0),
                                                 (130, 200, 384, 16, 5), (300, 257, 511, 1, 0),
                                                 (20, 640, 1024, 16, 16), (260, 260, 200, 8, 0)])
