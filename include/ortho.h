@@ -322,7 +322,7 @@ ortho_status fp8_quantize(ortho_mat X, int32_t block_rows, const ortho_mat* Q, c
  *     r = X + Res, rounded to X's dtype
  *     y = r / sqrt(mean(r^2) + eps) * W        row by row, in fp32
  *     Q, S = the codes and scales of y (as fp8_quantize)
- *   X     m x n, ORTHO_F32 or ORTHO_BF16; n <= 65536.
+ *   X     m x n, ORTHO_F32 or ORTHO_BF16; n <= 32768.
  *   Res   NULL (r = X), or m x n of X's dtype.
  *   W     1 x n, ORTHO_F32 or X's dtype.
  *   eps   >= 0 and finite, else ORTHO_E_PARAM.

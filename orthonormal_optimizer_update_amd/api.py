@@ -341,27 +341,30 @@ def _mats(*tensors):
         import torch
         _DTYPES = {torch.float32: ORTHO_F32, torch.bfloat16: ORTHO_BF16,
                    torch.float8_e4m3fn: ORTHO_E4M3, torch.float8_e8m0fnu: ORTHO_E8M0}
-    out, device = [], tensors[0].device
-    if device.type != "cuda":
-        raise ValueError(f"expected tensors on a GPU, got {device}")
+    dtypes, device, out = _DTYPES, tensors[0].get_device(), []
+    if device < 0:
+        raise ValueError(f"expected tensors on a GPU, got {tensors[0].device}")
     for t in tensors:
         if t is None:
             out.append(None)
             continue
-        if t.device != device:
-            raise ValueError(f"expected every tensor on {device}, got {t.device}")
-        if t.dim() != 2:
+        if t.get_device() != device:
+            raise ValueError(f"expected every tensor on {tensors[0].device}, got {t.device}")
+        shape = t.shape
+        if len(shape) != 2:
             raise ValueError("expected a 2-D tensor")
-        rows, cols = t.shape
+        rows, cols = shape
         ld, step = t.stride()
-        if cols > 1 and step != 1:
+        if step != 1 and cols > 1:
             raise ValueError("expected unit stride along columns")
-        if rows > 1 and ld < cols:
+        if rows <= 1:
+            ld = cols
+        elif ld < cols:
             raise ValueError("expected rows that do not overlap")
-        dt = _DTYPES.get(t.dtype)
+        dt = dtypes.get(t.dtype)
         if dt is None:
             raise ValueError(f"unsupported dtype {t.dtype}")
-        out.append(OrthoMat(t.data_ptr(), rows, cols, ld if rows > 1 else cols, dt))
+        out.append(OrthoMat(t.data_ptr(), rows, cols, ld, dt))
     return out
 
 
@@ -369,15 +372,24 @@ def _ref(m):
     return None if m is None else ctypes.byref(m)
 
 
-def _call(fn: str, device, *args):
-    """The library call on `device`'s current stream, with `device` current."""
+def _call(fn: str, t, *args):
+    """The library call on the current stream of t's device, with that device
+    current."""
     import torch
-    if device.index == torch.cuda.current_device():
-        status = getattr(lib(), fn)(*args, _stream_ptr(device))
+    device = t.get_device()
+    if device == torch.cuda.current_device():
+        status = getattr(lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
-            status = getattr(lib(), fn)(*args, _stream_ptr(device))
-    _check(fn, status)
+            status = getattr(lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(device))
+    if status != 0:
+        _check(fn, status)
+
+
+def _check_ws(ws, t):
+    if ws.get_device() != t.get_device():
+        raise ValueError(f"expected a workspace on {t.device}, got {ws.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _blocks(n: int) -> int:
@@ -413,7 +425,7 @@ def fp8_quantize(X, Q=None, S=None, QT=None, ST=None, block_rows: int = 1, scale
             QT = fp8_codes(n, m, X.device)
             ST = fp8_scales(n, m, X.device, block_rows, scale_dtype)
     x, q, s, qt, st = _mats(X, Q, S, QT, ST)
-    _call("fp8_quantize", X.device, x, block_rows, _ref(q), _ref(s), _ref(qt), _ref(st))
+    _call("fp8_quantize", X, x, block_rows, _ref(q), _ref(s), _ref(qt), _ref(st))
     return Q, S, QT, ST
 
 
@@ -427,7 +439,7 @@ def rms_norm_fp8(X, W, Q=None, S=None, eps: float = 1e-6, residual=None, sum_out
     if S is None:
         S = fp8_scales(X.size(0), X.size(1), X.device, 1, scale_dtype)
     x, res, w, total, y, q, s = _mats(X, residual, W, sum_out, y_out, Q, S)
-    _call("rms_norm_fp8", X.device, x, _ref(res), w, eps, _ref(total), _ref(y), q, s)
+    _call("rms_norm_fp8", X, x, _ref(res), w, eps, _ref(total), _ref(y), q, s)
     return Q, S
 
 
@@ -446,7 +458,7 @@ def rms_norm_backward(dY, X, W, dX=None, dW=None, eps: float = 1e-6, dsum=None, 
     if ws is None:
         ws = workspace(rms_norm_backward_workspace_size(X.size(0), X.size(1)), X.device)
     dy, x, w, ds, dx, dw = _mats(dY, X, W, dsum, dX, dW)
-    _call("rms_norm_backward", X.device, dy, x, w, eps, _ref(ds), dx, dw, _ptr(ws), ws.numel())
+    _call("rms_norm_backward", X, dy, x, w, eps, _ref(ds), dx, dw, *_check_ws(ws, X))
     return dX, dW
 
 
@@ -465,5 +477,5 @@ def fp8_matmul(A, SA, B, SB, out=None, add=None, ws=None, out_dtype=None):
     if ws is None:
         ws = workspace(fp8_matmul_workspace_size(A.size(0), B.size(0), A.size(1)), A.device)
     a, sa, b, sb, c, ad = _mats(A, SA, B, SB, out, add)
-    _call("fp8_matmul", A.device, a, sa, b, sb, c, _ref(ad), _ptr(ws), ws.numel())
+    _call("fp8_matmul", A, a, sa, b, sb, c, _ref(ad), *_check_ws(ws, A))
     return out

@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libortho.so")
 
 SOURCES = ["kernels_gemm.hip", "kernels_aux.hip", "kernels_stream.hip", "kernels_gram_ns.hip",
            "kernels_sweep.hip", "kernels_dion2.hip", "kernels_fp8_gemm.hip", "kernels_fp8_exact.hip",
-           "kernels_fp8_rows.hip",
+           "kernels_fp8_few.hip", "kernels_fp8_rows.hip",
            "noalloc.hip", "abi.cpp", "abi_fp8.cpp", "plan.cpp"]
 
 COMMON_FLAGS = [

@@ -64,6 +64,7 @@ ortho_status rms_norm_fp8(ortho_mat X, const ortho_mat* Res, ortho_mat W, float 
   a.ldres = ld_of(Res);
   a.w = W.data;
   a.w_bf = W.dtype == ORTHO_BF16;
+  a.wvec = reinterpret_cast<uintptr_t>(W.data) % 16 == 0;
   a.sum = data_of(Sum);
   a.ldsum = ld_of(Sum);
   a.y = data_of(Y);
@@ -99,12 +100,14 @@ ortho_status rms_norm_backward(ortho_mat dY, ortho_mat X, ortho_mat W, float eps
   a.ldx = X.ld;
   a.w = W.data;
   a.w_bf = W.dtype == ORTHO_BF16;
+  a.wvec = reinterpret_cast<uintptr_t>(W.data) % 16 == 0;
   a.dsum = data_of(dSum);
   a.lddsum = ld_of(dSum);
   a.dx = dX.data;
   a.lddx = dX.ld;
   a.dw = static_cast<float*>(dW.data);
   a.part = static_cast<float*>(ws);
+  a.ldpart = plan.ld;
   a.eps = eps;
   a.m = static_cast<int>(X.rows);
   a.n = static_cast<int>(X.cols);

@@ -49,7 +49,7 @@ struct NormArgs {
   int m, n;
   int vec;                  // x, res, sum, y rows of 16-byte multiples
   int qvec;                 // q rows of 8-byte multiples
-  int w_bf;                 // W is bf16
+  int w_bf, wvec;           // W is bf16; 16-byte aligned
 };
 hipError_t launch_rms_norm_fp8(const NormArgs& a, bool bf, bool e8m0, hipStream_t s);
 
@@ -59,11 +59,12 @@ struct NormGradArgs {
   void* dx;
   int64_t lddx;
   float* dw;
-  float* part;              // groups x n partial sums of dw
+  float* part;              // groups x n partial sums of dw, rows of ldpart (multiple of 8)
+  int64_t ldpart;
   float eps;
   int m, n, groups;
   int vec;
-  int w_bf;
+  int w_bf, wvec;
 };
 hipError_t launch_rms_norm_backward(const NormGradArgs& a, bool bf, hipStream_t s);
 
@@ -79,10 +80,12 @@ struct Fp8GemmArgs {
   int M, N, K;
   int dma;                  // A's and B's rows at multiples of 16 bytes, 256 of them within 2 GiB
   // set by the launcher
-  int e8m0;
+  int e8m0, c_bf;
   int splits, kchunk;       // splits of K, blocks of 128 in each
   float* part;              // splits x M x N partial sums (splits > 1)
 };
+constexpr int kFewRows = 64;         // rows of A up to which launch_fp8_few takes the product
+hipError_t launch_fp8_few(const Fp8GemmArgs& a, hipStream_t s);     // M <= kFewRows
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s);    // bf16 C
 hipError_t launch_fp8_exact(const Fp8GemmArgs& a, hipStream_t s);   // fp32 C
 hipError_t launch_fp8_matmul(const Fp8GemmArgs& a, bool c_bf, bool e8m0, hipStream_t s);

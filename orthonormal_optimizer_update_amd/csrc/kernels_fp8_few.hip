@@ -1,0 +1,113 @@
+// The 8-bit product for few rows of A (a decoding step's tokens): bound by
+// reading B once.
+#include <type_traits>
+
+#include "fp8_gemm.h"
+
+namespace ortho {
+
+namespace {
+
+// 16 rows of B per workgroup against 16 kMB rows of A.  The kWaves waves share
+// the blocks of K among them (block b goes to wave b % kWaves), hold kAhead
+// blocks' loads in flight straight from memory into registers, and their sums
+// are added in LDS in a fixed order.  Codes become bf16, which holds them
+// exactly, whatever C's type: at this size the conversions are free.
+template <bool kE8m0, int kMB, int kWaves, int kAhead>
+__global__ __launch_bounds__(kWaves * 64) void fp8_few_kernel(Fp8GemmArgs p) {
+  __shared__ __attribute__((aligned(16))) float part[kWaves][kMB][16][20];   // [m][n], rows 16 bytes apart in banks
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l16 = lane & 15, lg = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const int nkb = (p.K + kFp8Block - 1) / kFp8Block;
+  // Lane l holds codes 16 lg .. and 64 + 16 lg .. of row l16 of a block (the
+  // order of k within a block is free).
+  const uint8_t* const brow = p.b + (int64_t)min(n0 + l16, p.N - 1) * p.ldb;
+  floatx4 acc[kMB];
+#pragma unroll
+  for (int i = 0; i < kMB; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+  for (int b0 = wave; b0 < nkb; b0 += kWaves * kAhead) {
+    uint4 rb[kAhead][2], ra[kAhead][kMB][2];
+    float sa[kAhead][kMB], sb[kAhead][4];
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const int kb = b0 + x * kWaves, k = kb * 128 + lg * 16, ks = min(kb, nkb - 1);
+      rb[x][0] = load_codes16(brow, k, p.K);
+      rb[x][1] = load_codes16(brow, k + 64, p.K);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t r = min(n0 + lg * 4 + e, p.N - 1) >> p.sb.shift;
+        sb[x][e] = load_scale<kE8m0>(p.sb.p, r * p.sb.ld + ks);
+      }
+#pragma unroll
+      for (int i = 0; i < kMB; ++i) {
+        const int m = min(i * 16 + l16, p.M - 1);
+        ra[x][i][0] = load_codes16(p.a + m * p.lda, k, p.K);
+        ra[x][i][1] = load_codes16(p.a + m * p.lda, k + 64, p.K);
+        sa[x][i] = load_scale<kE8m0>(p.sa.p, (m >> p.sa.shift) * p.sa.ld + ks);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      if (b0 + x * kWaves >= nkb) break;
+#pragma unroll
+      for (int i = 0; i < kMB; ++i) {
+        floatx4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 ub = rb[x][h], ua = ra[x][i][h];
+          s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(ub.x, ub.y), codes_to_bf16(ua.x, ua.y), s, 0, 0, 0);
+          s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(ub.z, ub.w), codes_to_bf16(ua.z, ua.w), s, 0, 0, 0);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(s[e], sa[x][i] * sb[x][e], acc[i][e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kMB; ++i) *reinterpret_cast<floatx4*>(&part[wave][i][l16][lg * 4]) = acc[i];
+  __syncthreads();
+  for (int x = threadIdx.x; x < kMB * 256; x += kWaves * 64) {
+    const int i = x >> 8, m = (x >> 4) & 15, n = x & 15;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) v += part[w][i][m][n];
+    const int64_t row = i * 16 + m;
+    if (row >= p.M || n0 + n >= p.N) continue;
+    if (p.add)
+      v += p.add_bf ? bf16_bits_to_f32(static_cast<const uint16_t*>(p.add)[row * p.ldadd + n0 + n])
+                    : static_cast<const float*>(p.add)[row * p.ldadd + n0 + n];
+    if (p.c_bf) static_cast<uint16_t*>(p.c)[row * p.ldc + n0 + n] = to_bf16_bits(v);
+    else static_cast<float*>(p.c)[row * p.ldc + n0 + n] = v;
+  }
+}
+
+template <bool kE8m0, int kMB, int kAhead>
+void by_depth(const Fp8GemmArgs& a, hipStream_t s) {
+  // one wave for every kAhead blocks of K, 4 to 16
+  const dim3 grid((a.N + 15) / 16);
+  const int nkb = (a.K + kFp8Block - 1) / kFp8Block;
+  if (nkb <= 4 * kAhead)
+    hipLaunchKernelGGL((fp8_few_kernel<kE8m0, kMB, 4, kAhead>), grid, dim3(256), 0, s, a);
+  else if (nkb <= 8 * kAhead)
+    hipLaunchKernelGGL((fp8_few_kernel<kE8m0, kMB, 8, kAhead>), grid, dim3(512), 0, s, a);
+  else
+    hipLaunchKernelGGL((fp8_few_kernel<kE8m0, kMB, 16, kAhead>), grid, dim3(1024), 0, s, a);
+}
+
+template <bool kE8m0>
+void by_rows(const Fp8GemmArgs& a, hipStream_t s) {
+  if (a.M <= 16) by_depth<kE8m0, 1, 4>(a, s);
+  else if (a.M <= 32) by_depth<kE8m0, 2, 2>(a, s);
+  else by_depth<kE8m0, 4, 1>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_fp8_few(const Fp8GemmArgs& a, hipStream_t s) {
+  if (a.e8m0) by_rows<true>(a, s);
+  else by_rows<false>(a, s);
+  return hipGetLastError();
+}
+
+}  // namespace ortho

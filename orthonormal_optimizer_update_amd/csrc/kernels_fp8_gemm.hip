@@ -469,9 +469,11 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s) {
 hipError_t launch_fp8_matmul(const Fp8GemmArgs& a0, bool c_bf, bool e8m0, hipStream_t s) {
   Fp8GemmArgs a = a0;
   a.e8m0 = e8m0;
+  a.c_bf = c_bf;
   a.splits = 1;
   a.part = nullptr;
   a.kchunk = (a.K + kFp8Block - 1) / kFp8Block;
+  if (a.M <= kFewRows) return launch_fp8_few(a, s);
   return c_bf ? launch_fp8_gemm(a, s) : launch_fp8_exact(a, s);
 }
 

@@ -148,154 +148,235 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
   }
 }
 
-// Sum over the workgroup in a fixed order; every thread gets the total.
+// Sums of two values over the workgroup in a fixed order; every thread gets
+// the totals.  One barrier: calls alternate between two buffers.
 template <int kThreads>
-__device__ __forceinline__ float block_sum(float v, float* red) {
+__device__ __forceinline__ void block_sum2(float& x, float& y, float (*red)[2][kThreads / 64], int turn) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  if constexpr (kThreads == 64) return v;
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float total = 0.f;
+  for (int o = 32; o > 0; o >>= 1) {
+    x += __shfl_xor(x, o, 64);
+    y += __shfl_xor(y, o, 64);
+  }
+  if constexpr (kThreads > 64) {
+    if ((threadIdx.x & 63) == 0) {
+      red[turn][0][threadIdx.x >> 6] = x;
+      red[turn][1][threadIdx.x >> 6] = y;
+    }
+    __syncthreads();
+    x = y = 0.f;
 #pragma unroll
-  for (int w = 0; w < kThreads / 64; ++w) total += red[w];
-  return total;
+    for (int w = 0; w < kThreads / 64; ++w) {
+      x += red[turn][0][w];
+      y += red[turn][1][w];
+    }
+  }
 }
 
-__device__ __forceinline__ void load_w8(const void* w, int w_bf, int c, int n, float (&v)[8]) {
-  if (w_bf) load8<uint16_t>(static_cast<const uint16_t*>(w), c, n, false, v);
-  else load8<float>(static_cast<const float*>(w), c, n, false, v);
+__device__ __forceinline__ void load_w8(const void* w, int w_bf, int c, int n, bool vec, float (&v)[8]) {
+  if (w_bf) load8<uint16_t>(static_cast<const uint16_t*>(w), c, n, vec, v);
+  else load8<float>(static_cast<const float*>(w), c, n, vec, v);
 }
 
-// One row per workgroup, 8 kC elements per thread.
+// A workgroup takes the rows g, g + groups, ..., 8 kC elements per thread.  Up
+// to kC = 2 W stays in registers, and the next row's loads go out before this
+// row's sum is waited for; longer rows need the registers for themselves.
 //   r = round(x + res), t = 1 / sqrt(mean r^2 + eps), y = r t w
 // The sum is rounded to its storage type first and the rounded one is
 // normalised, so that the gradient, which sees only the stored sum, is that of
 // what was computed.
+//
+// The codes do not see the rounding of y: with u = r w, a block's codes are
+// u (448 / max|u|), in which t cancels (power-of-two scales: u (t / s), t kept
+// in fp64), and u and the factor each carry their rounding error as a second
+// fp32.  What is left is one fp32 rounding before the rounding to e4m3.
 template <typename T, bool kE8m0, int kThreads, int kC>
 __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
-  __shared__ float red[kThreads / 64];
-  const int64_t row = blockIdx.x;
+  __shared__ float red[2][2][kThreads / 64];
   const int t = threadIdx.x;
-  float v[kC][8];
-  float sq = 0.f;
+  constexpr bool kAhead = kC <= 2;
+  float w[kAhead ? kC : 1][8], x[kC][8], res[kC][8];
+  if constexpr (kAhead) {
 #pragma unroll
-  for (int i = 0; i < kC; ++i) {
-    const int c = (i * kThreads + t) * 8;
-    load8<T>(static_cast<const T*>(a.x) + row * a.ldx, c, a.n, a.vec, v[i]);
-    if (a.res) {
-      float r[8];
-      load8<T>(static_cast<const T*>(a.res) + row * a.ldres, c, a.n, a.vec, r);
+    for (int i = 0; i < kC; ++i) load_w8(a.w, a.w_bf, (i * kThreads + t) * 8, a.n, a.wvec, w[i]);
+  }
+  auto load_row = [&](int64_t row) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      const int c = (i * kThreads + t) * 8;
+      load8<T>(static_cast<const T*>(a.x) + row * a.ldx, c, a.n, a.vec, x[i]);
+      if (a.res) load8<T>(static_cast<const T*>(a.res) + row * a.ldres, c, a.n, a.vec, res[i]);
+    }
+  };
+  if (kAhead) load_row(blockIdx.x);
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x, turn ^= 1) {
+    if (!kAhead) load_row(row);
+    float v[kC][8];
+    float sq = 0.f, unused = 0.f;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[i][j] += r[j];
-        if constexpr (sizeof(T) == 2) v[i][j] = static_cast<float>(to_bf16(v[i][j]));
+        v[i][j] = x[i][j];
+        if (a.res) {
+          v[i][j] += res[i][j];
+          if constexpr (sizeof(T) == 2) v[i][j] = static_cast<float>(to_bf16(v[i][j]));
+        }
+        sq += v[i][j] * v[i][j];
       }
     }
-    if (a.sum) store8<T>(static_cast<T*>(a.sum) + row * a.ldsum, c, a.n, a.vec, v[i]);
+    if (kAhead && row + gridDim.x < a.m) load_row(row + gridDim.x);
+    if (a.sum) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sq += v[i][j] * v[i][j];
-  }
-  const float rs = 1.f / __builtin_sqrtf(block_sum<kThreads>(sq, red) / a.n + a.eps);
+      for (int i = 0; i < kC; ++i)
+        store8<T>(static_cast<T*>(a.sum) + row * a.ldsum, (i * kThreads + t) * 8, a.n, a.vec, v[i]);
+    }
+    block_sum2<kThreads>(sq, unused, red, turn);
+    const double rsd = 1.0 / __builtin_sqrt(static_cast<double>(sq / a.n + a.eps));
+    const float rs = static_cast<float>(rsd);
 #pragma unroll
-  for (int i = 0; i < kC; ++i) {
-    const int c = (i * kThreads + t) * 8;
-    if (c - (t & 15) * 8 >= a.n) continue;   // whole block past the row's end
-    float w[8];
-    load_w8(a.w, a.w_bf, c, a.n, w);
+    for (int i = 0; i < kC; ++i) {
+      const int c = (i * kThreads + t) * 8;
+      if (c - (t & 15) * 8 >= a.n) continue;   // whole block past the row's end
+      float u[8], ul[8], q[8];
+      float (&wi)[8] = w[kAhead ? i : 0];
+      if (!kAhead) load_w8(a.w, a.w_bf, c, a.n, a.wvec, wi);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rs * w[j];
-    if (a.y) store8<T>(static_cast<T*>(a.y) + row * a.ldy, c, a.n, a.vec, v[i]);
-    float scale, f;
-    block_scale<kE8m0>(max16(top8(v[i])), scale, f);
-    store_codes8(a.q + row * a.ldq, c, a.n, a.qvec, codes8(v[i], f));
-    if ((t & 15) == 0) store_scale<kE8m0>(a.s, row * a.lds + c / kFp8Block, scale);
+      for (int j = 0; j < 8; ++j) {
+        u[j] = v[i][j] * wi[j];
+        ul[j] = fmaf(v[i][j], wi[j], -u[j]);
+      }
+      if (a.y) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = v[i][j] * rs * wi[j];
+        store8<T>(static_cast<T*>(a.y) + row * a.ldy, c, a.n, a.vec, y);
+      }
+      const float top = max16(top8(u));
+      const float top_y = rsd > 0.0 ? static_cast<float>(top * rsd) : 0.f;   // 0: the row is infinite or NaN
+      float scale, f;
+      block_scale<kE8m0>(top_y, scale, f);
+      // fp32 scales: 448 / top, unless the scale is the smallest or 1
+      const double g = !kE8m0 && scale > 0x1p-126f && top_y > 0.f ? 448.0 / top : rsd / scale;
+      const float gh = static_cast<float>(g), gl = static_cast<float>(g - gh);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float h = u[j] * gh;
+        // (not finite: the product as it is, so that infinities give NaN codes)
+        const float e = fmaf(u[j], gh, -h) + fmaf(ul[j], gh, u[j] * gl);
+        q[j] = __builtin_fabsf(h) <= 512.f ? h + e : v[i][j] * rs * wi[j] * f;
+      }
+      store_codes8(a.q + row * a.ldq, c, a.n, a.qvec, codes8(q, 1.f));
+      if ((t & 15) == 0) store_scale<kE8m0>(a.s, row * a.lds + c / kFp8Block, scale);
+    }
   }
 }
 
 // Gradient of the norm.  With h = dy w, u = x t:
 //   dx = t (h - u mean(h u)) (+ dsum),  dw = sum over rows of dy u
-// Workgroup g takes the rows g, g + groups, ... and keeps its part of dw in
-// registers; the parts are added in a fixed order by a second launch.
+// Workgroup g takes the rows g, g + groups, ..., as above, and keeps its part
+// of dw in registers; the parts are added in a fixed order by a second launch.
 template <typename T, int kThreads, int kC>
 __global__ __launch_bounds__(kThreads) void rms_norm_grad_kernel(NormGradArgs a) {
-  __shared__ float red[2][kThreads / 64];
+  __shared__ float red[2][2][kThreads / 64];
   const int t = threadIdx.x;
-  float dw[kC][8];
+  constexpr bool kAhead = kC <= 2;
+  float w[kAhead ? kC : 1][8], dw[kC][8], nx[kC][8], ng[kC][8], nd[kAhead ? kC : 1][8];
 #pragma unroll
-  for (int i = 0; i < kC; ++i)
+  for (int i = 0; i < kC; ++i) {
+    if (kAhead) load_w8(a.w, a.w_bf, (i * kThreads + t) * 8, a.n, a.wvec, w[kAhead ? i : 0]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
-  for (int64_t row = blockIdx.x; row < a.m; row += a.groups) {
-    float x[kC][8], g[kC][8];
-    float sq = 0.f, dot = 0.f;
+  }
+  auto load_row = [&](int64_t row) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       const int c = (i * kThreads + t) * 8;
-      float w[8];
-      load8<T>(static_cast<const T*>(a.x) + row * a.ldx, c, a.n, a.vec, x[i]);
-      load8<T>(static_cast<const T*>(a.dy) + row * a.lddy, c, a.n, a.vec, g[i]);
-      load_w8(a.w, a.w_bf, c, a.n, w);
+      load8<T>(static_cast<const T*>(a.x) + row * a.ldx, c, a.n, a.vec, nx[i]);
+      load8<T>(static_cast<const T*>(a.dy) + row * a.lddy, c, a.n, a.vec, ng[i]);
+      if (kAhead && a.dsum)
+        load8<T>(static_cast<const T*>(a.dsum) + row * a.lddsum, c, a.n, a.vec, nd[kAhead ? i : 0]);
+    }
+  };
+  if (kAhead) load_row(blockIdx.x);
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.m; row += a.groups, turn ^= 1) {
+    if (!kAhead) load_row(row);
+    float x[kC][8], g[kC][8], d[kAhead ? kC : 1][8];
+    float sq = 0.f, dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      float (&wi)[8] = w[kAhead ? i : 0];
+      if (!kAhead) load_w8(a.w, a.w_bf, (i * kThreads + t) * 8, a.n, a.wvec, wi);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
+        x[i][j] = nx[i][j];
+        g[i][j] = ng[i][j];
+        if (kAhead) d[kAhead ? i : 0][j] = nd[kAhead ? i : 0][j];
         sq += x[i][j] * x[i][j];
-        dot += x[i][j] * (g[i][j] * w[j]);
+        dot += x[i][j] * (g[i][j] * wi[j]);
       }
     }
-    sq = block_sum<kThreads>(sq, red[0]);
-    dot = block_sum<kThreads>(dot, red[1]);
+    if (kAhead && row + a.groups < a.m) load_row(row + a.groups);
+    block_sum2<kThreads>(sq, dot, red, turn);
     const float rs = 1.f / __builtin_sqrtf(sq / a.n + a.eps);
     const float mean = dot * rs / a.n;   // mean(h u)
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       const int c = (i * kThreads + t) * 8;
-      if (c >= a.n) continue;
-      float w[8], d[8], o[8];
-      load_w8(a.w, a.w_bf, c, a.n, w);
-      if (a.dsum) load8<T>(static_cast<const T*>(a.dsum) + row * a.lddsum, c, a.n, a.vec, d);
+      float o[8];
+      float (&wi)[8] = w[kAhead ? i : 0], (&di)[8] = d[kAhead ? i : 0];
+      if (!kAhead) {
+        load_w8(a.w, a.w_bf, c, a.n, a.wvec, wi);
+        if (a.dsum) load8<T>(static_cast<const T*>(a.dsum) + row * a.lddsum, c, a.n, a.vec, di);
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float u = x[i][j] * rs;
         dw[i][j] += g[i][j] * u;
-        o[j] = rs * (g[i][j] * w[j] - u * mean);
-        if (a.dsum) o[j] += d[j];
+        o[j] = rs * (g[i][j] * wi[j] - u * mean);
+        if (a.dsum) o[j] += di[j];
       }
       store8<T>(static_cast<T*>(a.dx) + row * a.lddx, c, a.n, a.vec, o);
     }
   }
 #pragma unroll
-  for (int i = 0; i < kC; ++i) {
-    const int c = (i * kThreads + t) * 8;
-    store8<float>(a.part + (int64_t)blockIdx.x * a.n, c, a.n, false, dw[i]);
-  }
+  for (int i = 0; i < kC; ++i)
+    store8<float>(a.part + (int64_t)blockIdx.x * a.ldpart, (i * kThreads + t) * 8, a.n, true, dw[i]);
 }
 
-__global__ __launch_bounds__(256) void rms_norm_dw_kernel(NormGradArgs a) {
-  __shared__ float red[4][64];
+// dw: 64 columns per workgroup, the parts shared among 16 waves and added in a
+// fixed order.
+__global__ __launch_bounds__(1024) void rms_norm_dw_kernel(NormGradArgs a) {
+  __shared__ float red[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.x * 64 + lane;
   float sum = 0.f;
-  if (c < a.n)
-    for (int g = wave; g < a.groups; g += 4) sum += a.part[(int64_t)g * a.n + c];
+  if (c < a.n) {
+#pragma unroll 8
+    for (int g = wave; g < a.groups; g += 16) sum += a.part[(int64_t)g * a.ldpart + c];
+  }
   red[wave][lane] = sum;
   __syncthreads();
-  if (wave == 0 && c < a.n)
-    a.dw[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+  if (wave == 0 && c < a.n) {
+    float total = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) total += red[w][lane];
+    a.dw[c] = total;
+  }
 }
 
 // f(threads, elements per thread / 8) at the smallest workgroup that holds a
-// row of n elements; n <= 65536.
+// row of n elements; n <= 32768.
 template <class F>
 hipError_t by_width(int n, F f) {
   if (n <= 512) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
   else if (n <= 1024) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
   else if (n <= 2048) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
   else if (n <= 4096) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-  else if (n <= 8192) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
-  else if (n <= 16384) f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+  else if (n <= 8192) f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
+  else if (n <= 16384) f(std::integral_constant<int, 512>{}, std::integral_constant<int, 4>{});
   else if (n <= 32768) f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
-  else if (n <= 65536) f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 8>{});
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }
@@ -314,11 +395,19 @@ hipError_t quantize(const QuantArgs& a, bool tiles, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Workgroups of the forward norm: rows are shared among as many as the chip
+// holds at eight waves per SIMD.
+inline int64_t norm_groups(int64_t m, int threads) {
+  const int64_t most = 256 * 4 * 8 * 64 / threads;
+  return m < most ? m : most;
+}
+
 template <typename T, bool kE8m0>
 hipError_t norm(const NormArgs& a, hipStream_t s) {
   return by_width(a.n, [&](auto th, auto c) {
     hipLaunchKernelGGL((rms_norm_fp8_kernel<T, kE8m0, decltype(th)::value, decltype(c)::value>),
-                       dim3(a.m), dim3(decltype(th)::value), 0, s, a);
+                       dim3(static_cast<uint32_t>(norm_groups(a.m, decltype(th)::value))),
+                       dim3(decltype(th)::value), 0, s, a);
   });
 }
 
@@ -329,7 +418,7 @@ hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
                        dim3(a.groups), dim3(decltype(th)::value), 0, s, a);
   });
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(rms_norm_dw_kernel, dim3(static_cast<uint32_t>(cdiv(a.n, 64))), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(rms_norm_dw_kernel, dim3(static_cast<uint32_t>(cdiv(a.n, 64))), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 

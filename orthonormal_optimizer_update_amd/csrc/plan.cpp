@@ -499,8 +499,9 @@ bool plan_fp8_matmul(int64_t m, int64_t n, int64_t k, Fp8MatmulPlan* p) {
 
 bool plan_norm_grad(int64_t m, int64_t n, NormGradPlan* p) {
   if (m < 1 || n < 1 || m > kMaxDim || n > kNormMaxCols) return false;
-  p->groups = static_cast<int>(m < 512 ? m : 512);
-  p->total_bytes = align_up(static_cast<size_t>(p->groups) * static_cast<size_t>(n) * 4);
+  p->groups = static_cast<int>(m < 1024 ? m : 1024);
+  p->ld = cdiv(n, 8) * 8;
+  p->total_bytes = align_up(static_cast<size_t>(p->groups) * static_cast<size_t>(p->ld) * 4);
   return true;
 }
 

@@ -156,7 +156,7 @@ ortho_status validate_muon(int32_t batch, const ortho_mat* X, const ortho_mat* G
 // 8-bit operators (fp8_quantize, rms_norm_fp8, rms_norm_backward, fp8_matmul).
 constexpr int64_t kFp8BlockSize = 128;
 // Longest row of the norms: it stays in one workgroup's registers.
-constexpr int64_t kNormMaxCols = 65536;
+constexpr int64_t kNormMaxCols = 32768;
 
 struct Fp8MatmulPlan {
   size_t total_bytes;
@@ -166,6 +166,7 @@ bool plan_fp8_matmul(int64_t m, int64_t n, int64_t k, Fp8MatmulPlan* out);
 // dw partial sums: one row of n floats per workgroup of the norm's gradient.
 struct NormGradPlan {
   int groups;
+  int64_t ld;               // n rounded to 8
   size_t total_bytes;
 };
 bool plan_norm_grad(int64_t m, int64_t n, NormGradPlan* out);
