@@ -138,6 +138,102 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a < __builtin_inff() ? a : 0.f;
 }
 
+// Eight consecutive elements as stored: fp32 in two registers of four, bf16 in
+// one of eight.
+template <typename T> struct Raw8;
+template <> struct Raw8<uint16_t> { uint4 a; };
+template <> struct Raw8<float> { uint4 a, b; };
+
+__device__ __forceinline__ void unpack8(const Raw8<uint16_t>& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+}
+
+// From column c of a row of `limit` columns; zeros past its end.
+__device__ __forceinline__ Raw8<uint16_t> load_raw8(const uint16_t* row, int c, int limit, bool vec) {
+  Raw8<uint16_t> r;
+  if (vec && c + 8 <= limit) {
+    r.a = *reinterpret_cast<const uint4*>(row + c);
+    return r;
+  }
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j < limit) w[j >> 1] |= static_cast<uint32_t>(row[c + j]) << (16 * (j & 1));
+  r.a = make_uint4(w[0], w[1], w[2], w[3]);
+  return r;
+}
+__device__ __forceinline__ Raw8<float> load_raw8(const float* row, int c, int limit, bool vec) {
+  Raw8<float> r;
+  if (vec && c + 8 <= limit) {
+    r.a = *reinterpret_cast<const uint4*>(row + c);
+    r.b = *reinterpret_cast<const uint4*>(row + c + 4);
+    return r;
+  }
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = c + j < limit ? __float_as_uint(row[c + j]) : 0u;
+  r.a = make_uint4(w[0], w[1], w[2], w[3]);
+  r.b = make_uint4(w[4], w[5], w[6], w[7]);
+  return r;
+}
+
+// Magnitudes as integers, which order like the values: bf16 two to a register,
+// fp32 one.  Infinities and NaN are the largest, so a maximum from kTop on
+// says that there is one.
+typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
+template <typename T> struct Mags;
+template <> struct Mags<uint16_t> { ushort2v m[4]; };
+template <> struct Mags<float> { uint32_t m[8]; };
+
+__device__ __forceinline__ Mags<uint16_t> magnitudes(const Raw8<uint16_t>& r) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+  Mags<uint16_t> o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o.m[j] = __builtin_bit_cast(ushort2v, w[j] & 0x7fff7fffu);
+  return o;
+}
+__device__ __forceinline__ Mags<float> magnitudes(const Raw8<float>& r) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+  Mags<float> o;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o.m[j] = w[j] & 0x7fffffffu;
+  return o;
+}
+template <typename T>
+__device__ __forceinline__ Mags<T> max_of(const Mags<T>& a, const Mags<T>& b) {
+  Mags<T> o;
+#pragma unroll
+  for (int j = 0; j < (sizeof(T) == 2 ? 4 : 8); ++j) o.m[j] = __builtin_elementwise_max(a.m[j], b.m[j]);
+  return o;
+}
+// Element j's magnitude, and the largest of the eight, as fp32 bits.
+__device__ __forceinline__ uint32_t element(const Mags<uint16_t>& a, int j) {
+  return static_cast<uint32_t>(a.m[j >> 1][j & 1]) << 16;
+}
+__device__ __forceinline__ uint32_t element(const Mags<float>& a, int j) { return a.m[j]; }
+__device__ __forceinline__ uint32_t largest(const Mags<uint16_t>& a) {
+  const ushort2v m = __builtin_elementwise_max(__builtin_elementwise_max(a.m[0], a.m[1]),
+                                               __builtin_elementwise_max(a.m[2], a.m[3]));
+  return static_cast<uint32_t>(m[0] > m[1] ? m[0] : m[1]) << 16;
+}
+__device__ __forceinline__ uint32_t largest(const Mags<float>& a) {
+  uint32_t m = a.m[0];
+#pragma unroll
+  for (int j = 1; j < 8; ++j) m = m > a.m[j] ? m : a.m[j];
+  return m;
+}
+constexpr uint32_t kInfBits = 0x7f800000u;
+
 // Four fp32 values as four e4m3 codes, round to nearest even; infinities and
 // NaN give the NaN code.
 __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {

@@ -26,30 +26,41 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_few_kernel(Fp8GemmArgs p) {
   floatx4 acc[kMB];
 #pragma unroll
   for (int i = 0; i < kMB; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-  for (int b0 = wave; b0 < nkb; b0 += kWaves * kAhead) {
-    uint4 rb[kAhead][2], ra[kAhead][kMB][2];
-    float sa[kAhead][kMB], sb[kAhead][4];
+  const int64_t srow = min(n0 + lg * 4, p.N - 1);   // kept in bounds below, too
+  auto step = [&](int b0, auto ahead, auto checked) __attribute__((always_inline)) {
+    constexpr int kN = decltype(ahead)::value;
+    uint4 rb[kN][2], ra[kN][kMB][2];
+    float sa[kN][kMB], sb[kN][4];
 #pragma unroll
-    for (int x = 0; x < kAhead; ++x) {
-      const int kb = b0 + x * kWaves, k = kb * 128 + lg * 16, ks = min(kb, nkb - 1);
-      rb[x][0] = load_codes16(brow, k, p.K);
-      rb[x][1] = load_codes16(brow, k + 64, p.K);
+    for (int x = 0; x < kN; ++x) {
+      const int kb = b0 + x * kWaves, k = kb * 128 + lg * 16;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (decltype(checked)::value) rb[x][h] = load_codes16(brow, k + 64 * h, p.K);
+        else __builtin_memcpy(&rb[x][h], brow + k + 64 * h, 16);
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int64_t r = min(n0 + lg * 4 + e, p.N - 1) >> p.sb.shift;
-        sb[x][e] = load_scale<kE8m0>(p.sb.p, r * p.sb.ld + ks);
+        if (p.sb.shift != 0 && e > 0) {   // 128 rows of B share a scale, and 16 never lie in two blocks
+          sb[x][e] = sb[x][0];
+        } else {
+          const int64_t r = (p.sb.shift != 0 ? n0 : min(static_cast<int>(srow) + e, p.N - 1)) >> p.sb.shift;
+          sb[x][e] = load_scale<kE8m0>(p.sb.p, r * p.sb.ld + kb);
+        }
       }
 #pragma unroll
       for (int i = 0; i < kMB; ++i) {
         const int m = min(i * 16 + l16, p.M - 1);
-        ra[x][i][0] = load_codes16(p.a + m * p.lda, k, p.K);
-        ra[x][i][1] = load_codes16(p.a + m * p.lda, k + 64, p.K);
-        sa[x][i] = load_scale<kE8m0>(p.sa.p, (m >> p.sa.shift) * p.sa.ld + ks);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (decltype(checked)::value) ra[x][i][h] = load_codes16(p.a + m * p.lda, k + 64 * h, p.K);
+          else __builtin_memcpy(&ra[x][i][h], p.a + m * p.lda + k + 64 * h, 16);
+        }
+        sa[x][i] = load_scale<kE8m0>(p.sa.p, (m >> p.sa.shift) * p.sa.ld + kb);
       }
     }
 #pragma unroll
-    for (int x = 0; x < kAhead; ++x) {
-      if (b0 + x * kWaves >= nkb) break;
+    for (int x = 0; x < kN; ++x)
 #pragma unroll
       for (int i = 0; i < kMB; ++i) {
         floatx4 s = {0.f, 0.f, 0.f, 0.f};
@@ -62,8 +73,16 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_few_kernel(Fp8GemmArgs p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(s[e], sa[x][i] * sb[x][e], acc[i][e]);
       }
-    }
-  }
+  };
+  // whole blocks without bounds checks (a check per load would make each wait
+  // for the one before), then what is left of K
+  const int whole = p.K / kFp8Block;
+  int kb = wave;
+  for (; kb + (kAhead - 1) * kWaves < whole; kb += kAhead * kWaves)
+    step(kb, std::integral_constant<int, kAhead>{}, std::false_type{});
+  if constexpr (kAhead > 1)
+    for (; kb < whole; kb += kWaves) step(kb, std::integral_constant<int, 1>{}, std::false_type{});
+  if (kb < nkb) step(kb, std::integral_constant<int, 1>{}, std::true_type{});
 #pragma unroll
   for (int i = 0; i < kMB; ++i) *reinterpret_cast<floatx4*>(&part[wave][i][l16][lg * 4]) = acc[i];
   __syncthreads();

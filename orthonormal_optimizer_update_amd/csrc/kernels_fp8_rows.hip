@@ -19,6 +19,15 @@ __device__ __forceinline__ float max16(float v) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    const uint32_t w = __shfl_xor(v, o, 64);
+    v = v > w ? v : w;
+  }
+  return v;
+}
+
 __device__ __forceinline__ float top8(const float (&v)[8]) {
   float t = 0.f;
 #pragma unroll
@@ -50,39 +59,68 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
 // A 128 x 128 tile per workgroup, 8 x 8 elements per thread (columns of 16
 // threads, rows of 16 groups): codes by rows, transposed, or both, from one
 // read.  kTiles: one scale for the tile; otherwise one per row for the codes
-// by rows and one per column for the transposed ones.
+// by rows and one per column for the transposed ones.  The largest magnitudes
+// are found on the elements' bits (two bf16 per instruction); only a tile that
+// holds an infinity or NaN looks at the elements one by one.
 template <typename T, bool kE8m0, bool kTiles>
-__global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 1) void quant_tile_kernel(QuantArgs a) {
   constexpr int kPitch = 128 + 16;   // bytes per LDS row of transposed codes
   __shared__ __attribute__((aligned(16))) uint8_t tile[128 * kPitch];
-  __shared__ float red[4][128];
+  __shared__ uint32_t red[4][128];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int nbn = (a.n + 127) / 128;
   const int tn = blockIdx.x % nbn, tm = blockIdx.x / nbn;
   const int cl = (t & 15) * 8, rl = (t >> 4) * 8;
   const int c = tn * 128 + cl, r0 = tm * 128 + rl;
-  float v[8][8];
+  Raw8<T> x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (r0 + i < a.m) {
-      load8<T>(static_cast<const T*>(a.x) + (r0 + i) * a.ldx, c, a.n, a.vec, v[i]);
-    } else {
+    if (r0 + i < a.m) x[i] = load_raw8(static_cast<const T*>(a.x) + (r0 + i) * a.ldx, c, a.n, a.vec);
+    else x[i] = Raw8<T>{};
+  }
+  // largest finite magnitudes: of each row's 8 elements, and of each column's
+  uint32_t rows[8], cols[8];
+  Mags<T> down = magnitudes(x[0]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+  for (int i = 0; i < 8; ++i) {
+    const Mags<T> m = magnitudes(x[i]);
+    rows[i] = largest(m);
+    if (i > 0) down = max_of(down, m);
+  }
+  if (largest(down) >= kInfBits) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cols[j] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      rows[i] = 0;
+      const Mags<T> m = magnitudes(x[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t e = element(m, j) < kInfBits ? element(m, j) : 0;
+        rows[i] = rows[i] > e ? rows[i] : e;
+        cols[j] = cols[j] > e ? cols[j] : e;
+      }
     }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cols[j] = element(down, j);
   }
   float fr[8], fc[8];   // factors by row and by column
   if constexpr (kTiles) {
-    float top = 0.f;
+    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, top8(v[i]));
+    for (int i = 0; i < 8; ++i) top = top > rows[i] ? top : rows[i];
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    for (int o = 32; o > 0; o >>= 1) {
+      const uint32_t w = __shfl_xor(top, o, 64);
+      top = top > w ? top : w;
+    }
     if (lane == 0) red[0][wave] = top;
     __syncthreads();
-    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = top > red[0][w] ? top : red[0][w];
     float scale, f;
-    block_scale<kE8m0>(top, scale, f);
+    block_scale<kE8m0>(__uint_as_float(top), scale, f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) fr[i] = fc[i] = f;
     if (t == 0) {
@@ -90,35 +128,59 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(QuantArgs a) {
       if (a.qt) store_scale<kE8m0>(a.st, tn * a.ldst + tm, scale);
     }
   } else {
-    if (a.q) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float scale;
-        block_scale<kE8m0>(max16(top8(v[i])), scale, fr[i]);
-        if ((t & 15) == 0 && r0 + i < a.m) store_scale<kE8m0>(a.s, (r0 + i) * a.lds + tn, scale);
-      }
-    }
     if (a.qt) {
-      float top[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        top[j] = 0.f;
+        uint32_t top = cols[j];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top[j] = fmaxf(top[j], finite_abs(v[i][j]));
-        top[j] = fmaxf(top[j], __shfl_xor(top[j], 16, 64));
-        top[j] = fmaxf(top[j], __shfl_xor(top[j], 32, 64));
-        if (lane < 16) red[wave][cl + j] = top[j];
+        for (int o = 16; o <= 32; o <<= 1) {
+          const uint32_t w = __shfl_xor(top, o, 64);
+          top = top > w ? top : w;
+        }
+        cols[j] = top;
+      }
+      if (lane < 16) {
+        *reinterpret_cast<uint4*>(&red[wave][cl]) = make_uint4(cols[0], cols[1], cols[2], cols[3]);
+        *reinterpret_cast<uint4*>(&red[wave][cl + 4]) = make_uint4(cols[4], cols[5], cols[6], cols[7]);
+      }
+    }
+    if (a.q) {
+      // lane l of a row's 16 works out the scale of row l / 2
+      uint32_t mine = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t top = max16(rows[i]);
+        if ((lane & 15) >> 1 == i) mine = top;
+      }
+      float scale, f;
+      block_scale<kE8m0>(__uint_as_float(mine), scale, f);
+      const int r = r0 + ((lane & 15) >> 1);
+      if ((lane & 1) == 0 && r < a.m) store_scale<kE8m0>(a.s, r * a.lds + tn, scale);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) fr[i] = __shfl(f, (lane & 48) + 2 * i, 64);
+    }
+    if (a.qt) {
+      __syncthreads();
+      // thread c (of 128) works out the scale of column c
+      float* const factors = reinterpret_cast<float*>(&red[0][0]);
+      float f = 0.f;
+      if (t < 128) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = top > red[w][t] ? top : red[w][t];
+        float scale;
+        block_scale<kE8m0>(__uint_as_float(top), scale, f);
+        if (tn * 128 + t < a.n) store_scale<kE8m0>(a.st, (tn * 128 + t) * a.ldst + tm, scale);
+        factors[t] = f;   // its own column's, which no one else reads above
       }
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float scale;
-        block_scale<kE8m0>(fmaxf(fmaxf(red[0][cl + j], red[1][cl + j]),
-                                 fmaxf(red[2][cl + j], red[3][cl + j])), scale, fc[j]);
-        if (t < 16 && c + j < a.n) store_scale<kE8m0>(a.st, (c + j) * a.ldst + tm, scale);
-      }
+      for (int j = 0; j < 8; ++j) fc[j] = factors[cl + j];
     }
   }
+  float v[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) unpack8(x[i], v[i]);
   if (a.q) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -194,7 +256,8 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
   __shared__ float red[2][2][kThreads / 64];
   const int t = threadIdx.x;
   constexpr bool kAhead = kC <= 2;
-  float w[kAhead ? kC : 1][8], x[kC][8], res[kC][8];
+  float w[kAhead ? kC : 1][8];
+  Raw8<T> x[kC], res[kC];
   if constexpr (kAhead) {
 #pragma unroll
     for (int i = 0; i < kC; ++i) load_w8(a.w, a.w_bf, (i * kThreads + t) * 8, a.n, a.wvec, w[i]);
@@ -203,8 +266,8 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       const int c = (i * kThreads + t) * 8;
-      load8<T>(static_cast<const T*>(a.x) + row * a.ldx, c, a.n, a.vec, x[i]);
-      if (a.res) load8<T>(static_cast<const T*>(a.res) + row * a.ldres, c, a.n, a.vec, res[i]);
+      x[i] = load_raw8(static_cast<const T*>(a.x) + row * a.ldx, c, a.n, a.vec);
+      if (a.res) res[i] = load_raw8(static_cast<const T*>(a.res) + row * a.ldres, c, a.n, a.vec);
     }
   };
   if (kAhead) load_row(blockIdx.x);
@@ -215,15 +278,18 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
     float sq = 0.f, unused = 0.f;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
+      unpack8(x[i], v[i]);
+      if (a.res) {
+        float r[8];
+        unpack8(res[i], r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[i][j] = x[i][j];
-        if (a.res) {
-          v[i][j] += res[i][j];
+        for (int j = 0; j < 8; ++j) {
+          v[i][j] += r[j];
           if constexpr (sizeof(T) == 2) v[i][j] = static_cast<float>(to_bf16(v[i][j]));
         }
-        sq += v[i][j] * v[i][j];
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sq += v[i][j] * v[i][j];
     }
     if (kAhead && row + gridDim.x < a.m) load_row(row + gridDim.x);
     if (a.sum) {
@@ -272,16 +338,24 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
   }
 }
 
+// Unpacks r anew from here on: four registers of bf16 instead of eight of
+// fp32 stay alive across the sums.
+__device__ __forceinline__ void again(Raw8<uint16_t>& r) {
+  asm volatile("" : "+v"(r.a.x), "+v"(r.a.y), "+v"(r.a.z), "+v"(r.a.w));
+}
+__device__ __forceinline__ void again(Raw8<float>&) {}
+
 // Gradient of the norm.  With h = dy w, u = x t:
 //   dx = t (h - u mean(h u)) (+ dsum),  dw = sum over rows of dy u
 // Workgroup g takes the rows g, g + groups, ..., as above, and keeps its part
 // of dw in registers; the parts are added in a fixed order by a second launch.
 template <typename T, int kThreads, int kC>
-__global__ __launch_bounds__(kThreads) void rms_norm_grad_kernel(NormGradArgs a) {
+__global__ __launch_bounds__(kThreads, kC <= 2 && sizeof(T) == 2 ? 4 : 1) void rms_norm_grad_kernel(NormGradArgs a) {
   __shared__ float red[2][2][kThreads / 64];
   const int t = threadIdx.x;
   constexpr bool kAhead = kC <= 2;
-  float w[kAhead ? kC : 1][8], dw[kC][8], nx[kC][8], ng[kC][8], nd[kAhead ? kC : 1][8];
+  float w[kAhead ? kC : 1][8], dw[kC][8];
+  Raw8<T> nx[kC], ng[kC], nd[kAhead ? kC : 1];
 #pragma unroll
   for (int i = 0; i < kC; ++i) {
     if (kAhead) load_w8(a.w, a.w_bf, (i * kThreads + t) * 8, a.n, a.wvec, w[kAhead ? i : 0]);
@@ -292,29 +366,32 @@ __global__ __launch_bounds__(kThreads) void rms_norm_grad_kernel(NormGradArgs a)
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       const int c = (i * kThreads + t) * 8;
-      load8<T>(static_cast<const T*>(a.x) + row * a.ldx, c, a.n, a.vec, nx[i]);
-      load8<T>(static_cast<const T*>(a.dy) + row * a.lddy, c, a.n, a.vec, ng[i]);
+      nx[i] = load_raw8(static_cast<const T*>(a.x) + row * a.ldx, c, a.n, a.vec);
+      ng[i] = load_raw8(static_cast<const T*>(a.dy) + row * a.lddy, c, a.n, a.vec);
       if (kAhead && a.dsum)
-        load8<T>(static_cast<const T*>(a.dsum) + row * a.lddsum, c, a.n, a.vec, nd[kAhead ? i : 0]);
+        nd[kAhead ? i : 0] = load_raw8(static_cast<const T*>(a.dsum) + row * a.lddsum, c, a.n, a.vec);
     }
   };
   if (kAhead) load_row(blockIdx.x);
   int turn = 0;
   for (int64_t row = blockIdx.x; row < a.m; row += a.groups, turn ^= 1) {
     if (!kAhead) load_row(row);
-    float x[kC][8], g[kC][8], d[kAhead ? kC : 1][8];
+    Raw8<T> rx[kC], rg[kC], rd[kAhead ? kC : 1];
     float sq = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
+      rx[i] = nx[i];
+      rg[i] = ng[i];
+      if (kAhead) rd[kAhead ? i : 0] = nd[kAhead ? i : 0];
+      float x[8], g[8];
+      unpack8(rx[i], x);
+      unpack8(rg[i], g);
       float (&wi)[8] = w[kAhead ? i : 0];
       if (!kAhead) load_w8(a.w, a.w_bf, (i * kThreads + t) * 8, a.n, a.wvec, wi);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        x[i][j] = nx[i][j];
-        g[i][j] = ng[i][j];
-        if (kAhead) d[kAhead ? i : 0][j] = nd[kAhead ? i : 0][j];
-        sq += x[i][j] * x[i][j];
-        dot += x[i][j] * (g[i][j] * wi[j]);
+        sq += x[j] * x[j];
+        dot += x[j] * (g[j] * wi[j]);
       }
     }
     if (kAhead && row + a.groups < a.m) load_row(row + a.groups);
@@ -324,18 +401,26 @@ __global__ __launch_bounds__(kThreads) void rms_norm_grad_kernel(NormGradArgs a)
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       const int c = (i * kThreads + t) * 8;
-      float o[8];
-      float (&wi)[8] = w[kAhead ? i : 0], (&di)[8] = d[kAhead ? i : 0];
+      float o[8], x[8], g[8], d[8];
+      float (&wi)[8] = w[kAhead ? i : 0];
       if (!kAhead) {
         load_w8(a.w, a.w_bf, c, a.n, a.wvec, wi);
-        if (a.dsum) load8<T>(static_cast<const T*>(a.dsum) + row * a.lddsum, c, a.n, a.vec, di);
+        if (a.dsum) rd[0] = load_raw8(static_cast<const T*>(a.dsum) + row * a.lddsum, c, a.n, a.vec);
       }
+      again(rx[i]);
+      again(rg[i]);
+      unpack8(rx[i], x);
+      unpack8(rg[i], g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float u = x[i][j] * rs;
-        dw[i][j] += g[i][j] * u;
-        o[j] = rs * (g[i][j] * wi[j] - u * mean);
-        if (a.dsum) o[j] += di[j];
+        const float u = x[j] * rs;
+        dw[i][j] += g[j] * u;
+        o[j] = rs * (g[j] * wi[j] - u * mean);
+      }
+      if (a.dsum) {
+        unpack8(rd[kAhead ? i : 0], d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] += d[j];
       }
       store8<T>(static_cast<T*>(a.dx) + row * a.lddx, c, a.n, a.vec, o);
     }
