@@ -144,7 +144,16 @@ ortho_status fp8_matmul(ortho_mat A, ortho_mat SA, ortho_mat B, ortho_mat SB, or
   constexpr int64_t kMaxLd = 1 << 22;   // 256 rows within 32-bit byte offsets, scales' rows too
   a.dma = rows_at(&A, 16) && rows_at(&B, 16) && A.ld <= kMaxLd && B.ld <= kMaxLd &&
           SA.ld <= kMaxLd / 4 && SB.ld <= kMaxLd / 4;
-  return done(launch_fp8_matmul(a, C.dtype == ORTHO_BF16, SA.dtype == ORTHO_E8M0, as_stream(stream)));
+  static_assert(kFewRows == kFewRowsMax, "");
+  Fp8MatmulPlan plan;
+  plan_fp8_matmul(A.rows, B.rows, A.cols, &plan);
+  a.e8m0 = SA.dtype == ORTHO_E8M0;
+  a.c_bf = C.dtype == ORTHO_BF16;
+  a.splits = plan.splits;
+  a.kchunk = plan.kchunk;
+  a.part = plan.splits > 1 ? static_cast<float*>(ws) : nullptr;
+  a.ldp = plan.ldp;
+  return done(launch_fp8_matmul(a, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -79,16 +79,16 @@ struct Fp8GemmArgs {
   int cvec;                 // C's (and Add's) rows at multiples of 16 bytes
   int M, N, K;
   int dma;                  // A's and B's rows at multiples of 16 bytes, 256 of them within 2 GiB
-  // set by the launcher
-  int e8m0, c_bf;
+  int e8m0, c_bf;           // scale type, C's type
   int splits, kchunk;       // splits of K, blocks of 128 in each
-  float* part;              // splits x M x N partial sums (splits > 1)
+  float* part;              // splits x M x ldp partial sums (splits > 1), else null
+  int64_t ldp;
 };
-constexpr int kFewRows = 64;         // rows of A up to which launch_fp8_few takes the product
+constexpr int kFewRows = 64;         // rows of A that launch_fp8_few takes (must match plan.h)
 hipError_t launch_fp8_few(const Fp8GemmArgs& a, hipStream_t s);     // M <= kFewRows
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s);    // bf16 C
 hipError_t launch_fp8_exact(const Fp8GemmArgs& a, hipStream_t s);   // fp32 C
-hipError_t launch_fp8_matmul(const Fp8GemmArgs& a, bool c_bf, bool e8m0, hipStream_t s);
+hipError_t launch_fp8_matmul(const Fp8GemmArgs& a, hipStream_t s);
 
 // Scale of a block whose largest finite magnitude is `top`, and the factor
 // that takes the block's elements to codes.  fp32: top / 448, not below 2^-126

@@ -72,17 +72,35 @@ __device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
   return reinterpret_cast<const uint8_t*>((static_cast<uint64_t>(hi) << 32) | lo);
 }
 
-// 16 codes from column k of a row; zero codes from column K on.  Any byte.
+// 16 codes from column k of a row of K; zero codes from column K on.  Any byte.
+// A piece that the row's end cuts is loaded from 16 columns before the end and
+// shifted, so that no load depends on a branch.
 __device__ __forceinline__ uint4 load_codes16(const uint8_t* row, int k, int K) {
-  uint4 u = make_uint4(0, 0, 0, 0);
-  if (k + 16 <= K) {
-    __builtin_memcpy(&u, row + k, 16);
-    return u;
+  if (K >= 16) {   // uniform
+    uint4 u;
+    __builtin_memcpy(&u, row + min(k, K - 16), 16);
+    const int cut = k + 16 - K;   // bytes of the piece that lie past the end
+    if (cut <= 0) return u;
+    uint64_t lo = u.x | static_cast<uint64_t>(u.y) << 32, hi = u.z | static_cast<uint64_t>(u.w) << 32;
+    if (cut >= 8) {
+      lo = hi;
+      hi = 0;
+    }
+    const int s = (cut & 7) * 8;
+    if (s != 0) {
+      lo = lo >> s | hi << (64 - s);
+      hi >>= s;
+    }
+    if (cut >= 16) lo = hi = 0;
+    return make_uint4(static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
+                      static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32));
   }
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (k + j < K) w[j >> 2] |= static_cast<uint32_t>(row[k + j]) << (8 * (j & 3));
+  for (int j = 0; j < 16; ++j) {
+    const uint32_t c = row[min(k + j, K - 1)];
+    w[j >> 2] |= (k + j < K ? c : 0u) << (8 * (j & 3));
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 

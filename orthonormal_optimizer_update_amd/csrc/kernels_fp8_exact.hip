@@ -220,12 +220,12 @@ __global__ __launch_bounds__(256, 2) void fp8_exact_kernel(Fp8GemmArgs p) {
     cur3 = cur3 == 2 ? 0 : cur3 + 1;
   }
 
-  const bool whole = n0 + wn + 64 <= p.N && (p.part ? p.N % 4 == 0 : p.cvec != 0);
+  const bool whole = n0 + wn + 64 <= p.N && p.cvec;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int m = m0 + wm + i * 32 + l32;
     if (m >= p.M) continue;
-    float* const out = p.part ? p.part + ((int64_t)split * p.M + m) * p.N : static_cast<float*>(p.c) + m * p.ldc;
+    float* const out = p.part ? p.part + ((int64_t)split * p.M + m) * p.ldp : static_cast<float*>(p.c) + m * p.ldc;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(256, 2) void fp8_exact_kernel(Fp8GemmArgs p) {
                                      : load4<float>(static_cast<const float*>(p.add) + m * p.ldadd, n, p.N, p.cvec);
           v[0] += ad.x; v[1] += ad.y; v[2] += ad.z; v[3] += ad.w;
         }
-        if (whole) {
+        if (whole || (p.part && n < p.N)) {   // (the splits' rows are whole quads)
           *reinterpret_cast<floatx4*>(out + n) = v;
         } else {
 #pragma unroll

@@ -388,14 +388,10 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
     if (!kWhole && m >= p.M) continue;
     const int nl = n0 + wn + lg * 16;
     if (!kWhole && p.part) {
-      float* o = p.part + ((int64_t)split * p.M + m) * p.N;
+      float* o = p.part + ((int64_t)split * p.M + m) * p.ldp;
 #pragma unroll
       for (int j = 0; j < kNJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int n = nl + j * kBStep + e;
-          if (n < p.N) o[n] = acc[i][j][e];
-        }
+        if (nl + j * 4 < p.N) *reinterpret_cast<floatx4*>(o + nl + j * 4) = acc[i][j];
       continue;
     }
     if (p.add) {
@@ -435,6 +431,33 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   }
 }
 
+// C from the splits' sums: four columns per thread, the splits in order.
+template <typename T>
+__global__ __launch_bounds__(256) void fp8_join_kernel(Fp8GemmArgs p) {
+  const int64_t quads = p.ldp / 4, x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (x >= p.M * quads) return;
+  const int64_t m = x / quads;
+  const int n = static_cast<int>(x % quads) * 4;
+  const float* src = p.part + m * p.ldp + n;
+  floatx4 v = *reinterpret_cast<const floatx4*>(src);
+#pragma unroll 4
+  for (int i = 1; i < p.splits; ++i) v += *reinterpret_cast<const floatx4*>(src + i * (p.M * p.ldp));
+  if (p.add) {
+    const float4 ad = p.add_bf ? load4<uint16_t>(static_cast<const uint16_t*>(p.add) + m * p.ldadd, n, p.N, p.cvec)
+                               : load4<float>(static_cast<const float*>(p.add) + m * p.ldadd, n, p.N, p.cvec);
+    v[0] += ad.x; v[1] += ad.y; v[2] += ad.z; v[3] += ad.w;
+  }
+  T* const o = static_cast<T*>(p.c) + m * p.ldc;
+  if (p.cvec && n + 4 <= p.N) {
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(o + n) = pack_bf16x4(v);
+    else *reinterpret_cast<floatx4*>(o + n) = v;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < p.N) store_from_f32<T>(o, n + e, v[e]);
+  }
+}
+
 constexpr int kResident = 256;   // workgroups of eight waves that the chip holds at once
 
 template <int kMode, bool kRowB, int kWM, int kWN, int kMI, int kNJ, bool kDma, bool kWhole>
@@ -466,15 +489,15 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_fp8_matmul(const Fp8GemmArgs& a0, bool c_bf, bool e8m0, hipStream_t s) {
-  Fp8GemmArgs a = a0;
-  a.e8m0 = e8m0;
-  a.c_bf = c_bf;
-  a.splits = 1;
-  a.part = nullptr;
-  a.kchunk = (a.K + kFp8Block - 1) / kFp8Block;
+hipError_t launch_fp8_matmul(const Fp8GemmArgs& a, hipStream_t s) {
   if (a.M <= kFewRows) return launch_fp8_few(a, s);
-  return c_bf ? launch_fp8_gemm(a, s) : launch_fp8_exact(a, s);
+  const hipError_t e = a.c_bf ? launch_fp8_gemm(a, s) : launch_fp8_exact(a, s);
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t quads = (int64_t)a.M * (a.ldp / 4);
+  const dim3 grid(static_cast<uint32_t>((quads + 255) / 256));
+  if (a.c_bf) hipLaunchKernelGGL(fp8_join_kernel<uint16_t>, grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(fp8_join_kernel<float>, grid, dim3(256), 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace ortho

@@ -492,8 +492,19 @@ constexpr int64_t kMaxGrid = (int64_t{1} << 31) - 1;
 
 bool plan_fp8_matmul(int64_t m, int64_t n, int64_t k, Fp8MatmulPlan* p) {
   if (m < 1 || n < 1 || k < 1 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return false;
-  if (cdiv(m, 128) * cdiv(n, 128) > kMaxGrid) return false;
-  p->total_bytes = kWsAlign;
+  const int64_t tiles = cdiv(m, 128) * cdiv(n, 128), nkb = cdiv(k, kFp8BlockSize);
+  if (tiles > kMaxGrid) return false;
+  // at least three blocks each: a workgroup's first copies take about two
+  // blocks' time to arrive
+  int64_t splits = m <= kFewRowsMax ? 1 : kTargetWorkgroups / tiles;
+  if (splits > nkb / 3) splits = nkb / 3;
+  if (splits < 1) splits = 1;
+  const int64_t kchunk = cdiv(nkb, splits);
+  splits = cdiv(nkb, kchunk);
+  p->splits = static_cast<int>(splits);
+  p->kchunk = static_cast<int>(kchunk);
+  p->ldp = cdiv(n, 4) * 4;
+  p->total_bytes = splits == 1 ? kWsAlign : align_up(static_cast<size_t>(splits) * m * p->ldp * 4);
   return true;
 }
 

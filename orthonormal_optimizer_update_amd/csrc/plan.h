@@ -158,7 +158,13 @@ constexpr int64_t kFp8BlockSize = 128;
 // Longest row of the norms: it stays in one workgroup's registers.
 constexpr int64_t kNormMaxCols = 32768;
 
+// The product on 128 x 128 tiles of C splits K where there are fewer tiles than
+// two per CU: `splits` ranges of `kchunk` blocks of 128, whose fp32 sums (rows
+// of ldp) meet in the workspace and are added in order.
+constexpr int64_t kFewRowsMax = 64;       // rows of A that take the kernel for few rows
 struct Fp8MatmulPlan {
+  int splits, kchunk;
+  int64_t ldp;
   size_t total_bytes;
 };
 bool plan_fp8_matmul(int64_t m, int64_t n, int64_t k, Fp8MatmulPlan* out);
