@@ -72,6 +72,15 @@ __device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
   return reinterpret_cast<const uint8_t*>((static_cast<uint64_t>(hi) << 32) | lo);
 }
 
+// One of two kernel arguments by a condition that is the same for the whole
+// wave.  Both are read by scalar loads first: left alone, the compiler chooses
+// between their addresses and reads the argument block through vector memory.
+template <typename T>
+__device__ __forceinline__ T pick(bool first, T a, T b) {
+  asm("" : "+s"(a), "+s"(b));
+  return first ? a : b;
+}
+
 // 16 codes from column k of a row of K; zero codes from column K on.  Any byte.
 // A piece that the row's end cuts is loaded from 16 columns before the end and
 // shifted, so that no load depends on a branch.

@@ -47,9 +47,9 @@ __global__ __launch_bounds__(256, 2) void fp8_exact_kernel(Fp8GemmArgs p) {
   // copy g of this wave: rows 8 (8 wave + g) .. + 7 of the stage (A's, then
   // B's); lane = 8 * (row of the 8) + chunk position
   const bool is_a = wave < 2;
-  const int last = (is_a ? p.M : p.N) - 1, row0 = is_a ? m0 : n0 - BM;
-  const int64_t ld = is_a ? p.lda : p.ldb;
-  const uint8_t* const matrix = is_a ? p.a : p.b;
+  const int last = pick(is_a, p.M, p.N) - 1, row0 = is_a ? m0 : n0 - BM;
+  const int64_t ld = pick(is_a, p.lda, p.ldb);
+  const uint8_t* const matrix = pick(is_a, p.a, p.b);
   auto stage_row = [&](int g) ORTHO_INLINE { return (wave * 8 + g) * 8 + (lane >> 3); };
   auto matrix_row = [&](int r) ORTHO_INLINE { return min(row0 + r, last); };
   auto chunk_of = [&](int g) ORTHO_INLINE { return swz<false>(stage_row(g), lane & 7); };
@@ -62,10 +62,10 @@ __global__ __launch_bounds__(256, 2) void fp8_exact_kernel(Fp8GemmArgs p) {
   const unsigned lds0 = uniform((unsigned)(uintptr_t)(lds_ptr_t)(smem));
   const unsigned scales0 = uniform((unsigned)(uintptr_t)(lds_ptr_t)(&scales[0][0]));
   // scales: the wave's 64 rows of the stage, one per lane (bytes as words)
-  const int shift = is_a ? p.sa.shift : p.sb.shift;
-  const int64_t s_ld = (is_a ? p.sa.ld : p.sb.ld) * (kE8m0 ? 1 : 4);
+  const int shift = pick(is_a, p.sa.shift, p.sb.shift);
+  const int64_t s_ld = pick(is_a, p.sa.ld, p.sb.ld) * (kE8m0 ? 1 : 4);
   const uint8_t* const s_base =
-      uniform_ptr(static_cast<const uint8_t*>(is_a ? p.sa.p : p.sb.p) + (from >> shift) * s_ld);
+      uniform_ptr(static_cast<const uint8_t*>(pick(is_a, p.sa.p, p.sb.p)) + (from >> shift) * s_ld);
   const int s_row = (matrix_row(wave * 64 + lane) >> shift) - (from >> shift);
 
   auto copy_scales = [&](int kt, int buf) ORTHO_INLINE {
@@ -99,8 +99,10 @@ __global__ __launch_bounds__(256, 2) void fp8_exact_kernel(Fp8GemmArgs p) {
     }
   };
   auto patch_tail = [&](int st) ORTHO_INLINE {
+    int x = lane;
+    asm volatile("" : "+v"(x));   // nothing of this is worked out ahead of the loop over k
 #pragma unroll 1
-    for (int x = lane; x < 64 * 8; x += 64) {
+    for (; x < 64 * 8; x += 64) {
       const int r = wave * 64 + (x >> 3), c = x & 7;
       if (c < (tail >> 4)) continue;
       *reinterpret_cast<uint4*>(smem + st * kStage + (r * 8 + swz<false>(r, c)) * 16) =

@@ -16,6 +16,8 @@
 // accumulates across blocks by itself.  With fp32 scales, and with the bf16
 // instruction, a block's sum starts at zero and joins the accumulators with
 // one fused multiply-add per element.
+#include <limits.h>
+
 #include "fp8_gemm.h"
 
 namespace ortho {
@@ -97,9 +99,15 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
     const int half = (g - kCopyB) / kCopyA, x = (wave * kCopyA + (g - kCopyB) % kCopyA) * 8;
     return x / (8 * kMI) * (16 * kMI) + half * (8 * kMI) + x % (8 * kMI);
   };
-  auto row_of = [&](int g) ORTHO_INLINE { return rows8(g) + (lane >> 3); };
   auto place = [&](int r, int c) ORTHO_INLINE { return r < BM ? swz<false>(r, c) : swz<true>(r - BM, c); };
-  auto chunk_of = [&](int g) ORTHO_INLINE { return place(row_of(g), lane & 7); };
+  const int sub = lane >> 3;
+  auto chunk_of = [&](int g) ORTHO_INLINE {
+    return g < kCopyB ? swz<true>(rows8(g) - BM + sub, lane & 7) : swz<false>(rows8(g) + sub, lane & 7);
+  };
+  auto row_of = [&](int g) ORTHO_INLINE {   // of the operand
+    if (g < kCopyB) return min(n0 + rows8(g) - BM + sub, kWhole ? INT_MAX : p.N - 1);
+    return min(m0 + rows8(g) + sub, kWhole ? INT_MAX : p.M - 1);
+  };
   auto matrix_row = [&](int r) ORTHO_INLINE {
     if (kWhole) return r < BM ? m0 + r : n0 + r - BM;
     return r < BM ? min(m0 + r, p.M - 1) : min(n0 + r - BM, p.N - 1);
@@ -107,16 +115,14 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   // What a lane adds to a copy's base address.  kWhole: its row of the 8, and
   // the chunk that belongs at its position (the part of swz that depends on
   // the 8 rows is uniform); otherwise rows past the matrix are the last row.
-  const int sub = lane >> 3;
   const unsigned row_a = sub * static_cast<unsigned>(p.lda), row_b = sub * static_cast<unsigned>(p.ldb);
   const unsigned chunk_a = swz<false>(sub, lane & 7) * 16, chunk_b = swz<true>(sub, lane & 7) * 16;
   unsigned voff[kWhole ? 1 : kCopies];
   if constexpr (!kWhole) {
 #pragma unroll
-    for (int g = 0; g < kCopies; ++g) {
-      const int r = row_of(g), mr = matrix_row(r);
-      voff[g] = static_cast<unsigned>(r < BM ? (mr - m0) * p.lda : (mr - n0) * p.ldb) + chunk_of(g) * 16;
-    }
+    for (int g = 0; g < kCopies; ++g)
+      voff[g] = (g < kCopyB ? (row_of(g) - n0) * static_cast<unsigned>(p.ldb)
+                            : (row_of(g) - m0) * static_cast<unsigned>(p.lda)) + chunk_of(g) * 16;
   }
   const unsigned scales0 = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(lds_ptr_t)(&scales[0][0]));
   const unsigned lds0 = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(lds_ptr_t)(smem));
@@ -144,16 +150,17 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
       const int64_t k0 = kt == tail_kt ? 0 : (int64_t)kt * 128;   // the last tile's offsets hold its k
       dma16(voff[g], uniform_ptr((is_a ? a0 : b0) + k0), at);
     } else {
-      const int r = row_of(g), mr = matrix_row(r);
-      const uint8_t* src = r < BM ? p.a + (int64_t)mr * p.lda : p.b + (int64_t)mr * p.ldb;
+      const uint8_t* src = g < kCopyB ? p.b + row_of(g) * p.ldb : p.a + row_of(g) * p.lda;
       *reinterpret_cast<uint4*>(smem + st * kStage + r8 * 128 + lane * 16) =
           load_codes16(src, kt * 128 + chunk_of(g) * 16, p.K);
     }
   };
   // The last tile's codes from the first chunk that is not whole on.
   auto patch_tail = [&](int st) ORTHO_INLINE {
+    int x = t;
+    asm volatile("" : "+v"(x));   // nothing of this is worked out ahead of the loop over k
 #pragma unroll 1
-    for (int x = t; x < (BM + BN) * 8; x += kThreads) {
+    for (; x < (BM + BN) * 8; x += kThreads) {
       const int r = x >> 3, c = x & 7;
       if (c < (tail >> 4)) continue;
       const int mr = matrix_row(r);
@@ -167,12 +174,13 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   constexpr bool kByteOnly = kMode == kHardware;
   constexpr int scale_size = kByteOnly ? 1 : 4;
   const bool scales_a = wave * 64 < BM;
-  const int s_shift = scales_a ? p.sa.shift : p.sb.shift;
-  const int64_t s_ld = (scales_a ? p.sa.ld : p.sb.ld) * scale_size;
+  const int s_shift = pick(scales_a, p.sa.shift, p.sb.shift);
+  const int64_t s_ld = pick(scales_a, p.sa.ld, p.sb.ld) * scale_size;
+  const uint8_t* const s_all = static_cast<const uint8_t*>(pick(scales_a, p.sa.p, p.sb.p));
   const int s_first = (scales_a ? m0 : n0) >> s_shift;
-  const uint8_t* s0 =
-      uniform_ptr(static_cast<const uint8_t*>(scales_a ? p.sa.p : p.sb.p) + s_first * s_ld);
-  const int s_row = (matrix_row(wave * 64 + lane) >> s_shift) - s_first;
+  const uint8_t* s0 = uniform_ptr(s_all + s_first * s_ld);
+  const int s_at = (scales_a ? m0 : n0 - BM) + wave * 64 + lane;
+  const int s_row = ((kWhole ? s_at : min(s_at, pick(scales_a, p.M, p.N) - 1)) >> s_shift) - s_first;
   auto copy_scales = [&](int kt, int st) ORTHO_INLINE {
     const uint8_t* base = s0 + (int64_t)kt * scale_size;
     if constexpr (kDma) {
@@ -249,8 +257,7 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
       place_unit(ahead_unit, m, n, sp);
       a0 = uniform_ptr(p.a + (int64_t)m * p.lda);
       b0 = uniform_ptr(p.b + (int64_t)n * p.ldb);
-      s0 = uniform_ptr(static_cast<const uint8_t*>(scales_a ? p.sa.p : p.sb.p) +
-                       ((scales_a ? m : n) >> s_shift) * s_ld);
+      s0 = uniform_ptr(s_all + ((scales_a ? m : n) >> s_shift) * s_ld);
       ahead = sp * p.kchunk;
       ahead_end = min(ahead + p.kchunk, nkb);
     }
