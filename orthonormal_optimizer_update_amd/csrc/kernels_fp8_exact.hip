@@ -99,14 +99,13 @@ __global__ __launch_bounds__(256, 2) void fp8_exact_kernel(Fp8GemmArgs p) {
     }
   };
   auto patch_tail = [&](int st) ORTHO_INLINE {
-    int x = lane;
-    asm volatile("" : "+v"(x));   // nothing of this is worked out ahead of the loop over k
+    int r = wave * 64 + lane;
+    asm volatile("" : "+v"(r));   // nothing of this is worked out ahead of the loop over k
+    uint4 u = load_codes16(matrix + matrix_row(r) * ld, (nkb - 1) * 128 + (tail & ~15), p.K);
 #pragma unroll 1
-    for (; x < 64 * 8; x += 64) {
-      const int r = wave * 64 + (x >> 3), c = x & 7;
-      if (c < (tail >> 4)) continue;
-      *reinterpret_cast<uint4*>(smem + st * kStage + (r * 8 + swz<false>(r, c)) * 16) =
-          load_codes16(matrix + matrix_row(r) * ld, (nkb - 1) * 128 + c * 16, p.K);
+    for (int c = tail >> 4; c < 8; ++c) {
+      *reinterpret_cast<uint4*>(smem + st * kStage + (r * 8 + swz<false>(r, c)) * 16) = u;
+      u = make_uint4(0, 0, 0, 0);
     }
   };
   auto scale_value = [&](uint32_t u) ORTHO_INLINE {

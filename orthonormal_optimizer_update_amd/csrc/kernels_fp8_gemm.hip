@@ -157,16 +157,15 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   };
   // The last tile's codes from the first chunk that is not whole on.
   auto patch_tail = [&](int st) ORTHO_INLINE {
-    int x = t;
-    asm volatile("" : "+v"(x));   // nothing of this is worked out ahead of the loop over k
+    int r = t;
+    asm volatile("" : "+v"(r));   // nothing of this is worked out ahead of the loop over k
+    const int mr = matrix_row(r);
+    const uint8_t* src = r < BM ? p.a + (int64_t)mr * p.lda : p.b + (int64_t)mr * p.ldb;
+    uint4 u = load_codes16(src, (nkb - 1) * 128 + (tail & ~15), p.K);
 #pragma unroll 1
-    for (; x < (BM + BN) * 8; x += kThreads) {
-      const int r = x >> 3, c = x & 7;
-      if (c < (tail >> 4)) continue;
-      const int mr = matrix_row(r);
-      const uint8_t* src = r < BM ? p.a + (int64_t)mr * p.lda : p.b + (int64_t)mr * p.ldb;
-      *reinterpret_cast<uint4*>(smem + st * kStage + (r * 8 + place(r, c)) * 16) =
-          load_codes16(src, (nkb - 1) * 128 + c * 16, p.K);
+    for (int c = tail >> 4; c < 8; ++c) {
+      *reinterpret_cast<uint4*>(smem + st * kStage + (r * 8 + place(r, c)) * 16) = u;
+      u = make_uint4(0, 0, 0, 0);
     }
   };
 
@@ -387,8 +386,45 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
     }
   }
 
+  // Rows of C (or Add) at any byte: through LDS, 64 rows of the wave's 64
+  // columns at a time, so that a store covers neighbouring columns of one row
+  // (element by element from the accumulators, 64 separate pieces each,
+  // 1000 x 1537 x 1111 took twice as long).
+  if (!kWhole && !p.cvec && !p.part) {
+    __syncthreads();   // every wave is done with the stages
+    float* const rows = reinterpret_cast<float*>(smem) + wave * (64 * 64);
+#pragma unroll
+    for (int h = 0; h < kMI / 4; ++h) {
+      // row r's quads of columns at q ^ (r % 16)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < kNJ; ++j)
+          *reinterpret_cast<floatx4*>(rows + (i * 16 + l16) * 64 + ((lg * 4 + j) ^ l16) * 4) = acc[h * 4 + i][j];
+      const int n = n0 + wn + lane, m1 = m0 + wm + h * 64, left = n < p.N ? p.M - m1 : 0;
+      auto value = [&](int r) ORTHO_INLINE {
+        return rows[r * 64 + (((lane >> 2) ^ (r & 15)) << 2) + (lane & 3)];
+      };
+      uint16_t* const o = static_cast<uint16_t*>(p.c) + m1 * p.ldc + n;
+      if (!p.add) {
+#pragma unroll 16
+        for (int r = 0; r < 64; ++r)
+          if (r < left) o[r * p.ldc] = to_bf16_bits(value(r));
+      } else {
+#pragma unroll 4
+        for (int r = 0; r < 64; ++r)
+          if (r < left) {
+            const int64_t at = (m1 + r) * p.ldadd + n;
+            o[r * p.ldc] = to_bf16_bits(value(r) + (p.add_bf ? bf16_bits_to_f32(static_cast<const uint16_t*>(p.add)[at])
+                                                            : static_cast<const float*>(p.add)[at]));
+          }
+      }
+    }
+    return;
+  }
+
   // Columns of piece j of a lane: four, next to those of piece j + 1 for bf16.
-  const bool whole = kWhole || (n0 + wn + 64 <= p.N && p.cvec);
+  const bool whole = kWhole || n0 + wn + 64 <= p.N;
 #pragma unroll
   for (int i = 0; i < kMI; ++i) {
     const int m = m0 + wm + i * 16 + l16;

@@ -485,6 +485,7 @@ ortho_status check_ws(const void* ws, size_t have, size_t need) {
   return reinterpret_cast<uintptr_t>(ws) % kWsAlign != 0 ? ORTHO_E_WORKSPACE : ORTHO_OK;
 }
 
+constexpr int64_t kCus = 256;
 // Workgroups of a launch are counted in 31 bits.
 constexpr int64_t kMaxGrid = (int64_t{1} << 31) - 1;
 
@@ -494,11 +495,14 @@ bool plan_fp8_matmul(int64_t m, int64_t n, int64_t k, Fp8MatmulPlan* p) {
   if (m < 1 || n < 1 || k < 1 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return false;
   const int64_t tiles = cdiv(m, 128) * cdiv(n, 128), nkb = cdiv(k, kFp8BlockSize);
   if (tiles > kMaxGrid) return false;
-  // at least three blocks each: a workgroup's first copies take about two
-  // blocks' time to arrive
-  int64_t splits = m <= kFewRowsMax ? 1 : kTargetWorkgroups / tiles;
+  // One workgroup per CU, of at least three blocks (its first copies take about
+  // two blocks' time to arrive), and only where the blocks saved, about 1 us
+  // each, outweigh the second launch and its traffic, about 6 us:
+  // 1000 x 1536 x 1024 takes 11.4 us whole and 17.9 in two, 65 x 2048 x 8192
+  // 57 us whole and 15 in 16.
+  int64_t splits = m <= kFewRowsMax ? 1 : kCus / tiles;
   if (splits > nkb / 3) splits = nkb / 3;
-  if (splits < 1) splits = 1;
+  if (splits < 1 || nkb - cdiv(nkb, splits) < 8) splits = 1;
   const int64_t kchunk = cdiv(nkb, splits);
   splits = cdiv(nkb, kchunk);
   p->splits = static_cast<int>(splits);

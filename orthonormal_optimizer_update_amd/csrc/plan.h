@@ -159,7 +159,7 @@ constexpr int64_t kFp8BlockSize = 128;
 constexpr int64_t kNormMaxCols = 32768;
 
 // The product on 128 x 128 tiles of C splits K where there are fewer tiles than
-// two per CU: `splits` ranges of `kchunk` blocks of 128, whose fp32 sums (rows
+// CUs: `splits` ranges of `kchunk` blocks of 128, whose fp32 sums (rows
 // of ldp) meet in the workspace and are added in order.
 constexpr int64_t kFewRowsMax = 64;       // rows of A that take the kernel for few rows
 struct Fp8MatmulPlan {
