@@ -84,7 +84,7 @@ struct Fp8GemmArgs {
   float* part;              // splits x M x ldp partial sums (splits > 1), else null
   int64_t ldp;
 };
-constexpr int kFewRows = 64;         // rows of A that launch_fp8_few takes (must match plan.h)
+constexpr int kFewRows = 32;         // rows of A that launch_fp8_few takes (must match plan.h)
 hipError_t launch_fp8_few(const Fp8GemmArgs& a, hipStream_t s);     // M <= kFewRows
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s);    // bf16 C
 hipError_t launch_fp8_exact(const Fp8GemmArgs& a, hipStream_t s);   // fp32 C

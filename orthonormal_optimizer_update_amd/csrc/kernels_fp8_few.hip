@@ -8,17 +8,22 @@ namespace ortho {
 
 namespace {
 
-// 16 rows of B per workgroup against 16 kMB rows of A.  The kWaves waves share
+// 16 kMB rows of A against 16 rows of B per workgroup.  The kWaves waves share
 // the blocks of K among them (block b goes to wave b % kWaves), hold kAhead
 // blocks' loads in flight straight from memory into registers, and their sums
 // are added in LDS in a fixed order.  Codes become bf16, which holds them
 // exactly, whatever C's type: at this size the conversions are free.
+//
+// The workgroups that share 16 rows of B follow each other on one XCD
+// (workgroup id mod 8), where all but the first find them in the L2.
 template <bool kE8m0, int kMB, int kWaves, int kAhead>
 __global__ __launch_bounds__(kWaves * 64) void fp8_few_kernel(Fp8GemmArgs p) {
   __shared__ __attribute__((aligned(16))) float part[kWaves][kMB][16][20];   // [m][n], rows 16 bytes apart in banks
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, lg = lane >> 4;
-  const int n0 = blockIdx.x * 16;
+  const int parts = (p.M + 16 * kMB - 1) / (16 * kMB), turn = blockIdx.x >> 3;
+  const int m0 = turn % parts * (16 * kMB), n0 = ((blockIdx.x & 7) + 8 * (turn / parts)) * 16;
+  if (n0 >= p.N) return;
   const int nkb = (p.K + kFp8Block - 1) / kFp8Block;
   // Lane l holds codes 16 lg .. and 64 + 16 lg .. of row l16 of a block (the
   // order of k within a block is free).
@@ -50,7 +55,7 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_few_kernel(Fp8GemmArgs p) {
       }
 #pragma unroll
       for (int i = 0; i < kMB; ++i) {
-        const int m = min(i * 16 + l16, p.M - 1);
+        const int m = min(m0 + i * 16 + l16, p.M - 1);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if constexpr (decltype(checked)::value) ra[x][i][h] = load_codes16(p.a + m * p.lda, k + 64 * h, p.K);
@@ -91,7 +96,7 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_few_kernel(Fp8GemmArgs p) {
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) v += part[w][i][m][n];
-    const int64_t row = i * 16 + m;
+    const int64_t row = m0 + i * 16 + m;
     if (row >= p.M || n0 + n >= p.N) continue;
     if (p.add)
       v += p.add_bf ? bf16_bits_to_f32(static_cast<const uint16_t*>(p.add)[row * p.ldadd + n0 + n])
@@ -104,7 +109,8 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_few_kernel(Fp8GemmArgs p) {
 template <bool kE8m0, int kMB, int kAhead>
 void by_depth(const Fp8GemmArgs& a, hipStream_t s) {
   // one wave for every kAhead blocks of K, 4 to 16
-  const dim3 grid((a.N + 15) / 16);
+  const int tiles = (a.N + 15) / 16, parts = (a.M + 16 * kMB - 1) / (16 * kMB);
+  const dim3 grid((tiles + 7) / 8 * 8 * parts);
   const int nkb = (a.K + kFp8Block - 1) / kFp8Block;
   if (nkb <= 4 * kAhead)
     hipLaunchKernelGGL((fp8_few_kernel<kE8m0, kMB, 4, kAhead>), grid, dim3(256), 0, s, a);
@@ -116,9 +122,12 @@ void by_depth(const Fp8GemmArgs& a, hipStream_t s) {
 
 template <bool kE8m0>
 void by_rows(const Fp8GemmArgs& a, hipStream_t s) {
+  // 16 or 32 rows of A per workgroup.  Where B's rows alone do not give every
+  // CU one, 16 (24 x 2048 x 8192: 15.0 us with 32 rows, 10.8 with 16;
+  // 32 x 8192 x 2048: 9.4 and 12.6 us).
   if (a.M <= 16) by_depth<kE8m0, 1, 4>(a, s);
-  else if (a.M <= 32) by_depth<kE8m0, 2, 2>(a, s);
-  else by_depth<kE8m0, 4, 1>(a, s);
+  else if ((a.N + 15) / 16 >= 256) by_depth<kE8m0, 2, 2>(a, s);
+  else by_depth<kE8m0, 1, 2>(a, s);
 }
 
 }  // namespace
