@@ -207,11 +207,11 @@ def matmul_reference(a, sa, bra, b, sb, brb):
 
 def group_tops(a, sa, bra, b, sb, brb):
     """Sum over the groups of eight consecutive k of the largest product."""
-    A = (ref.e4m3_values(a) * ref.expand(ref.scale_values(sa), *a.shape, bra)).abs().float().cuda()
-    B = (ref.e4m3_values(b) * ref.expand(ref.scale_values(sb), *b.shape, brb)).abs().float().cuda()
+    A = (ref.e4m3_values(a) * ref.expand(ref.scale_values(sa), *a.shape, bra)).abs().cuda()
+    B = (ref.e4m3_values(b) * ref.expand(ref.scale_values(sb), *b.shape, brb)).abs().cuda()
     total = torch.zeros(a.size(0), b.size(0), dtype=torch.float64, device="cuda")
     for k in range(0, a.size(1), 8):
-        top = torch.zeros(a.size(0), b.size(0), device="cuda")
+        top = torch.zeros(a.size(0), b.size(0), dtype=torch.float64, device="cuda")
         for j in range(k, min(k + 8, a.size(1))):
             top = torch.maximum(top, A[:, j:j + 1] * B[:, j:j + 1].t())
         total += top
