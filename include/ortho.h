@@ -299,8 +299,8 @@ ortho_status dion2_step(ortho_mat X, ortho_mat G, ortho_mat M, int32_t k, int32_
  * applied by the matrix instructions themselves and make every scaling exact;
  * fp32 scales use a block's whole 8-bit range.
  *
- * Rows of codes that start at multiples of 16 bytes (data and ld) are read and
- * written fastest; any other layout is accepted. */
+ * fp8_matmul reads rows of codes that start at multiples of 16 bytes (data and
+ * ld) fastest; any other layout is accepted. */
 
 /* X (m x n, ORTHO_F32 or ORTHO_BF16) as 8-bit codes and scales.
  *   block_rows  1 (blocks of 1 x 128: activations, gradients) or 128 (blocks of
@@ -327,9 +327,10 @@ ortho_status fp8_quantize(ortho_mat X, int32_t block_rows, const ortho_mat* Q, c
  *   W     1 x n, ORTHO_F32 or X's dtype.
  *   eps   >= 0 and finite, else ORTHO_E_PARAM.
  *   Sum   NULL, or m x n of X's dtype: receives r (the next residual, and what
- *         rms_norm_backward takes as X).  May be the same memory as X or Res.
+ *         rms_norm_backward takes as X).  May be the same memory as X or Res,
+ *         with the same ld (else ORTHO_E_LAYOUT).
  *   Y     NULL, or m x n of X's dtype: receives y, e.g. to be quantised along
- *         the tokens for the weight gradient.
+ *         the tokens for the weight gradient.  Memory of its own.
  *   Q, S  m x n ORTHO_E4M3, and m x ceil(n / 128). */
 ortho_status rms_norm_fp8(ortho_mat X, const ortho_mat* Res, ortho_mat W, float eps,
                           const ortho_mat* Sum, const ortho_mat* Y, ortho_mat Q, ortho_mat S,
@@ -349,7 +350,7 @@ size_t ortho_rms_norm_backward_workspace_size(int64_t m, int64_t n);
  *   dSum  NULL, or m x n of X's dtype: the gradient that reaches Sum along the
  *         residual, added to dX.
  *   dX    m x n of X's dtype: the gradient of X and of Res.  May be the same
- *         memory as dY, X or dSum.
+ *         memory as dY, X or dSum, with the same ld (else ORTHO_E_LAYOUT).
  *   dW    1 x n, ORTHO_F32, overwritten; the rows are added in a fixed order.
  *   ws    >= ortho_rms_norm_backward_workspace_size(m, n) bytes. */
 ortho_status rms_norm_backward(ortho_mat dY, ortho_mat X, ortho_mat W, float eps,
@@ -370,9 +371,10 @@ size_t ortho_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
  *   ws     >= ortho_fp8_matmul_workspace_size(m, n, k) bytes.
  * Products are accumulated in fp32, in an order that depends on the sizes and
  * layouts alone.  With an ORTHO_F32 C every product counts in full.  With an
- * ORTHO_BF16 C the 8-bit matrix instruction is used, which cuts each product
- * below 2^-13 of the largest of its group of eight neighbours along k (about
- * 1e-5 of the result, against the 2^-9 of C's rounding).  A NaN code or scale reaches the elements of C that it enters into,
+ * ORTHO_BF16 C of more than a few rows the 8-bit matrix instruction is used,
+ * which cuts each product below 2^-13 of the largest of its group of eight
+ * neighbours along k (about 1e-5 of the result, against the 2^-9 of C's
+ * rounding).  A NaN code or scale reaches the elements of C that it enters into,
  * and no others. */
 ortho_status fp8_matmul(ortho_mat A, ortho_mat SA, ortho_mat B, ortho_mat SB, ortho_mat C,
                         const ortho_mat* Add, void* ws, size_t ws_bytes, void* stream);

@@ -35,13 +35,10 @@ ortho_status fp8_quantize(ortho_mat X, int32_t block_rows, const ortho_mat* Q, c
   QuantArgs a{};
   a.x = X.data;
   a.ldx = X.ld;
-  a.vec = rows_at(&X, 16);
   a.q = static_cast<uint8_t*>(data_of(Q));
   a.ldq = ld_of(Q);
-  a.qvec = rows_at(Q, 8);
   a.qt = static_cast<uint8_t*>(data_of(QT));
   a.ldqt = ld_of(QT);
-  a.qtvec = rows_at(QT, 16);
   a.s = data_of(S);
   a.lds = ld_of(S);
   a.st = data_of(ST);
@@ -64,7 +61,6 @@ ortho_status rms_norm_fp8(ortho_mat X, const ortho_mat* Res, ortho_mat W, float 
   a.ldres = ld_of(Res);
   a.w = W.data;
   a.w_bf = W.dtype == ORTHO_BF16;
-  a.wvec = reinterpret_cast<uintptr_t>(W.data) % 16 == 0;
   a.sum = data_of(Sum);
   a.ldsum = ld_of(Sum);
   a.y = data_of(Y);
@@ -76,8 +72,6 @@ ortho_status rms_norm_fp8(ortho_mat X, const ortho_mat* Res, ortho_mat W, float 
   a.eps = eps;
   a.m = static_cast<int>(X.rows);
   a.n = static_cast<int>(X.cols);
-  a.vec = rows_at(&X, 16) && rows_at(Res, 16) && rows_at(Sum, 16) && rows_at(Y, 16);
-  a.qvec = rows_at(&Q, 8);
   return done(launch_rms_norm_fp8(a, X.dtype == ORTHO_BF16, S.dtype == ORTHO_E8M0, as_stream(stream)));
 }
 
@@ -100,7 +94,6 @@ ortho_status rms_norm_backward(ortho_mat dY, ortho_mat X, ortho_mat W, float eps
   a.ldx = X.ld;
   a.w = W.data;
   a.w_bf = W.dtype == ORTHO_BF16;
-  a.wvec = reinterpret_cast<uintptr_t>(W.data) % 16 == 0;
   a.dsum = data_of(dSum);
   a.lddsum = ld_of(dSum);
   a.dx = dX.data;
@@ -112,7 +105,6 @@ ortho_status rms_norm_backward(ortho_mat dY, ortho_mat X, ortho_mat W, float eps
   a.m = static_cast<int>(X.rows);
   a.n = static_cast<int>(X.cols);
   a.groups = plan.groups;
-  a.vec = rows_at(&dY, 16) && rows_at(&X, 16) && rows_at(dSum, 16) && rows_at(&dX, 16);
   return done(launch_rms_norm_backward(a, X.dtype == ORTHO_BF16, as_stream(stream)));
 }
 

@@ -26,10 +26,8 @@ struct ScaleArg {
 struct QuantArgs {
   const void* x;
   int64_t ldx;
-  int vec;                  // X's rows start at multiples of 16 bytes
   uint8_t *q, *qt;          // codes by rows (m x n) and transposed (n x m); either may be null
   int64_t ldq, ldqt;
-  int qvec, qtvec;          // rows of 16-byte multiples
   void *s, *st;
   int64_t lds, ldst;
   int m, n;
@@ -47,9 +45,7 @@ struct NormArgs {
   int64_t lds;
   float eps;
   int m, n;
-  int vec;                  // x, res, sum, y rows of 16-byte multiples
-  int qvec;                 // q rows of 8-byte multiples
-  int w_bf, wvec;           // W is bf16; 16-byte aligned
+  int w_bf;                 // W is bf16
 };
 hipError_t launch_rms_norm_fp8(const NormArgs& a, bool bf, bool e8m0, hipStream_t s);
 
@@ -63,8 +59,7 @@ struct NormGradArgs {
   int64_t ldpart;
   float eps;
   int m, n, groups;
-  int vec;
-  int w_bf, wvec;
+  int w_bf;
 };
 hipError_t launch_rms_norm_backward(const NormGradArgs& a, bool bf, hipStream_t s);
 
@@ -158,33 +153,81 @@ __device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
   for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
 }
 
-// From column c of a row of `limit` columns; zeros past its end.
-__device__ __forceinline__ Raw8<uint16_t> load_raw8(const uint16_t* row, int c, int limit, bool vec) {
-  Raw8<uint16_t> r;
-  if (vec && c + 8 <= limit) {
-    r.a = *reinterpret_cast<const uint4*>(row + c);
-    return r;
+// The 16 bytes u without its first `cut` (a multiple of 2, 1 .. 16), zeros behind.
+__device__ __forceinline__ uint4 cut16(uint4 u, int cut) {
+  uint64_t lo = u.x | static_cast<uint64_t>(u.y) << 32, hi = u.z | static_cast<uint64_t>(u.w) << 32;
+  if (cut >= 8) {
+    lo = hi;
+    hi = 0;
+  }
+  const int s = (cut & 7) * 8;
+  if (s != 0) {
+    lo = lo >> s | hi << (64 - s);
+    hi >>= s;
+  }
+  if (cut >= 16) lo = hi = 0;
+  return make_uint4(static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
+                    static_cast<uint32_t>(hi >> 32));
+}
+
+// 16 bytes' worth of elements from column c of a row of `limit` columns; zeros
+// past its end.  The row may start at any element (the accesses need no
+// alignment); what its end cuts is loaded from further left and shifted, so
+// that no load depends on a branch.
+template <typename T>
+__device__ __forceinline__ uint4 load16(const T* row, int c, int limit) {
+  constexpr int kN = 16 / sizeof(T);
+  if (limit >= kN) {   // uniform
+    uint4 u;
+    __builtin_memcpy(&u, row + (c < limit - kN ? c : limit - kN), 16);
+    const int over = c - (limit - kN);
+    return over > 0 ? cut16(u, (over < kN ? over : kN) * static_cast<int>(sizeof(T))) : u;
   }
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (c + j < limit) w[j >> 1] |= static_cast<uint32_t>(row[c + j]) << (16 * (j & 1));
-  r.a = make_uint4(w[0], w[1], w[2], w[3]);
-  return r;
-}
-__device__ __forceinline__ Raw8<float> load_raw8(const float* row, int c, int limit, bool vec) {
-  Raw8<float> r;
-  if (vec && c + 8 <= limit) {
-    r.a = *reinterpret_cast<const uint4*>(row + c);
-    r.b = *reinterpret_cast<const uint4*>(row + c + 4);
-    return r;
+  for (int j = 0; j < kN; ++j) {
+    const T e = row[c + j < limit ? c + j : 0];
+    if (c + j < limit) {
+      if constexpr (sizeof(T) == 2) w[j >> 1] |= static_cast<uint32_t>(e) << (16 * (j & 1));
+      else w[j] = __float_as_uint(e);
+    }
   }
-  uint32_t w[8];
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ Raw8<uint16_t> load_raw8(const uint16_t* row, int c, int limit) {
+  return {load16(row, c, limit)};
+}
+__device__ __forceinline__ Raw8<float> load_raw8(const float* row, int c, int limit) {
+  return {load16(row, c, limit), load16(row, c + 4, limit)};
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int c, int limit, float (&v)[8]) {
+  unpack8(load_raw8(row, c, limit), v);
+}
+
+// Eight elements to column c of a row of `limit` columns.
+__device__ __forceinline__ void store8(uint16_t* row, int c, int limit, const float (&v)[8]) {
+  const uint2 lo = pack_bf16x4(floatx4{v[0], v[1], v[2], v[3]});
+  const uint2 hi = pack_bf16x4(floatx4{v[4], v[5], v[6], v[7]});
+  const uint4 u = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  if (c + 8 <= limit) {
+    __builtin_memcpy(row + c, &u, 16);
+    return;
+  }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = c + j < limit ? __float_as_uint(row[c + j]) : 0u;
-  r.a = make_uint4(w[0], w[1], w[2], w[3]);
-  r.b = make_uint4(w[4], w[5], w[6], w[7]);
-  return r;
+  for (int j = 0; j < 8; ++j)
+    if (c + j < limit) row[c + j] = to_bf16_bits(v[j]);
+}
+__device__ __forceinline__ void store8(float* row, int c, int limit, const float (&v)[8]) {
+  if (c + 8 <= limit) {
+    const floatx4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+    __builtin_memcpy(row + c, &lo, 16);
+    __builtin_memcpy(row + c + 4, &hi, 16);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j < limit) row[c + j] = v[j];
 }
 
 // Magnitudes as integers, which order like the values: bf16 two to a register,
@@ -241,71 +284,10 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
   return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, u, true));
 }
 
-// Eight consecutive elements from column c of a row of `limit` columns.
-template <typename T>
-__device__ __forceinline__ void load8(const T* row, int c, int limit, bool vec, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8<uint16_t>(const uint16_t* row, int c, int limit, bool vec,
-                                                float (&v)[8]) {
-  if (vec && c + 8 <= limit) {
-    const uint4 u = *reinterpret_cast<const uint4*>(row + c);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = c + j < limit ? bf16_bits_to_f32(row[c + j]) : 0.f;
-}
-template <>
-__device__ __forceinline__ void load8<float>(const float* row, int c, int limit, bool vec,
-                                             float (&v)[8]) {
-  if (vec && c + 8 <= limit) {
-    const float4 u = *reinterpret_cast<const float4*>(row + c);
-    const float4 w = *reinterpret_cast<const float4*>(row + c + 4);
-    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-    v[4] = w.x; v[5] = w.y; v[6] = w.z; v[7] = w.w;
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = c + j < limit ? row[c + j] : 0.f;
-}
-
-template <typename T>
-__device__ __forceinline__ void store8(T* row, int c, int limit, bool vec, const float (&v)[8]);
-template <>
-__device__ __forceinline__ void store8<uint16_t>(uint16_t* row, int c, int limit, bool vec,
-                                                 const float (&v)[8]) {
-  if (vec && c + 8 <= limit) {
-    const uint2 lo = pack_bf16x4(floatx4{v[0], v[1], v[2], v[3]});
-    const uint2 hi = pack_bf16x4(floatx4{v[4], v[5], v[6], v[7]});
-    *reinterpret_cast<uint4*>(row + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (c + j < limit) row[c + j] = to_bf16_bits(v[j]);
-}
-template <>
-__device__ __forceinline__ void store8<float>(float* row, int c, int limit, bool vec,
-                                              const float (&v)[8]) {
-  if (vec && c + 8 <= limit) {
-    *reinterpret_cast<float4*>(row + c) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(row + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (c + j < limit) row[c + j] = v[j];
-}
-
 // Eight codes to column c of a row of `limit` columns.
-__device__ __forceinline__ void store_codes8(uint8_t* row, int c, int limit, bool vec, uint2 u) {
-  if (vec && c + 8 <= limit) {
-    *reinterpret_cast<uint2*>(row + c) = u;
+__device__ __forceinline__ void store_codes8(uint8_t* row, int c, int limit, uint2 u) {
+  if (c + 8 <= limit) {
+    __builtin_memcpy(row + c, &u, 8);
     return;
   }
 #pragma unroll

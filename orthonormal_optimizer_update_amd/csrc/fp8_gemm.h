@@ -89,20 +89,7 @@ __device__ __forceinline__ uint4 load_codes16(const uint8_t* row, int k, int K) 
     uint4 u;
     __builtin_memcpy(&u, row + min(k, K - 16), 16);
     const int cut = k + 16 - K;   // bytes of the piece that lie past the end
-    if (cut <= 0) return u;
-    uint64_t lo = u.x | static_cast<uint64_t>(u.y) << 32, hi = u.z | static_cast<uint64_t>(u.w) << 32;
-    if (cut >= 8) {
-      lo = hi;
-      hi = 0;
-    }
-    const int s = (cut & 7) * 8;
-    if (s != 0) {
-      lo = lo >> s | hi << (64 - s);
-      hi >>= s;
-    }
-    if (cut >= 16) lo = hi = 0;
-    return make_uint4(static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
-                      static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32));
+    return cut <= 0 ? u : cut16(u, min(cut, 16));
   }
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll

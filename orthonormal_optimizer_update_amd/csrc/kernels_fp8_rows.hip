@@ -49,10 +49,10 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
   const int row = static_cast<int>(blk / nb), b = static_cast<int>(blk % nb);
   const int c = b * kFp8Block + (threadIdx.x & 15) * 8;
   float v[8];
-  load8<T>(static_cast<const T*>(a.x) + row * a.ldx, c, a.n, a.vec, v);
+  load8(static_cast<const T*>(a.x) + row * a.ldx, c, a.n, v);
   float scale, f;
   block_scale<kE8m0>(max16(top8(v)), scale, f);
-  store_codes8(a.q + row * a.ldq, c, a.n, a.qvec, codes8(v, f));
+  store_codes8(a.q + row * a.ldq, c, a.n, codes8(v, f));
   if ((threadIdx.x & 15) == 0) store_scale<kE8m0>(a.s, row * a.lds + b, scale);
 }
 
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 1) void quant_tile_kernel
   Raw8<T> x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (r0 + i < a.m) x[i] = load_raw8(static_cast<const T*>(a.x) + (r0 + i) * a.ldx, c, a.n, a.vec);
+    if (r0 + i < a.m) x[i] = load_raw8(static_cast<const T*>(a.x) + (r0 + i) * a.ldx, c, a.n);
     else x[i] = Raw8<T>{};
   }
   // largest finite magnitudes: of each row's 8 elements, and of each column's
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 1) void quant_tile_kernel
   if (a.q) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (r0 + i < a.m) store_codes8(a.q + (r0 + i) * a.ldq, c, a.n, a.qvec, codes8(v[i], fr[i]));
+      if (r0 + i < a.m) store_codes8(a.q + (r0 + i) * a.ldq, c, a.n, codes8(v[i], fr[i]));
   }
   if (a.qt) {
 #pragma unroll
@@ -200,11 +200,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 1) void quant_tile_kernel
       const uint4 u = *reinterpret_cast<const uint4*>(tile + cc * kPitch + k);
       uint8_t* dst = a.qt + (tn * 128 + cc) * a.ldqt;
       const int m0 = tm * 128 + k;
-      if (a.qtvec && m0 + 16 <= a.m) {
-        *reinterpret_cast<uint4*>(dst + m0) = u;
+      if (m0 + 16 <= a.m) {
+        __builtin_memcpy(dst + m0, &u, 16);
       } else {
-        store_codes8(dst, m0, a.m, false, make_uint2(u.x, u.y));
-        store_codes8(dst, m0 + 8, a.m, false, make_uint2(u.z, u.w));
+        store_codes8(dst, m0, a.m, make_uint2(u.x, u.y));
+        store_codes8(dst, m0 + 8, a.m, make_uint2(u.z, u.w));
       }
     }
   }
@@ -234,14 +234,15 @@ __device__ __forceinline__ void block_sum2(float& x, float& y, float (*red)[2][k
   }
 }
 
-__device__ __forceinline__ void load_w8(const void* w, int w_bf, int c, int n, bool vec, float (&v)[8]) {
-  if (w_bf) load8<uint16_t>(static_cast<const uint16_t*>(w), c, n, vec, v);
-  else load8<float>(static_cast<const float*>(w), c, n, vec, v);
+__device__ __forceinline__ void load_w8(const void* w, int w_bf, int c, int n, float (&v)[8]) {
+  if (w_bf) load8(static_cast<const uint16_t*>(w), c, n, v);
+  else load8(static_cast<const float*>(w), c, n, v);
 }
 
 // A workgroup takes the rows g, g + groups, ..., 8 kC elements per thread.  Up
 // to kC = 2 W stays in registers, and the next row's loads go out before this
-// row's sum is waited for; longer rows need the registers for themselves.
+// row's sum is waited for; longer rows need the registers for themselves (so
+// do fp32 rows of over 8192 in the gradient).
 //   r = round(x + res), t = 1 / sqrt(mean r^2 + eps), y = r t w
 // The sum is rounded to its storage type first and the rounded one is
 // normalised, so that the gradient, which sees only the stored sum, is that of
@@ -260,14 +261,14 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
   Raw8<T> x[kC], res[kC];
   if constexpr (kAhead) {
 #pragma unroll
-    for (int i = 0; i < kC; ++i) load_w8(a.w, a.w_bf, (i * kThreads + t) * 8, a.n, a.wvec, w[i]);
+    for (int i = 0; i < kC; ++i) load_w8(a.w, a.w_bf, (i * kThreads + t) * 8, a.n, w[i]);
   }
   auto load_row = [&](int64_t row) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       const int c = (i * kThreads + t) * 8;
-      x[i] = load_raw8(static_cast<const T*>(a.x) + row * a.ldx, c, a.n, a.vec);
-      if (a.res) res[i] = load_raw8(static_cast<const T*>(a.res) + row * a.ldres, c, a.n, a.vec);
+      x[i] = load_raw8(static_cast<const T*>(a.x) + row * a.ldx, c, a.n);
+      if (a.res) res[i] = load_raw8(static_cast<const T*>(a.res) + row * a.ldres, c, a.n);
     }
   };
   if (kAhead) load_row(blockIdx.x);
@@ -295,7 +296,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
     if (a.sum) {
 #pragma unroll
       for (int i = 0; i < kC; ++i)
-        store8<T>(static_cast<T*>(a.sum) + row * a.ldsum, (i * kThreads + t) * 8, a.n, a.vec, v[i]);
+        store8(static_cast<T*>(a.sum) + row * a.ldsum, (i * kThreads + t) * 8, a.n, v[i]);
     }
     block_sum2<kThreads>(sq, unused, red, turn);
     const double rsd = 1.0 / __builtin_sqrt(static_cast<double>(sq / a.n + a.eps));
@@ -306,7 +307,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
       if (c - (t & 15) * 8 >= a.n) continue;   // whole block past the row's end
       float u[8], ul[8], q[8];
       float (&wi)[8] = w[kAhead ? i : 0];
-      if (!kAhead) load_w8(a.w, a.w_bf, c, a.n, a.wvec, wi);
+      if (!kAhead) load_w8(a.w, a.w_bf, c, a.n, wi);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         u[j] = v[i][j] * wi[j];
@@ -316,10 +317,11 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
         float y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = v[i][j] * rs * wi[j];
-        store8<T>(static_cast<T*>(a.y) + row * a.ldy, c, a.n, a.vec, y);
+        store8(static_cast<T*>(a.y) + row * a.ldy, c, a.n, y);
       }
       const float top = max16(top8(u));
-      const float top_y = rsd > 0.0 ? static_cast<float>(top * rsd) : 0.f;   // 0: the row is infinite or NaN
+      // (0 where the row is infinite or NaN, or eps 0 and the row too)
+      const float top_y = rsd > 0.0 && rsd < 1e300 ? static_cast<float>(top * rsd) : 0.f;
       float scale, f;
       block_scale<kE8m0>(top_y, scale, f);
       // fp32 scales: 448 / top, unless the scale is the smallest or 1
@@ -332,7 +334,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
         const float e = fmaf(u[j], gh, -h) + fmaf(ul[j], gh, u[j] * gl);
         q[j] = __builtin_fabsf(h) <= 512.f ? h + e : v[i][j] * rs * wi[j] * f;
       }
-      store_codes8(a.q + row * a.ldq, c, a.n, a.qvec, codes8(q, 1.f));
+      store_codes8(a.q + row * a.ldq, c, a.n, codes8(q, 1.f));
       if ((t & 15) == 0) store_scale<kE8m0>(a.s, row * a.lds + c / kFp8Block, scale);
     }
   }
@@ -353,12 +355,12 @@ template <typename T, int kThreads, int kC>
 __global__ __launch_bounds__(kThreads, kC <= 2 && sizeof(T) == 2 ? 4 : 1) void rms_norm_grad_kernel(NormGradArgs a) {
   __shared__ float red[2][2][kThreads / 64];
   const int t = threadIdx.x;
-  constexpr bool kAhead = kC <= 2;
+  constexpr bool kAhead = kC <= 2 && (sizeof(T) == 2 || kThreads <= 512);
   float w[kAhead ? kC : 1][8], dw[kC][8];
   Raw8<T> nx[kC], ng[kC], nd[kAhead ? kC : 1];
 #pragma unroll
   for (int i = 0; i < kC; ++i) {
-    if (kAhead) load_w8(a.w, a.w_bf, (i * kThreads + t) * 8, a.n, a.wvec, w[kAhead ? i : 0]);
+    if (kAhead) load_w8(a.w, a.w_bf, (i * kThreads + t) * 8, a.n, w[kAhead ? i : 0]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
   }
@@ -366,10 +368,10 @@ __global__ __launch_bounds__(kThreads, kC <= 2 && sizeof(T) == 2 ? 4 : 1) void r
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       const int c = (i * kThreads + t) * 8;
-      nx[i] = load_raw8(static_cast<const T*>(a.x) + row * a.ldx, c, a.n, a.vec);
-      ng[i] = load_raw8(static_cast<const T*>(a.dy) + row * a.lddy, c, a.n, a.vec);
+      nx[i] = load_raw8(static_cast<const T*>(a.x) + row * a.ldx, c, a.n);
+      ng[i] = load_raw8(static_cast<const T*>(a.dy) + row * a.lddy, c, a.n);
       if (kAhead && a.dsum)
-        nd[kAhead ? i : 0] = load_raw8(static_cast<const T*>(a.dsum) + row * a.lddsum, c, a.n, a.vec);
+        nd[kAhead ? i : 0] = load_raw8(static_cast<const T*>(a.dsum) + row * a.lddsum, c, a.n);
     }
   };
   if (kAhead) load_row(blockIdx.x);
@@ -387,7 +389,7 @@ __global__ __launch_bounds__(kThreads, kC <= 2 && sizeof(T) == 2 ? 4 : 1) void r
       unpack8(rx[i], x);
       unpack8(rg[i], g);
       float (&wi)[8] = w[kAhead ? i : 0];
-      if (!kAhead) load_w8(a.w, a.w_bf, (i * kThreads + t) * 8, a.n, a.wvec, wi);
+      if (!kAhead) load_w8(a.w, a.w_bf, (i * kThreads + t) * 8, a.n, wi);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         sq += x[j] * x[j];
@@ -404,8 +406,8 @@ __global__ __launch_bounds__(kThreads, kC <= 2 && sizeof(T) == 2 ? 4 : 1) void r
       float o[8], x[8], g[8], d[8];
       float (&wi)[8] = w[kAhead ? i : 0];
       if (!kAhead) {
-        load_w8(a.w, a.w_bf, c, a.n, a.wvec, wi);
-        if (a.dsum) rd[0] = load_raw8(static_cast<const T*>(a.dsum) + row * a.lddsum, c, a.n, a.vec);
+        load_w8(a.w, a.w_bf, c, a.n, wi);
+        if (a.dsum) rd[0] = load_raw8(static_cast<const T*>(a.dsum) + row * a.lddsum, c, a.n);
       }
       again(rx[i]);
       again(rg[i]);
@@ -422,31 +424,33 @@ __global__ __launch_bounds__(kThreads, kC <= 2 && sizeof(T) == 2 ? 4 : 1) void r
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] += d[j];
       }
-      store8<T>(static_cast<T*>(a.dx) + row * a.lddx, c, a.n, a.vec, o);
+      store8(static_cast<T*>(a.dx) + row * a.lddx, c, a.n, o);
     }
   }
 #pragma unroll
   for (int i = 0; i < kC; ++i)
-    store8<float>(a.part + (int64_t)blockIdx.x * a.ldpart, (i * kThreads + t) * 8, a.n, true, dw[i]);
+    store8(a.part + (int64_t)blockIdx.x * a.ldpart, (i * kThreads + t) * 8, a.n, dw[i]);
 }
 
-// dw: 64 columns per workgroup, the parts shared among 16 waves and added in a
-// fixed order.
+// dw: kCols columns per workgroup, the parts shared among 1024 / kCols threads
+// of each and added in a fixed order.
+template <int kCols>
 __global__ __launch_bounds__(1024) void rms_norm_dw_kernel(NormGradArgs a) {
-  __shared__ float red[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
+  constexpr int kSlices = 1024 / kCols;
+  __shared__ float red[kSlices][kCols];
+  const int x = threadIdx.x % kCols, slice = threadIdx.x / kCols;
+  const int c = blockIdx.x * kCols + x;
   float sum = 0.f;
   if (c < a.n) {
-#pragma unroll 8
-    for (int g = wave; g < a.groups; g += 16) sum += a.part[(int64_t)g * a.ldpart + c];
+#pragma unroll 16
+    for (int g = slice; g < a.groups; g += kSlices) sum += a.part[(int64_t)g * a.ldpart + c];
   }
-  red[wave][lane] = sum;
+  red[slice][x] = sum;
   __syncthreads();
-  if (wave == 0 && c < a.n) {
+  if (slice == 0 && c < a.n) {
     float total = 0.f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) total += red[w][lane];
+    for (int w = 0; w < kSlices; ++w) total += red[w][x];
     a.dw[c] = total;
   }
 }
@@ -460,7 +464,7 @@ hipError_t by_width(int n, F f) {
   else if (n <= 2048) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
   else if (n <= 4096) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
   else if (n <= 8192) f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
-  else if (n <= 16384) f(std::integral_constant<int, 512>{}, std::integral_constant<int, 4>{});
+  else if (n <= 16384) f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
   else if (n <= 32768) f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
   else return hipErrorInvalidValue;
   return hipGetLastError();
@@ -503,7 +507,10 @@ hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
                        dim3(a.groups), dim3(decltype(th)::value), 0, s, a);
   });
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(rms_norm_dw_kernel, dim3(static_cast<uint32_t>(cdiv(a.n, 64))), dim3(1024), 0, s, a);
+  // 16 columns per workgroup (64-byte pieces of a part) where 64 would leave
+  // most CUs idle
+  if (a.n <= 4096) hipLaunchKernelGGL(rms_norm_dw_kernel<16>, dim3(static_cast<uint32_t>(cdiv(a.n, 16))), dim3(1024), 0, s, a);
+  else hipLaunchKernelGGL(rms_norm_dw_kernel<64>, dim3(static_cast<uint32_t>(cdiv(a.n, 64))), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 

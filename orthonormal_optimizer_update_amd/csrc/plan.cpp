@@ -464,6 +464,11 @@ ortho_status check_like(const ortho_mat* a, int32_t dtype, int64_t rows, int64_t
   return shape_is(*a, rows, cols) ? ORTHO_OK : ORTHO_E_SHAPE;
 }
 
+// An output that starts where an input does has to lie over it row by row.
+bool same_or_apart(const ortho_mat* out, const ortho_mat* in) {
+  return out == nullptr || in == nullptr || out->data != in->data || out->ld == in->ld || out->rows == 1;
+}
+
 // Codes of a rows x cols matrix and the scales of its br x 128 blocks.
 ortho_status check_codes(const ortho_mat& q, const ortho_mat& s, int64_t rows, int64_t cols,
                          int64_t br) {
@@ -516,7 +521,9 @@ bool plan_fp8_matmul(int64_t m, int64_t n, int64_t k, Fp8MatmulPlan* p) {
 
 bool plan_norm_grad(int64_t m, int64_t n, NormGradPlan* p) {
   if (m < 1 || n < 1 || m > kMaxDim || n > kNormMaxCols) return false;
-  p->groups = static_cast<int>(m < 1024 ? m : 1024);
+  // workgroups of one wave up to 1024 columns, of four and more above
+  const int64_t most = n <= 1024 ? 2048 : 1024;
+  p->groups = static_cast<int>(m < most ? m : most);
   p->ld = cdiv(n, 8) * 8;
   p->total_bytes = align_up(static_cast<size_t>(p->groups) * static_cast<size_t>(p->ld) * 4);
   return true;
@@ -544,6 +551,9 @@ ortho_status validate_rms_norm_fp8(const ortho_mat& X, const ortho_mat* Res, con
   if ((st = check_norm_weight(W, X, eps)) != ORTHO_OK) return st;
   for (const ortho_mat* t : {Res, Sum, Y})
     if ((st = check_like(t, X.dtype, X.rows, X.cols)) != ORTHO_OK) return st;
+  if (!same_or_apart(Sum, &X) || !same_or_apart(Sum, Res)) return ORTHO_E_LAYOUT;
+  if (Y && (Y->data == X.data || (Res && Y->data == Res->data) || (Sum && Y->data == Sum->data)))
+    return ORTHO_E_LAYOUT;
   return check_codes(Q, S, X.rows, X.cols, 1);
 }
 
@@ -556,6 +566,8 @@ ortho_status validate_rms_norm_backward(const ortho_mat& dY, const ortho_mat& X,
   for (const ortho_mat* t : {&dY, dSum, &dX})
     if ((st = check_like(t, X.dtype, X.rows, X.cols)) != ORTHO_OK) return st;
   if ((st = check_like(&dW, ORTHO_F32, 1, X.cols)) != ORTHO_OK) return st;
+  if (!same_or_apart(&dX, &dY) || !same_or_apart(&dX, &X) || !same_or_apart(&dX, dSum))
+    return ORTHO_E_LAYOUT;
   NormGradPlan plan;
   if (!plan_norm_grad(X.rows, X.cols, &plan)) return ORTHO_E_SHAPE;
   return check_ws(ws, ws_bytes, plan.total_bytes);

@@ -50,10 +50,11 @@ def test_quantize_argument_errors(change, want):
     (dict(y=M(30, 200, BF, data=None)), NULL), (dict(q=M(30, 200, E8)), DTYPE), (dict(q=M(30, 100, C8)), SHAPE),
     (dict(s=M(30, 1, F)), SHAPE), (dict(s=M(1, 2, F)), SHAPE), (dict(s=M(30, 2, C8)), DTYPE),
     (dict(x=M(30, 32769, BF), w=M(1, 32769, F)), SHAPE),
+    (dict(total=M(30, 200, BF, ld=208)), LAYOUT), (dict(y=M(30, 200, BF)), LAYOUT),
 ])
 def test_norm_argument_errors(change, want):
     a = dict(x=M(30, 200, BF), res=M(30, 200, BF), w=M(1, 200, F), eps=1e-6, total=M(30, 200, BF),
-             y=M(30, 200, BF), q=M(30, 200, C8), s=M(30, 2, F))
+             y=M(30, 200, BF, data=FAKE + (1 << 20)), q=M(30, 200, C8), s=M(30, 2, F))
     a.update(change)
     got = api.lib().rms_norm_fp8(a["x"], ref(a["res"]), a["w"], a["eps"], ref(a["total"]), ref(a["y"]),
                                  a["q"], a["s"], None)
@@ -67,7 +68,7 @@ def test_norm_argument_errors(change, want):
     (dict(dy=M(30, 200, F)), DTYPE), (dict(dy=M(30, 100, BF)), SHAPE), (dict(dx=M(30, 200, F)), DTYPE),
     (dict(dx=M(30, 200, BF, data=None)), NULL), (dict(dw=M(1, 200, BF)), DTYPE), (dict(dw=M(200, 1, F)), SHAPE),
     (dict(ds=M(31, 200, BF)), SHAPE), (dict(eps=-1.0), PARAM), (dict(ws=None), WS), (dict(ws=FAKE + 16), WS),
-    (dict(short=1), WS), (dict(x=M(30, 200, E8)), DTYPE),
+    (dict(short=1), WS), (dict(x=M(30, 200, E8)), DTYPE), (dict(dx=M(30, 200, BF, ld=208)), LAYOUT),
 ])
 def test_norm_gradient_argument_errors(change, want):
     a = dict(dy=M(30, 200, BF), x=M(30, 200, BF), w=M(1, 200, F), eps=1e-6, ds=M(30, 200, BF),
