@@ -33,9 +33,9 @@ enum { kScaled = 0, kHardware = 1 };
 // whole wave.  Which row of B is which row of instruction j is free: row
 // 4 g + e is column 16 g + 4 j + e of the wave's 64, so that lane group g ends
 // up with 16 consecutive columns and stores them as two 16-byte pieces.  C is
-// written straight from the accumulators:
-// the LDS is free at once for the next workgroup, whose first copies overlap
-// the stores.
+// written straight from the accumulators, so the LDS is free at once for the
+// next copies, which overlap the stores.  (kWhole: M, N multiples of 256 and K of
+// 128.  8192 x 8192 x 2048 spends about 25 us of its 160 on writing C.)
 //
 // A k tile is one block of 128: 128-byte LDS rows of eight 16-byte chunks, two
 // stages.  B's fragments and the scales of a tile sit in registers from its
@@ -59,8 +59,10 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   constexpr int kSlots = kMI * kNJ;
   // 8-row copies per wave and tile: B's, the first half of A's rows, the second
   constexpr int kCopyB = BN / 8 / kWaves, kCopyA = BM / 16 / kWaves, kCopies = kCopyB + 2 * kCopyA;
-  constexpr int kM = kMI / 2 - 1, kE = kMI - 1;   // groups of products behind the barriers
-  static_assert(kSlots % 4 == 0 && kNJ == 4, "");
+  // A's fragments are read kDepth groups of products ahead, so all of a half has
+  // been read kDepth groups before its end: the groups behind the barriers.
+  constexpr int kDepth = 2, kM = kMI / 2 - kDepth, kE = kMI - kDepth;
+  static_assert(kMI % 4 == 0 && kNJ == 4, "");
   static_assert(kThreads == BM + BN && kCopyB * kWaves * 8 == BN && kCopyA * kWaves * 16 == BM, "");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
   __shared__ __attribute__((aligned(16))) uint32_t scales[3][BM + BN];
@@ -214,10 +216,10 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   const uint32_t* const my_sb =
       &scales[0][BM + wn + (kMode == kHardware ? brow : (kRowB ? lg * 16 : 0))];
 
-  intx8 fa[2], fb[kNJ];
+  intx8 fa[4], fb[kNJ];
   floatx4 sum[4];                        // block sums of the last slots,
   floatx4 factor[4];                     // and what they are multiplied by
-  uint32_t sa[2];                        // scales as they were copied: A's of the
+  uint32_t sa[4];                        // scales as they were copied: A's of the
   floatx4 sb[kRowB ? kNJ : 1];           // 16 rows at hand, B's of the tile
   int eb[kNJ];                           // (kHardware: bytes)
   auto load_sb = [&](int j, int buf) ORTHO_INLINE {
@@ -276,8 +278,11 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
     patch_tail(0);
     __syncthreads();
   }
-  fa[0] = frag_a(offa);
-  sa[0] = my_sa[0];
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i) {
+    fa[i] = frag_a(offa + i * 2048);
+    sa[i] = my_sa[i * 16];
+  }
 #pragma unroll
   for (int j = 0; j < kNJ; ++j) {
     fb[j] = frag_b(offb + j * kBStep * 128);
@@ -325,17 +330,18 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
       for (int j = 0; j < kNJ; ++j) {
         const int slot = i * kNJ + j;
         if (j == 0) {
-          fa[(i + 1) & 1] = frag_a(i + 1 < kMI ? here + offa + (i + 1) * 2048 : next + offa);
-          sa[(i + 1) & 1] = i + 1 < kMI ? my_sa[cur3 * (BM + BN) + (i + 1) * 16] : my_sa[next3 * (BM + BN)];
+          constexpr int kLast = kMI - kDepth;
+          fa[(i + kDepth) & 3] = frag_a((i < kLast ? here : next) + offa + (i + kDepth) % kMI * 2048);
+          sa[(i + kDepth) & 3] = my_sa[(i < kLast ? cur3 : next3) * (BM + BN) + (i + kDepth) % kMI * 16];
         }
         if constexpr (kMode == kHardware) {
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i & 1], acc[i][j], 0, 0, 0,
-                                                                       eb[j], 0, sa[i & 1]);
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i & 3], acc[i][j], 0, 0, 0,
+                                                                       eb[j], 0, sa[i & 3]);
           const int ds = (slot + kSlots - 4) % kSlots;   // keeps the products in this order
           asm volatile("" : "+v"(acc[ds / kNJ][ds % kNJ]));
         } else {
           floatx4 s = {0.f, 0.f, 0.f, 0.f};
-          s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i & 1], s, 0, 0, 0, 0, 0, 0);
+          s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i & 3], s, 0, 0, 0, 0, 0, 0);
           // the sum of two slots ago joins its accumulators (pinned here: left
           // alone, the compiler gathers the additions at the tile's end and
           // keeps every sum alive until then)
@@ -347,12 +353,12 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
           sum[slot & 3] = s;
           if constexpr (kRowB) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) factor[slot & 3][e] = __uint_as_float(sa[i & 1]) * sb[j][e];
+            for (int e = 0; e < 4; ++e) factor[slot & 3][e] = __uint_as_float(sa[i & 3]) * sb[j][e];
           } else {
-            factor[slot & 3][0] = __uint_as_float(sa[i & 1]) * sb[0][0];
+            factor[slot & 3][0] = __uint_as_float(sa[i & 3]) * sb[0][0];
           }
         }
-        if (i == kE) {
+        if (i == kMI - 1) {
           fb[j] = frag_b(next + offb + j * kBStep * 128);
           load_sb(j, next3);
         }
