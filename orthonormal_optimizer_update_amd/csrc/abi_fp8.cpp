@@ -129,7 +129,6 @@ ortho_status fp8_matmul(ortho_mat A, ortho_mat SA, ortho_mat B, ortho_mat SB, or
   a.add = data_of(Add);
   a.ldadd = ld_of(Add);
   a.add_bf = Add && Add->dtype == ORTHO_BF16;
-  a.cvec = rows_at(&C, 16) && rows_at(Add, 16);
   a.M = static_cast<int>(A.rows);
   a.N = static_cast<int>(B.rows);
   a.K = static_cast<int>(A.cols);

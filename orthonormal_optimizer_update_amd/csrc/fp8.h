@@ -71,7 +71,6 @@ struct Fp8GemmArgs {
   const void* add;
   int64_t ldc, ldadd;
   int add_bf;
-  int cvec;                 // C's (and Add's) rows at multiples of 16 bytes
   int M, N, K;
   int dma;                  // A's and B's rows at multiples of 16 bytes, 256 of them within 2 GiB
   int e8m0, c_bf;           // scale type, C's type

@@ -100,4 +100,48 @@ __device__ __forceinline__ uint4 load_codes16(const uint8_t* row, int k, int K) 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Four elements of Add from column n of row m, and four of C to it (C's type
+// T); rows of either may start at any element (the accesses need no alignment).
+__device__ __forceinline__ floatx4 load_add4(const Fp8GemmArgs& p, int64_t m, int n) {
+  floatx4 v = {0.f, 0.f, 0.f, 0.f};
+  if (p.add_bf) {
+    const uint16_t* src = static_cast<const uint16_t*>(p.add) + m * p.ldadd + n;
+    if (n + 4 <= p.N) {
+      uint2 u;
+      __builtin_memcpy(&u, src, 8);
+      return floatx4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xffff0000u)};
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < p.N) v[e] = bf16_bits_to_f32(src[e]);
+    return v;
+  }
+  const float* src = static_cast<const float*>(p.add) + m * p.ldadd + n;
+  if (n + 4 <= p.N) {
+    __builtin_memcpy(&v, src, 16);
+    return v;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n + e < p.N) v[e] = src[e];
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void store_c4(const Fp8GemmArgs& p, int64_t m, int n, floatx4 v) {
+  T* const dst = static_cast<T*>(p.c) + m * p.ldc + n;
+  if (n + 4 <= p.N) {
+    if constexpr (sizeof(T) == 2) {
+      const uint2 u = pack_bf16x4(v);
+      __builtin_memcpy(dst, &u, 8);
+    } else {
+      __builtin_memcpy(dst, &v, 16);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n + e < p.N) store_from_f32<T>(dst, e, v[e]);
+}
+
 }  // namespace ortho

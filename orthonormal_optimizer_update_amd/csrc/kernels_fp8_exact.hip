@@ -221,30 +221,23 @@ __global__ __launch_bounds__(256, 2) void fp8_exact_kernel(Fp8GemmArgs p) {
     cur3 = cur3 == 2 ? 0 : cur3 + 1;
   }
 
-  const bool whole = n0 + wn + 64 <= p.N && p.cvec;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int m = m0 + wm + i * 32 + l32;
     if (m >= p.M) continue;
-    float* const out = p.part ? p.part + ((int64_t)split * p.M + m) * p.ldp : static_cast<float*>(p.c) + m * p.ldc;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int n = n0 + wn + j * 32 + g * 8 + half * 4;
         floatx4 v = {acc[i][j][g * 4], acc[i][j][g * 4 + 1], acc[i][j][g * 4 + 2], acc[i][j][g * 4 + 3]};
-        if (p.add && !p.part) {
-          const float4 ad = p.add_bf ? load4<uint16_t>(static_cast<const uint16_t*>(p.add) + m * p.ldadd, n, p.N, p.cvec)
-                                     : load4<float>(static_cast<const float*>(p.add) + m * p.ldadd, n, p.N, p.cvec);
-          v[0] += ad.x; v[1] += ad.y; v[2] += ad.z; v[3] += ad.w;
+        if (p.part) {   // rows of whole quads
+          if (n < p.N)
+            *reinterpret_cast<floatx4*>(p.part + ((int64_t)split * p.M + m) * p.ldp + n) = v;
+          continue;
         }
-        if (whole || (p.part && n < p.N)) {   // (the splits' rows are whole quads)
-          *reinterpret_cast<floatx4*>(out + n) = v;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n + e < p.N) out[n + e] = v[e];
-        }
+        if (p.add) v += load_add4(p, m, n);
+        store_c4<float>(p, m, n, v);
       }
   }
 }

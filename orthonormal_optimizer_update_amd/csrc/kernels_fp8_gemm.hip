@@ -32,7 +32,8 @@ enum { kScaled = 0, kHardware = 1 };
 // of A per 16 rows; the scale of a 128 x 128 block of B is the same for the
 // whole wave.  Which row of B is which row of instruction j is free: row
 // 4 g + e is column 16 g + 4 j + e of the wave's 64, so that lane group g ends
-// up with 16 consecutive columns and stores them as two 16-byte pieces.  C is
+// up with 16 consecutive columns and stores them as two 16-byte pieces (at any
+// element: no alignment is needed).  C is
 // written straight from the accumulators, so the LDS is free at once for the
 // next copies, which overlap the stores.  (kWhole: M, N multiples of 256 and K of
 // 128.  8192 x 8192 x 2048 spends about 25 us of its 160 on writing C.)
@@ -392,44 +393,7 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
     }
   }
 
-  // Rows of C (or Add) at any byte: through LDS, 64 rows of the wave's 64
-  // columns at a time, so that a store covers neighbouring columns of one row
-  // (element by element from the accumulators, 64 separate pieces each,
-  // 1000 x 1537 x 1111 took twice as long).
-  if (!kWhole && !p.cvec && !p.part) {
-    __syncthreads();   // every wave is done with the stages
-    float* const rows = reinterpret_cast<float*>(smem) + wave * (64 * 64);
-#pragma unroll
-    for (int h = 0; h < kMI / 4; ++h) {
-      // row r's quads of columns at q ^ (r % 16)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < kNJ; ++j)
-          *reinterpret_cast<floatx4*>(rows + (i * 16 + l16) * 64 + ((lg * 4 + j) ^ l16) * 4) = acc[h * 4 + i][j];
-      const int n = n0 + wn + lane, m1 = m0 + wm + h * 64, left = n < p.N ? p.M - m1 : 0;
-      auto value = [&](int r) ORTHO_INLINE {
-        return rows[r * 64 + (((lane >> 2) ^ (r & 15)) << 2) + (lane & 3)];
-      };
-      uint16_t* const o = static_cast<uint16_t*>(p.c) + m1 * p.ldc + n;
-      if (!p.add) {
-#pragma unroll 16
-        for (int r = 0; r < 64; ++r)
-          if (r < left) o[r * p.ldc] = to_bf16_bits(value(r));
-      } else {
-#pragma unroll 4
-        for (int r = 0; r < 64; ++r)
-          if (r < left) {
-            const int64_t at = (m1 + r) * p.ldadd + n;
-            o[r * p.ldc] = to_bf16_bits(value(r) + (p.add_bf ? bf16_bits_to_f32(static_cast<const uint16_t*>(p.add)[at])
-                                                            : static_cast<const float*>(p.add)[at]));
-          }
-      }
-    }
-    return;
-  }
-
-  // Columns of piece j of a lane: four, next to those of piece j + 1 for bf16.
+  // Columns of piece j of a lane: four, next to those of piece j + 1.
   const bool whole = kWhole || n0 + wn + 64 <= p.N;
 #pragma unroll
   for (int i = 0; i < kMI; ++i) {
@@ -445,26 +409,19 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
     }
     if (p.add) {
 #pragma unroll
-      for (int j = 0; j < kNJ; ++j) {
-        const int n = nl + j * kBStep;
-        const float4 ad = p.add_bf ? load4<uint16_t>(static_cast<const uint16_t*>(p.add) + m * p.ldadd, n, p.N, p.cvec)
-                                   : load4<float>(static_cast<const float*>(p.add) + m * p.ldadd, n, p.N, p.cvec);
-        acc[i][j][0] += ad.x; acc[i][j][1] += ad.y; acc[i][j][2] += ad.z; acc[i][j][3] += ad.w;
-      }
+      for (int j = 0; j < kNJ; ++j) acc[i][j] += load_add4(p, m, nl + j * kBStep);
     }
-    uint16_t* o = static_cast<uint16_t*>(p.c) + m * p.ldc;
+    if (whole) {
+      uint16_t* const o = static_cast<uint16_t*>(p.c) + m * p.ldc + nl;
 #pragma unroll
-    for (int j = 0; j < kNJ; j += 2) {
-      const uint2 lo = pack_bf16x4(acc[i][j]), hi = pack_bf16x4(acc[i][j + 1]);
-      const int n = nl + j * 4;
-      if (whole) {
-        *reinterpret_cast<uint4*>(o + n) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-      } else {
-        const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (n + e < p.N) o[n + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+      for (int j = 0; j < kNJ; j += 2) {
+        const uint2 lo = pack_bf16x4(acc[i][j]), hi = pack_bf16x4(acc[i][j + 1]);
+        const uint4 u = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        __builtin_memcpy(o + j * 4, &u, 16);
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kNJ; ++j) store_c4<uint16_t>(p, m, nl + j * 4, acc[i][j]);
     }
   }
   if constexpr (kWhole) {
@@ -491,20 +448,8 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8GemmArgs p) {
   floatx4 v = *reinterpret_cast<const floatx4*>(src);
 #pragma unroll 4
   for (int i = 1; i < p.splits; ++i) v += *reinterpret_cast<const floatx4*>(src + i * (p.M * p.ldp));
-  if (p.add) {
-    const float4 ad = p.add_bf ? load4<uint16_t>(static_cast<const uint16_t*>(p.add) + m * p.ldadd, n, p.N, p.cvec)
-                               : load4<float>(static_cast<const float*>(p.add) + m * p.ldadd, n, p.N, p.cvec);
-    v[0] += ad.x; v[1] += ad.y; v[2] += ad.z; v[3] += ad.w;
-  }
-  T* const o = static_cast<T*>(p.c) + m * p.ldc;
-  if (p.cvec && n + 4 <= p.N) {
-    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(o + n) = pack_bf16x4(v);
-    else *reinterpret_cast<floatx4*>(o + n) = v;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (n + e < p.N) store_from_f32<T>(o, n + e, v[e]);
-  }
+  if (p.add) v += load_add4(p, m, n);
+  store_c4<T>(p, m, n, v);
 }
 
 constexpr int kResident = 256;   // workgroups of eight waves that the chip holds at once
@@ -520,9 +465,12 @@ void launch(const Fp8GemmArgs& a, hipStream_t s) {
 
 template <int kMode, bool kRowB>
 void by_tile(const Fp8GemmArgs& a, hipStream_t s) {
-  const bool whole = a.M % 256 == 0 && a.N % 256 == 0 && a.K % kFp8Block == 0 && a.cvec;
+  const bool whole = a.M % 256 == 0 && a.N % 256 == 0 && a.K % kFp8Block == 0;
   if (!a.dma || a.K < 16) return launch<kMode, kRowB, 2, 2, 4, 4, false, false>(a, s);
-  if ((int64_t)a.M * a.N >= 256 * 256 * 128) {
+  // 256 x 256 tiles from 160 of them on (below, the CUs without one cost more
+  // than twice the copies do: 4096 x 2048 x 2048 34.3 us with them, 27.5 on
+  // 128 x 128; 4096 x 2800 x 2048 40.8 and 49.3 us)
+  if ((int64_t)a.M * a.N >= 256 * 256 * 160) {
     if (whole) return launch<kMode, kRowB, 2, 4, 8, 4, true, true>(a, s);
     return launch<kMode, kRowB, 2, 4, 8, 4, true, false>(a, s);
   }

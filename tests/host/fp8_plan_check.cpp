@@ -40,7 +40,7 @@ int main() {
           EXPECT(p.total_bytes >= (size_t)p.splits * m * p.ldp * 4, m, n, k);
           EXPECT(m > kFewRowsMax && tiles * p.splits <= 256 && p.kchunk >= 3, m, n, k);
           // what a launch for large results takes is never split
-          EXPECT(m * n < 256 * 256 * 128, m, n, k);
+          EXPECT(m * n < 256 * 256 * 160, m, n, k);
         }
       }
   for (int64_t m : dims)
