@@ -250,10 +250,8 @@ __device__ __forceinline__ void load_w8(const void* w, int w_bf, int c, int n, f
 //
 // The codes do not see the rounding of y: with u = r w, a block's codes are
 // u (448 / max|u|), in which t cancels (power-of-two scales: u (t / s), t kept
-// in fp64 until then).  Three fp32 roundings (u, the factor, the product) stand
-// before the one to e4m3: of the 33.5 million codes of 8192 x 4096 about 20 are
-// on the other side of a tie.  (With u and the factor in two fp32 each, 14, and
-// 54.3 us against 52.1 in bf16, 4096 x 8192 in fp32 128.5 against 114.0.)
+// in fp64), and u and the factor each carry their rounding error as a second
+// fp32.  What is left is one fp32 rounding before the rounding to e4m3.
 template <typename T, bool kE8m0, int kThreads, int kC>
 __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
   __shared__ float red[2][2][kThreads / 64];
@@ -307,11 +305,14 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
     for (int i = 0; i < kC; ++i) {
       const int c = (i * kThreads + t) * 8;
       if (c - (t & 15) * 8 >= a.n) continue;   // whole block past the row's end
-      float u[8], q[8];
+      float u[8], ul[8], q[8];
       float (&wi)[8] = w[kAhead ? i : 0];
       if (!kAhead) load_w8(a.w, a.w_bf, c, a.n, wi);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] = v[i][j] * wi[j];
+      for (int j = 0; j < 8; ++j) {
+        u[j] = v[i][j] * wi[j];
+        ul[j] = fmaf(v[i][j], wi[j], -u[j]);
+      }
       if (a.y) {
         float y[8];
 #pragma unroll
@@ -324,12 +325,14 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
       float scale, f;
       block_scale<kE8m0>(top_y, scale, f);
       // fp32 scales: 448 / top, unless the scale is the smallest or 1
-      const float g = static_cast<float>(!kE8m0 && scale > 0x1p-126f && top_y > 0.f ? 448.0 / top : rsd / scale);
+      const double g = !kE8m0 && scale > 0x1p-126f && top_y > 0.f ? 448.0 / top : rsd / scale;
+      const float gh = static_cast<float>(g), gl = static_cast<float>(g - gh);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float h = u[j] * g;
+        const float h = u[j] * gh;
         // (not finite: the product as it is, so that infinities give NaN codes)
-        q[j] = __builtin_fabsf(h) <= 512.f ? h : v[i][j] * rs * wi[j] * f;
+        const float e = fmaf(u[j], gh, -h) + fmaf(ul[j], gh, u[j] * gl);
+        q[j] = __builtin_fabsf(h) <= 512.f ? h + e : v[i][j] * rs * wi[j] * f;
       }
       store_codes8(a.q + row * a.ldq, c, a.n, codes8(q, 1.f));
       if ((t & 15) == 0) store_scale<kE8m0>(a.s, row * a.lds + c / kFp8Block, scale);
