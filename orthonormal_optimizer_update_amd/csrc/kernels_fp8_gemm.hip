@@ -36,7 +36,8 @@ enum { kScaled = 0, kHardware = 1 };
 // element: no alignment is needed).  C is
 // written straight from the accumulators, so the LDS is free at once for the
 // next copies, which overlap the stores.  (kWhole: M, N multiples of 256 and K of
-// 128.  8192 x 8192 x 2048 spends about 25 us of its 160 on writing C.)
+// 128.  8192 x 8192 x 2048 takes 136 us with fp32 scales, 2.02 PFLOP/s, and 126
+// with e8m0 ones; its C alone is 26 us of a copy's rate.)
 //
 // A k tile is one block of 128: 128-byte LDS rows of eight 16-byte chunks, two
 // stages.  B's fragments and the scales of a tile sit in registers from its

@@ -1,7 +1,9 @@
 // Conversion to 8-bit codes with block scales, and the RMS norm around it: the
 // residual's addition, the 8-bit output and the gradient.  All are bound by
 // HBM traffic: each element is read once, held in registers, and written once
-// per output.
+// per output.  In bf16: quantisation by rows of 8192 x 4096 20.2 us (5.0 TB/s),
+// both orientations 31 (4.3); the norm with residual, sum and y 54 (5.6); the
+// gradient 48 (5.6).  In fp32, 4096 x 8192: 28 (6.0), 42 (4.8), 128 (4.4), 109 (4.9).
 #include <type_traits>
 
 #include "fp8.h"
@@ -251,7 +253,10 @@ __device__ __forceinline__ void load_w8(const void* w, int w_bf, int c, int n, f
 // The codes do not see the rounding of y: with u = r w, a block's codes are
 // u (448 / max|u|), in which t cancels (power-of-two scales: u (t / s), t kept
 // in fp64), and u and the factor each carry their rounding error as a second
-// fp32.  What is left is one fp32 rounding before the rounding to e4m3.
+// fp32.  What is left are the roundings of max|u| (of the row's sum, with
+// power-of-two scales) and of the result before the one to e4m3: of the 33.5
+// million codes of 8192 x 4096 about 14 are on the other side of a tie (20
+// without the second fp32s, which cost 4% of the time in bf16).
 template <typename T, bool kE8m0, int kThreads, int kC>
 __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
   __shared__ float red[2][2][kThreads / 64];

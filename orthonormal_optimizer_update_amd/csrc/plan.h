@@ -161,8 +161,8 @@ constexpr int64_t kNormMaxCols = 32768;
 // The product on 128 x 128 tiles of C splits K where there are fewer tiles than
 // CUs: `splits` ranges of `kchunk` blocks of 128, whose fp32 sums (rows
 // of ldp) meet in the workspace and are added in order.
-// Rows of A that take the kernel for few rows (48 x 8192 x 2048: 15.1 us with
-// it, 14.2 on tiles; 32 x 8192 x 2048: 9.8 us).
+// Rows of A that take the kernel for few rows (48 x 8192 x 2048: 17.8 us with
+// it, 12.8 on tiles; 48 x 2048 x 8192: 21.5 and 13.5 us).
 constexpr int64_t kFewRowsMax = 32;
 struct Fp8MatmulPlan {
   int splits, kchunk;
