@@ -2,8 +2,8 @@
 // residual's addition, the 8-bit output and the gradient.  All are bound by
 // HBM traffic: each element is read once, held in registers, and written once
 // per output.  In bf16: quantisation by rows of 8192 x 4096 20.2 us (5.0 TB/s),
-// both orientations 31 (4.3); the norm with residual, sum and y 54 (5.6); the
-// gradient 48 (5.6).  In fp32, 4096 x 8192: 28 (6.0), 42 (4.8), 128 (4.4), 109 (4.9).
+// both orientations 31 (4.3); the norm with residual, sum and y 53 (5.7); the
+// gradient 48 (5.6).  In fp32, 4096 x 8192: 28 (6.0), 42 (4.8), 126 (4.5), 109 (4.9).
 #include <type_traits>
 
 #include "fp8.h"
@@ -334,10 +334,9 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
       const float gh = static_cast<float>(g), gl = static_cast<float>(g - gh);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float h = u[j] * gh;
+        const float e = fmaf(u[j], gh, fmaf(ul[j], gh, u[j] * gl));
         // (not finite: the product as it is, so that infinities give NaN codes)
-        const float e = fmaf(u[j], gh, -h) + fmaf(ul[j], gh, u[j] * gl);
-        q[j] = __builtin_fabsf(h) <= 512.f ? h + e : v[i][j] * rs * wi[j] * f;
+        q[j] = __builtin_fabsf(e) <= 512.f ? e : v[i][j] * rs * wi[j] * f;
       }
       store_codes8(a.q + row * a.ldq, c, a.n, codes8(q, 1.f));
       if ((t & 15) == 0) store_scale<kE8m0>(a.s, row * a.lds + c / kFp8Block, scale);
