@@ -488,7 +488,8 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_fp8_matmul(const Fp8GemmArgs& a, hipStream_t s) {
-  if (a.M <= kFewRows) return launch_fp8_few(a, s);
+  // (from 2^25 rows of B on its launch could pass 2^32 threads)
+  if (a.M <= kFewRows && a.N < 1 << 25) return launch_fp8_few(a, s);
   const hipError_t e = a.c_bf ? launch_fp8_gemm(a, s) : launch_fp8_exact(a, s);
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t quads = (int64_t)a.M * (a.ldp / 4);

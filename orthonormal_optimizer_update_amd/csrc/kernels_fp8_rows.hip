@@ -476,8 +476,9 @@ hipError_t by_width(int n, F f) {
 
 template <typename T, bool kE8m0>
 hipError_t quantize(const QuantArgs& a, bool tiles, hipStream_t s) {
-  if (!tiles && a.qt == nullptr) {
-    const int64_t blocks = cdiv((int64_t)a.m * cdiv(a.n, kFp8Block), 16);
+  const int64_t blocks = cdiv((int64_t)a.m * cdiv(a.n, kFp8Block), 16);
+  // (more workgroups of 256 would be 2^32 threads, too many for one launch)
+  if (!tiles && a.qt == nullptr && blocks < int64_t{1} << 24) {
     hipLaunchKernelGGL((quant_rows_kernel<T, kE8m0>), dim3(static_cast<uint32_t>(blocks)), dim3(256),
                        0, s, a);
     return hipGetLastError();

@@ -493,15 +493,15 @@ ortho_status check_ws(const void* ws, size_t have, size_t need) {
 }
 
 constexpr int64_t kCus = 256;
-// Workgroups of a launch are counted in 31 bits.
-constexpr int64_t kMaxGrid = (int64_t{1} << 31) - 1;
+// A launch holds fewer than 2^32 threads: workgroups of 256, one per 128 x 128.
+constexpr int64_t kMaxTiles = (int64_t{1} << 24) - 1;
 
 }  // namespace
 
 bool plan_fp8_matmul(int64_t m, int64_t n, int64_t k, Fp8MatmulPlan* p) {
   if (m < 1 || n < 1 || k < 1 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return false;
   const int64_t tiles = cdiv(m, 128) * cdiv(n, 128), nkb = cdiv(k, kFp8BlockSize);
-  if (tiles > kMaxGrid) return false;
+  if (tiles > kMaxTiles) return false;
   // One workgroup per CU, of at least three blocks (its first copies take about
   // two blocks' time to arrive), and only where the blocks saved, about 1 us
   // each, outweigh the second launch and its traffic, about 6 us:
@@ -539,7 +539,7 @@ ortho_status validate_fp8_quantize(const ortho_mat& X, int32_t block_rows, const
   if (Q && (st = check_codes(*Q, *S, X.rows, X.cols, block_rows)) != ORTHO_OK) return st;
   if (QT && (st = check_codes(*QT, *ST, X.cols, X.rows, block_rows)) != ORTHO_OK) return st;
   if (S && ST && S->dtype != ST->dtype) return ORTHO_E_DTYPE;
-  if (X.rows * cdiv(X.cols, kFp8BlockSize) > kMaxGrid) return ORTHO_E_SHAPE;
+  if (cdiv(X.rows, 128) * cdiv(X.cols, 128) > kMaxTiles) return ORTHO_E_SHAPE;
   return ORTHO_OK;
 }
 

@@ -57,6 +57,7 @@ int main() {
   EXPECT(plan_fp8_matmul(big, 128, big, &p), big, 128, big);
   EXPECT(plan_fp8_matmul(1, big, big, &p) && p.splits == 1, 1, big, big);
   EXPECT(!plan_fp8_matmul(big, big, 1, &p), big, big, 1);
+  EXPECT(!plan_fp8_matmul(big, 129, 1, &p), big, 129, 1);   // 2^24 tiles: 2^32 threads
   EXPECT(!plan_fp8_matmul(big + 1, 1, 1, &p), big + 1, 1, 1);
   EXPECT(!plan_fp8_matmul(0, 1, 1, &p) && !plan_fp8_matmul(1, 1, 0, &p), 0, 1, 1);
   EXPECT(plan_norm_grad(big, 1, &g) && !plan_norm_grad(1, 0, &g), big, 1, 0);

@@ -255,3 +255,38 @@ def test_binding_refuses_mixed_devices_and_layouts():
     assert e.value.status in (2, 7)
     with pytest.raises(api.OrthoError):
         api.fp8_quantize(torch.empty(0, 256, device="cuda"))
+
+
+def test_more_blocks_and_rows_than_one_thread_each():
+    """Sizes at which 16 threads per block, or a workgroup per 16 rows of B,
+    would pass the 2^32 threads of a launch."""
+    m = (1 << 28) + 131
+    x = torch.arange(m, device="cuda", dtype=torch.int32).remainder_(7).sub_(3).to(torch.bfloat16)[:, None]
+    Q = torch.zeros(m, 1, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    S = torch.zeros(m, 1, dtype=torch.float8_e8m0fnu, device="cuda")
+    note(f"fp8_quantize {m} x 1")
+    api.fp8_quantize(x, Q, S)
+    torch.cuda.synchronize()
+    # one element per block: rows of seven repeat, so the last ones and a sample
+    # across equal the same rows alone
+    part = torch.arange(7, device="cuda").sub(3).to(torch.bfloat16)[:, None]
+    q1 = torch.zeros(7, 1, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    s1 = torch.zeros(7, 1, dtype=torch.float8_e8m0fnu, device="cuda")
+    api.fp8_quantize(part, q1, s1)
+    torch.cuda.synchronize()
+    at = torch.cat([torch.arange(0, m, 65521), torch.arange(m - 1000, m)]).cuda()
+    for big, small in ((Q, q1), (S, s1)):
+        assert torch.equal(big.view(torch.uint8)[at], small.view(torch.uint8)[at % 7])
+    del x, Q, S, at
+    n, k = (1 << 25) + 21, 16
+    b = torch.arange(n * k, device="cuda", dtype=torch.int32).remainder_(13).sub_(6).to(torch.float8_e4m3fn).view(n, k)
+    a = torch.arange(k, device="cuda").sub(8).to(torch.float8_e4m3fn)[None]
+    sa = torch.ones(1, 1, device="cuda")
+    sb = torch.full((-(-n // 128), 1), 2.0, device="cuda")
+    for dt in (torch.bfloat16, torch.float32):
+        note(f"fp8_matmul 1 x {n} x {k} {dt}")
+        c = api.fp8_matmul(a, sa, b, sb, out_dtype=dt)
+        torch.cuda.synchronize()
+        # integers below 2^11: the products and sums are exact
+        want = (b.float() * (2 * a.float())).sum(1)[None].to(dt)
+        assert torch.equal(c, want)
