@@ -374,8 +374,9 @@ size_t ortho_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
  * ORTHO_BF16 C of more than a few rows the 8-bit matrix instruction is used,
  * which cuts each product below 2^-13 of the largest of its group of eight
  * neighbours along k (about 1e-5 of the result, against the 2^-9 of C's
- * rounding).  A NaN code or scale reaches the elements of C that it enters into,
- * and no others. */
+ * rounding).  The product of an element's two scales need not be an fp32 number,
+ * only the element.  A NaN code or scale reaches the elements of C that it enters
+ * into, and no others. */
 ortho_status fp8_matmul(ortho_mat A, ortho_mat SA, ortho_mat B, ortho_mat SB, ortho_mat C,
                         const ortho_mat* Add, void* ws, size_t ws_bytes, void* stream);
 

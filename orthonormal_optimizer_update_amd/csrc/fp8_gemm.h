@@ -13,12 +13,13 @@ typedef int intx8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
-// Eight codes as eight bf16 (exact; the NaN code gives NaN).
-__device__ __forceinline__ bf16x8 codes_to_bf16(int lo, int hi) {
-  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false);
-  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
-  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false);
-  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
+// Eight codes times the power of two `by` as eight bf16 (exact while that is a
+// normal number; the NaN code gives NaN).
+__device__ __forceinline__ bf16x8 codes_to_bf16(int lo, int hi, float by = 1.f) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, by, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, by, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, by, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, by, true);
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
@@ -81,16 +82,86 @@ __device__ __forceinline__ T pick(bool first, T a, T b) {
   return first ? a : b;
 }
 
+// A block's sum is 2^-18 to 2^24.7 (or 0), so sum sa sb can be a number though
+// sa sb is subnormal, zero or infinite (0 with a block of zeros beside an infinite
+// one).  That is rare: a wave keeps the range of the scales that it met, and the
+// rows of C where a product could have left fp32's are formed anew, in the same
+// order, with what a scale has beyond 2^-63 .. 2^62 (an exact power of two) in the
+// codes' products and only the rest, whose products are normal numbers, in the
+// factor.  Elements with no such scale come out the same either way.
+constexpr int kFar = 62;
+__device__ __forceinline__ int excess(float s) {
+  const int e = __builtin_amdgcn_frexp_expf(s);   // 0 for zero, infinities and NaN
+  return e - min(max(e, -kFar), kFar);
+}
+__device__ __forceinline__ float moved(float s) { return __builtin_ldexpf(s, -excess(s)); }
+
+// Whether the product f of two scales left fp32's normal range (power-of-two scales
+// are never 0).
+template <bool kE8m0>
+__device__ __forceinline__ bool leaves_range(float f, float sa, float sb) {
+  const bool odd = __builtin_amdgcn_classf(f, 0x2f4);   // infinite, subnormal or zero, of either sign
+  if constexpr (kE8m0) return odd;
+  return odd && sa != 0.f && sb != 0.f;
+}
+
+// Smallest exponents of the scales of a wave's 64 kRows rows of A (lane l: rows
+// 64 h + l, in one of kH registers) and of its rows of B (spread over the lanes in
+// any way), and the largest of both: s in [2^(e-1), 2^e).
+template <int kRows, int kH>
+struct ScaleRange {
+  int lo_a[kH] = {}, lo_b = 0, hi = 0;
+  __device__ __forceinline__ void a(int h, float s) {
+    const int e = __builtin_amdgcn_frexp_expf(s);
+    lo_a[h % kH] = min(lo_a[h % kH], e);
+    hi = max(hi, e);
+  }
+  __device__ __forceinline__ void b(float s) {
+    const int e = __builtin_amdgcn_frexp_expf(s);
+    lo_b = min(lo_b, e);
+    hi = max(hi, e);
+  }
+  // Bit i: whether a product with one of the rows 16 i .. 16 i + 15 may have left
+  // fp32's normal range.  The same for the wave.
+  __device__ __forceinline__ uint32_t lost() const {
+    int lo = lo_b;
+#pragma unroll
+    for (int h = 0; h < kH; ++h) lo = min(lo, lo_a[h]);
+    if (!__any(lo < -kFar || hi > kFar)) return 0;
+    int y = lo_b;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) y = min(y, __shfl_xor(y, o, 64));
+    const bool all = __any(hi > kFar);
+    uint32_t rows = 0;
+#pragma unroll
+    for (int h = 0; h < kRows; ++h) {
+      const uint64_t some = __ballot(all || lo_a[h % kH] + y < -124);   // 2^(x-1) 2^(y-1) < 2^-126
+#pragma unroll
+      for (int q = 0; q < 4; ++q) rows |= (some >> 16 * q & 0xffff) != 0 ? 1u << (4 * h + q) : 0u;
+    }
+    return rows;
+  }
+};
+
+// The kernel's arguments (its only parameter) read anew from here on: a rare path
+// that uses them then does not keep them in scalar registers through the others.
+__device__ __forceinline__ Fp8GemmArgs args_again() {
+  auto* q = __builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(q));
+  return *(const Fp8GemmArgs*)(const void*)q;
+}
+
 // 16 codes from column k of a row of K; zero codes from column K on.  Any byte.
 // A piece that the row's end cuts is loaded from 16 columns before the end and
 // shifted, so that no load depends on a branch.
+__device__ __forceinline__ uint4 load_codes16_of_long_rows(const uint8_t* row, int k, int K) {   // K >= 16
+  uint4 u;
+  __builtin_memcpy(&u, row + min(k, K - 16), 16);
+  const int cut = k + 16 - K;   // bytes of the piece that lie past the end
+  return cut <= 0 ? u : cut16(u, min(cut, 16));
+}
 __device__ __forceinline__ uint4 load_codes16(const uint8_t* row, int k, int K) {
-  if (K >= 16) {   // uniform
-    uint4 u;
-    __builtin_memcpy(&u, row + min(k, K - 16), 16);
-    const int cut = k + 16 - K;   // bytes of the piece that lie past the end
-    return cut <= 0 ? u : cut16(u, min(cut, 16));
-  }
+  if (K >= 16) return load_codes16_of_long_rows(row, k, K);   // uniform
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int j = 0; j < 16; ++j) {

@@ -152,6 +152,8 @@ __global__ __launch_bounds__(256, 2) void fp8_exact_kernel(Fp8GemmArgs p) {
 #pragma unroll
   for (int f = 0; f < 4; ++f) raw[0][f] = chunk(0, f, 0);
 
+  ScaleRange<1, 1> range;          // where B's rows have scales of their own
+  bool left[2] = {false, false};   // elsewhere: whether a product of scales left fp32's range
   int cur = 0, cur3 = 0;   // stage, and buffer of scales, of the tile being computed
   for (int kt = kt_begin; kt < kt_end; ++kt) {
     const int ahead3 = cur3 == 0 ? 2 : cur3 - 1;
@@ -202,6 +204,14 @@ __global__ __launch_bounds__(256, 2) void fp8_exact_kernel(Fp8GemmArgs p) {
     float sa[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) sa[i] = scale_value(scales[cur3][wm + i * 32 + l32]);
+    if constexpr (kRowB) {
+      range.a(0, scale_value(scales[cur3][wm + lane]));
+      range.b(scale_value(scales[cur3][BM + wn + lane]));
+    } else {
+      const float sb = scale_value(scales[cur3][BM + wn]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) left[i] |= leaves_range<kE8m0>(sa[i] * sb, sa[i], sb);
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -224,24 +234,73 @@ __global__ __launch_bounds__(256, 2) void fp8_exact_kernel(Fp8GemmArgs p) {
     cur3 = cur3 == 2 ? 0 : cur3 + 1;
   }
 
+  // What a lane holds of one 32 x 32 of C: four columns in four places.
+  auto store = [&](const Fp8GemmArgs& to, int i, int j, const floatx16& c) ORTHO_INLINE {
+    const int m = m0 + wm + i * 32 + l32;
+    if (m >= to.M) return;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int n = n0 + wn + j * 32 + g * 8 + half * 4;
+      floatx4 v = {c[g * 4], c[g * 4 + 1], c[g * 4 + 2], c[g * 4 + 3]};
+      if (to.part) {   // rows of whole quads
+        if (n < to.N)
+          *reinterpret_cast<floatx4*>(to.part + ((int64_t)split * to.M + m) * to.ldp + n) = v;
+        continue;
+      }
+      if (to.add) v += load_add4(to, m, n);
+      store_c4<float>(to, m, n, v);
+    }
+  };
+  bool lost[2];
+  if constexpr (kRowB) {
+    const uint32_t rows = range.lost();
+    lost[0] = (rows & 3) != 0;
+    lost[1] = (rows & 12) != 0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) lost[i] = __any(left[i]);
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int m = m0 + wm + i * 32 + l32;
-    if (m >= p.M) continue;
+    if (lost[i]) continue;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j) store(p, i, j, acc[i][j]);
+  }
+  if (!lost[0] && !lost[1]) return;
+  // Straight from memory, with the excess of far scales in the conversions.
+  const Fp8GemmArgs r = args_again();
+#pragma unroll 1
+  for (int ij = 0; ij < 4; ++ij) {
+    const int i = ij >> 1, j = ij & 1;
+    if (!(i == 0 ? lost[0] : lost[1])) continue;
+    const int64_t ra = min(m0 + wm + i * 32 + l32, r.M - 1), rb = min(n0 + wn + j * 32 + l32, r.N - 1);
+    floatx16 to;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int n = n0 + wn + j * 32 + g * 8 + half * 4;
-        floatx4 v = {acc[i][j][g * 4], acc[i][j][g * 4 + 1], acc[i][j][g * 4 + 2], acc[i][j][g * 4 + 3]};
-        if (p.part) {   // rows of whole quads
-          if (n < p.N)
-            *reinterpret_cast<floatx4*>(p.part + ((int64_t)split * p.M + m) * p.ldp + n) = v;
-          continue;
-        }
-        if (p.add) v += load_add4(p, m, n);
-        store_c4<float>(p, m, n, v);
+    for (int e = 0; e < 16; ++e) to[e] = 0.f;
+#pragma unroll 1
+    for (int kt = kt_begin; kt < kt_end; ++kt) {
+      const float sa = load_scale<kE8m0>(r.sa.p, (ra >> r.sa.shift) * r.sa.ld + kt);
+      const float by_a = __builtin_ldexpf(1.f, excess(sa));
+      const float by_b = __builtin_ldexpf(1.f, excess(load_scale<kE8m0>(r.sb.p, (rb >> r.sb.shift) * r.sb.ld + kt)));
+      floatx16 s;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] = 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int k = kt * 128 + (half * 4 + q) * 16;
+        const uint4 a = kDma ? load_codes16_of_long_rows(r.a + ra * r.lda, k, r.K) : load_codes16(r.a + ra * r.lda, k, r.K);
+        const uint4 b = kDma ? load_codes16_of_long_rows(r.b + rb * r.ldb, k, r.K) : load_codes16(r.b + rb * r.ldb, k, r.K);
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(b.x, b.y, by_b), codes_to_bf16(a.x, a.y, by_a), s, 0, 0, 0);
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(b.z, b.w, by_b), codes_to_bf16(a.z, a.w, by_a), s, 0, 0, 0);
       }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int64_t n = min(n0 + wn + j * 32 + (e >> 2) * 8 + half * 4 + (e & 3), r.N - 1);
+        const float sb = load_scale<kE8m0>(r.sb.p, (n >> r.sb.shift) * r.sb.ld + kt);
+        to[e] = fmaf(s[e], moved(sa) * moved(sb), to[e]);
+      }
+    }
+    store(r, i, j, to);
   }
 }
 

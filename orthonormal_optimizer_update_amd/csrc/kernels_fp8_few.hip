@@ -32,6 +32,7 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_few_kernel(Fp8GemmArgs p) {
 #pragma unroll
   for (int i = 0; i < kMB; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
   const int64_t srow = min(n0 + lg * 4, p.N - 1);   // kept in bounds below, too
+  bool lost = false;   // a product of scales left fp32's range
   auto step = [&](int b0, auto ahead, auto checked) __attribute__((always_inline)) {
     constexpr int kN = decltype(ahead)::value;
     uint4 rb[kN][2], ra[kN][kMB][2];
@@ -76,7 +77,11 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_few_kernel(Fp8GemmArgs p) {
           s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(ub.z, ub.w), codes_to_bf16(ua.z, ua.w), s, 0, 0, 0);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(s[e], sa[x][i] * sb[x][e], acc[i][e]);
+        for (int e = 0; e < 4; ++e) {
+          const float f = sa[x][i] * sb[x][e];
+          lost |= leaves_range<kE8m0>(f, sa[x][i], sb[x][e]);
+          acc[i][e] = fmaf(s[e], f, acc[i][e]);
+        }
       }
   };
   // whole blocks without bounds checks (a check per load would make each wait
@@ -88,8 +93,38 @@ __global__ __launch_bounds__(kWaves * 64) void fp8_few_kernel(Fp8GemmArgs p) {
   if constexpr (kAhead > 1)
     for (; kb < whole; kb += kWaves) step(kb, std::integral_constant<int, 1>{}, std::false_type{});
   if (kb < nkb) step(kb, std::integral_constant<int, 1>{}, std::true_type{});
+  if (!__any(lost)) {
 #pragma unroll
-  for (int i = 0; i < kMB; ++i) *reinterpret_cast<floatx4*>(&part[wave][i][l16][lg * 4]) = acc[i];
+    for (int i = 0; i < kMB; ++i) *reinterpret_cast<floatx4*>(&part[wave][i][l16][lg * 4]) = acc[i];
+  } else {
+    // with the excess of far scales in the conversions
+    const Fp8GemmArgs r = args_again();
+#pragma unroll 1
+    for (int i = 0; i < kMB; ++i) {
+      const int64_t ra = min(m0 + i * 16 + l16, r.M - 1), rb = min(n0 + l16, r.N - 1);
+      floatx4 to = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (kb = wave; kb < nkb; kb += kWaves) {
+        const float sa = load_scale<kE8m0>(r.sa.p, (ra >> r.sa.shift) * r.sa.ld + kb);
+        const float by_a = __builtin_ldexpf(1.f, excess(sa));
+        const float by_b = __builtin_ldexpf(1.f, excess(load_scale<kE8m0>(r.sb.p, (rb >> r.sb.shift) * r.sb.ld + kb)));
+        floatx4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = kb * 128 + h * 64 + lg * 16;
+          const uint4 a = load_codes16(r.a + ra * r.lda, k, r.K), b = load_codes16(r.b + rb * r.ldb, k, r.K);
+          s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(b.x, b.y, by_b), codes_to_bf16(a.x, a.y, by_a), s, 0, 0, 0);
+          s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(b.z, b.w, by_b), codes_to_bf16(a.z, a.w, by_a), s, 0, 0, 0);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t row = min(n0 + lg * 4 + e, r.N - 1);
+          to[e] = fmaf(s[e], moved(sa) * moved(load_scale<kE8m0>(r.sb.p, (row >> r.sb.shift) * r.sb.ld + kb)), to[e]);
+        }
+      }
+      *reinterpret_cast<floatx4*>(&part[wave][i][l16][lg * 4]) = to;
+    }
+  }
   __syncthreads();
   for (int x = threadIdx.x; x < kMB * 256; x += kWaves * 64) {
     const int i = x >> 8, m = (x >> 4) & 15, n = x & 15;

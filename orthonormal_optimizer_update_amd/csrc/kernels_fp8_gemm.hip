@@ -26,6 +26,88 @@ namespace {
 
 enum { kScaled = 0, kHardware = 1 };
 
+// The units of work, tiles of C times splits of K, of this workgroup: first,
+// first + step, ... below end.  Each XCD (workgroup id mod 8) gets a contiguous run
+// of them, walked in groups of 4 tile rows so that what runs together shares row
+// blocks in that XCD's L2.
+struct Walk {
+  int bm, bn, tiles_n, tiles_m, tiles, first, end, step;
+  __device__ __forceinline__ Walk(const Fp8GemmArgs& p, int bm_, int bn_) : bm(bm_), bn(bn_) {
+    tiles_n = (p.N + bn - 1) / bn;
+    tiles_m = (p.M + bm - 1) / bm;
+    tiles = tiles_n * tiles_m;
+    const int units = tiles * p.splits, xcd = blockIdx.x & 7, each = units >> 3, rest = units & 7;
+    const int run_first = xcd * each + min(xcd, rest);
+    end = run_first + each + (xcd < rest ? 1 : 0);
+    step = static_cast<int>(gridDim.x) < units ? gridDim.x >> 3 : units;
+    first = run_first + (blockIdx.x >> 3);
+  }
+  __device__ __forceinline__ void place(int u, int& m, int& n, int& sp) const {
+    sp = u / tiles;
+    const int tile = u - sp * tiles, group = 4 * tiles_n, g = tile / group;
+    const int gsize = min(tiles_m - g * 4, 4), in = tile - g * group, col = in / gsize;
+    m = (g * 4 + in - col * gsize) * bm;
+    n = col * bn;
+  }
+};
+
+// Of a wave's (16 kMI) x 64 of C from row m0 and column n0 on, the rows 16 i .. 16 i +
+// 15 of each bit i of `lost`, straight from memory, with what far fp32 scales have in
+// excess as operands of the instruction.  kLook: `lost` is found anew.
+template <int kMI, int kRanges, bool kLook, bool kLongRows>
+__device__ __forceinline__ void redo_rows(const Fp8GemmArgs& p, int m0, int n0, int split, uint32_t lost) {
+  const int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0)), l16 = lane & 15, lg = lane >> 4;
+  const int nkb = (p.K + kFp8Block - 1) / kFp8Block;
+  const int kt_begin = split * p.kchunk, kt_end = min(kt_begin + p.kchunk, nkb);
+  auto scale_a = [&](int64_t row, int kt) ORTHO_INLINE {
+    return load_scale<false>(p.sa.p, (min(row, (int64_t)p.M - 1) >> p.sa.shift) * p.sa.ld + kt);
+  };
+  auto scale_b = [&](int64_t row, int kt) ORTHO_INLINE {
+    return load_scale<false>(p.sb.p, (min(row, (int64_t)p.N - 1) >> p.sb.shift) * p.sb.ld + kt);
+  };
+  if constexpr (kLook) {
+    ScaleRange<kMI / 4, kRanges> range;
+#pragma unroll 1
+    for (int kt = kt_begin; kt < kt_end; ++kt) {
+#pragma unroll
+      for (int h = 0; h < kMI / 4; ++h) range.a(h, scale_a(m0 + h * 64 + lane, kt));
+      range.b(scale_b(n0 + lane, kt));
+    }
+    lost = range.lost();
+  }
+#pragma unroll 1
+  for (int ij = 0; ij < kMI * 4; ++ij) {
+    if (!(lost >> ij / 4 & 1)) continue;
+    const int m = m0 + ij / 4 * 16 + l16, n = n0 + lg * 16 + ij % 4 * 4;
+    const int row_b = n0 + l16 / 4 * 16 + l16 % 4 + ij % 4 * 4;   // the lane's of the fragment
+    const uint8_t* const src_a = p.a + (int64_t)min(m, p.M - 1) * p.lda;
+    const uint8_t* const src_b = p.b + (int64_t)min(row_b, p.N - 1) * p.ldb;
+    auto codes = [&](const uint8_t* row, int k) ORTHO_INLINE {
+      const uint4 x = kLongRows ? load_codes16_of_long_rows(row, k, p.K) : load_codes16(row, k, p.K);
+      const uint4 y = kLongRows ? load_codes16_of_long_rows(row, k + 64, p.K) : load_codes16(row, k + 64, p.K);
+      return intx8{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
+    };
+    floatx4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int kt = kt_begin; kt < kt_end; ++kt) {
+      const int k = kt * 128 + lg * 16;
+      const float a = scale_a(m, kt);
+      floatx4 s = {0.f, 0.f, 0.f, 0.f};
+      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes(src_b, k), codes(src_a, k), s, 0, 0, 0,
+                                                           127 + excess(scale_b(row_b, kt)), 0, 127 + excess(a));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = fmaf(s[e], moved(a) * moved(scale_b(n + e, kt)), c[e]);
+    }
+    if (m >= p.M) continue;
+    if (p.part) {
+      if (n < p.N) *reinterpret_cast<floatx4*>(p.part + ((int64_t)split * p.M + m) * p.ldp + n) = c;
+      continue;
+    }
+    if (p.add) c += load_add4(p, m, n);
+    store_c4<uint16_t>(p, m, n, c);
+  }
+}
+
 // A BM x BN tile of C per workgroup, kWM x kWN waves of (16 kMI) x 64.  The
 // rows of B are the matrix instruction's rows and the rows of A its columns, so
 // a lane holds four columns of one row of C per instruction and needs one scale
@@ -72,22 +154,10 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = (wave / kWN) * (kMI * 16), wn = (wave % kWN) * (kNJ * 16);
 
-  // Units of work: tiles of C times splits of K.  Each XCD (workgroup id mod 8)
-  // gets a contiguous run of them, walked in groups of 4 tile rows so that what
-  // runs together shares row blocks in that XCD's L2.
-  const int tiles_n = (p.N + BN - 1) / BN, tiles_m = (p.M + BM - 1) / BM;
-  const int tiles = tiles_n * tiles_m, units = tiles * p.splits;
-  const int xcd = blockIdx.x & 7, each = units >> 3, rest = units & 7;
-  const int run_first = xcd * each + min(xcd, rest), run_end = run_first + each + (xcd < rest ? 1 : 0);
-  const int run_step = static_cast<int>(gridDim.x) < units ? gridDim.x >> 3 : units;   // < units: kWhole only
-  auto place_unit = [&](int u, int& m, int& n, int& sp) ORTHO_INLINE {
-    sp = u / tiles;
-    const int tile = u - sp * tiles, group = 4 * tiles_n, g = tile / group;
-    const int gsize = min(tiles_m - g * 4, 4), in = tile - g * group, col = in / gsize;
-    m = (g * 4 + in - col * gsize) * BM;
-    n = col * BN;
-  };
-  int unit = run_first + (blockIdx.x >> 3), m0, n0, split;
+  const Walk walk(p, BM, BN);
+  const int run_end = walk.end, run_step = walk.step;   // step < units: kWhole only
+  auto place_unit = [&](int u, int& m, int& n, int& sp) ORTHO_INLINE { walk.place(u, m, n, sp); };
+  int unit = walk.first, m0, n0, split;
   place_unit(unit, m0, n0, split);
 
   const int nkb = (p.K + kFp8Block - 1) / kFp8Block;
@@ -294,6 +364,11 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
   // copies; the three waits after them are for copies issued before them.
   constexpr int kStores = kMI * 2;
   int stores_ahead = 0;
+  // (one register for both halves of the rows where B's scales take 16)
+  constexpr int kRanges = kRowB ? 1 : kMI / 4;
+  ScaleRange<kMI / 4, kRanges> range;   // (fp32 scales) of this unit, and the rows of
+  uint32_t lost_ever = 0;               // any unit whose products left fp32's range
+  float met[kMI / 4 + 1];
   int cur = 0, cur3 = 0;   // stage, and buffer of scales, of the k tile being computed
 
   for (;;) {
@@ -364,6 +439,21 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
           fb[j] = frag_b(next + offb + j * kBStep * 128);
           load_sb(j, next3);
         }
+        if constexpr (kMode == kScaled) {
+          // the tile's scales, read and looked at where little else is (1000 x 1537 x
+          // 1111 with a scale per row of B 17.0 us, 17.6 at slots 2 and 5)
+          constexpr int kReadAt = kMI == 8 ? 2 : 8;
+          if (slot == kReadAt) {
+            const float* const rows = reinterpret_cast<const float*>(&scales[cur3][0]);
+#pragma unroll
+            for (int h = 0; h < kMI / 4; ++h) met[h] = rows[wm + h * 64 + lane];
+            if (kRowB) met[kMI / 4] = rows[BM + wn + lane];
+          } else if (slot == kReadAt + 3) {
+#pragma unroll
+            for (int h = 0; h < kMI / 4; ++h) range.a(h, met[h]);
+            range.b(kRowB ? met[kMI / 4] : sb[0][0]);
+          }
+        }
         // the copies behind barrier M, one every second or third slot, and
         // those behind barrier E
         if (more) {
@@ -394,10 +484,13 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
     }
   }
 
+  uint32_t lost = 0;
+  if constexpr (kMode == kScaled) lost = range.lost();
   // Columns of piece j of a lane: four, next to those of piece j + 1.
   const bool whole = kWhole || n0 + wn + 64 <= p.N;
 #pragma unroll
   for (int i = 0; i < kMI; ++i) {
+    if (kMode == kScaled && (lost >> i & 1)) continue;   // below
     const int m = m0 + wm + i * 16 + l16;
     if (!kWhole && m >= p.M) continue;
     const int nl = n0 + wn + lg * 16;
@@ -426,15 +519,32 @@ __global__ __launch_bounds__(kWM * kWN * 64, 2) void fp8_gemm_kernel(Fp8GemmArgs
     }
   }
   if constexpr (kWhole) {
-    stores_ahead = p.add ? 0 : 3;   // with Add its loads were waited for, and with them all before
+    // with Add its loads were waited for, and with them all before
+    stores_ahead = p.add || lost != 0 ? 0 : 3;
+    lost_ever |= lost;
+    range = {};
     unit += run_step;
-    if (unit >= run_end) return;
+    if (unit >= run_end) break;
     place_unit(unit, m0, n0, split);
     kt_begin = split * p.kchunk;
     kt_end = min(kt_begin + p.kchunk, nkb);
   } else {
-    return;
+    lost_ever = lost;
+    break;
   }
+  }
+  if (lost_ever == 0) return;
+  // After the pipeline, and from the arguments read again: nothing of this is held in
+  // registers before (redone at a unit's end it cost 8192 x 8192 x 2048 12%).
+  if constexpr (kMode == kScaled) {
+    const Fp8GemmArgs again = args_again();
+    const Walk walk(again, BM, BN);
+    for (int u = walk.first; u < walk.end; u += walk.step) {
+      int m, n, sp;
+      walk.place(u, m, n, sp);
+      redo_rows<kMI, kRanges, kWhole, kDma>(again, m + wm, n + wn, sp, lost_ever);
+      if (!kWhole) break;
+    }
   }
 }
 
