@@ -324,14 +324,27 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
         for (int j = 0; j < 8; ++j) y[j] = v[i][j] * rs * wi[j];
         store8(static_cast<T*>(a.y) + row * a.ldy, c, a.n, y);
       }
-      const float top = max16(top8(u));
-      // (0 where the row is infinite or NaN, or eps 0 and the row too)
-      const float top_y = rsd > 0.0 && rsd < 1e300 ? static_cast<float>(top * rsd) : 0.f;
-      float scale, f;
-      block_scale<kE8m0>(top_y, scale, f);
-      // fp32 scales: 448 / top, unless the scale is the smallest or 1
-      const double g = !kE8m0 && scale > 0x1p-126f && top_y > 0.f ? 448.0 / top : rsd / scale;
-      const float gh = static_cast<float>(g), gl = static_cast<float>(g - gh);
+      // (NaN counts for nothing here, and below the codes are of y itself)
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(u[j]));
+      top = max16(top);
+      float scale, f, gh, gl;
+      if (top >= 0x1p-100f && top < __builtin_inff() && rsd > 0.0 && rsd < 1e300) {
+        block_scale<kE8m0>(static_cast<float>(top * rsd), scale, f);
+        // fp32 scales: 448 / top, unless the scale is the smallest
+        const double g = !kE8m0 && scale > 0x1p-126f ? 448.0 / top : rsd / scale;
+        gh = static_cast<float>(g);
+        gl = static_cast<float>(g - gh);
+      } else {
+        // u is not a number that stands for y: infinite (as r may be, or only the
+        // product), too small to hold its rounding error, or of a row without a factor
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = v[i][j] * rs * wi[j];
+        block_scale<kE8m0>(max16(top8(y)), scale, f);
+        gh = gl = __builtin_nanf("");
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float e = fmaf(u[j], gh, fmaf(ul[j], gh, u[j] * gl));
