@@ -396,7 +396,7 @@ __global__ __launch_bounds__(kThreads, kC <= 2 && sizeof(T) == 2 ? 4 : 1) void r
   for (int64_t row = blockIdx.x; row < a.m; row += a.groups, turn ^= 1) {
     if (!kAhead) load_row(row);
     Raw8<T> rx[kC], rg[kC], rd[kAhead ? kC : 1];
-    float sq = 0.f, dot = 0.f;
+    float sq = 0.f, dot = 0.f, unused;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       rx[i] = nx[i];
@@ -416,7 +416,27 @@ __global__ __launch_bounds__(kThreads, kC <= 2 && sizeof(T) == 2 ? 4 : 1) void r
     if (kAhead && row + a.groups < a.m) load_row(row + a.groups);
     block_sum2<kThreads>(sq, dot, red, turn);
     const float rs = 1.f / __builtin_sqrtf(sq / a.n + a.eps);
-    const float mean = dot * rs / a.n;   // mean(h u)
+    float mean = dot * rs / a.n;   // mean(h u)
+    // Of rows far from 1 (no eps, or huge), x h may leave fp32's range where u h
+    // does not: their sums are formed of u.  (The same for the workgroup.)
+    if (!(rs >= 0x1p-16f && rs <= 0x1p16f && __builtin_fabsf(dot) < __builtin_inff())) {
+      dot = unused = 0.f;
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        float x[8], g[8];
+        again(rx[i]);
+        again(rg[i]);
+        unpack8(rx[i], x);
+        unpack8(rg[i], g);
+        float (&wi)[8] = w[kAhead ? i : 0];
+        if (!kAhead) load_w8(a.w, a.w_bf, (i * kThreads + t) * 8, a.n, wi);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dot += x[j] * rs * (g[j] * wi[j]);
+      }
+      turn ^= 1;
+      block_sum2<kThreads>(dot, unused, red, turn);
+      mean = dot / a.n;
+    }
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       const int c = (i * kThreads + t) * 8;

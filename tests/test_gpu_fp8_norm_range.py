@@ -7,7 +7,7 @@ import torch
 import fp8_ref as ref
 from orthonormal_optimizer_update_amd import api
 from parity_util import note
-from test_gpu_fp8 import TYPES, check_norm, normal
+from test_gpu_fp8 import TYPES, U32, check_norm, half, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,30 @@ def test_infinite_weights_and_rows_beside_large_products():
     bad[7], bad[300], bad[20] = True, True, True
     assert torch.equal(torch.isnan(qv[3]), bad) and torch.all(sv[3] == 1)
     assert torch.all(torch.nan_to_num(qv[3]) == 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n", [(3, 200), (5, 1000), (2200, 1000), (4, 2048), (3, 4096), (1100, 8192), (2, 16384), (2, 20000)])
+def test_gradient_of_rows_far_from_one(m, n, dtype):
+    """Rows of 2^-55 without an eps under gradients of 2^-85, and of 2^55 under 2^85:
+    products of 2^-140 and 2^140, means of 2^-85 and 2^85; the gradients are 2^-30 and
+    2^30.  Ordinary rows beside them, and a zero gradient."""
+    x, dy = normal(1, m, n, dtype), normal(2, m, n, dtype, 0.25)
+    size = torch.zeros(m, 1)
+    size[0], size[m - 1] = -1.0, 1.0
+    x, dy = x * torch.exp2(55 * size).to(x.dtype), dy * torch.exp2(85 * size).to(dy.dtype)
+    w = 1 + 0.1 * normal(4, 1, n)
+    dy += x * torch.exp2(30 * size).to(dy.dtype)   # (so that the mean counts)
+    if m > 2:
+        dy[1] = 0.0
+    note(f"rms_norm_backward far rows {m}x{n} {dtype}")
+    dx, dw = api.rms_norm_backward(dy.cuda(), x.cuda(), w.cuda(), eps=0.0)
+    torch.cuda.synchronize()
+    wx, ww = ref.rms_norm_backward(dy, x, w, 0.0)
+    t = 1 / torch.sqrt(x.double().square().mean(1, keepdim=True))
+    h, u = (dy.double() * w.double()).abs(), x.double().abs() * t
+    mags = t * (h + u * (h * u).mean(1, keepdim=True))
+    tol = 2 * (n + 12) * U32 * mags + half(x.dtype) * wx.abs()
+    assert torch.all((dx.cpu().double() - wx).abs() <= tol)
+    mw = (dy.double().abs() * u).sum(0, keepdim=True)
+    assert torch.all((dw.cpu().double() - ww).abs() <= (m + n / 2 + 10) * U32 * mw)
