@@ -300,7 +300,10 @@ ortho_status dion2_step(ortho_mat X, ortho_mat G, ortho_mat M, int32_t k, int32_
  * fp32 scales use a block's whole 8-bit range.
  *
  * fp8_matmul reads rows of codes that start at multiples of 16 bytes (data and
- * ld) fastest; any other layout is accepted. */
+ * ld) fastest; any other layout is accepted.  Outputs have memory of their own,
+ * apart from the inputs, from the workspace and from each other, except where a
+ * call below says which input one may share.  Rows of one matrix may lie between
+ * another's (two halves of wider rows). */
 
 /* X (m x n, ORTHO_F32 or ORTHO_BF16) as 8-bit codes and scales.
  *   block_rows  1 (blocks of 1 x 128: activations, gradients) or 128 (blocks of
@@ -328,9 +331,10 @@ ortho_status fp8_quantize(ortho_mat X, int32_t block_rows, const ortho_mat* Q, c
  *   eps   >= 0 and finite, else ORTHO_E_PARAM.
  *   Sum   NULL, or m x n of X's dtype: receives r (the next residual, and what
  *         rms_norm_backward takes as X).  May be the same memory as X or Res,
- *         with the same ld (else ORTHO_E_LAYOUT).
+ *         with the same ld; any other overlap is refused (ORTHO_E_LAYOUT).
  *   Y     NULL, or m x n of X's dtype: receives y, e.g. to be quantised along
- *         the tokens for the weight gradient.  Memory of its own.
+ *         the tokens for the weight gradient.  Memory of its own, apart from X,
+ *         Res and Sum (else ORTHO_E_LAYOUT).
  *   Q, S  m x n ORTHO_E4M3, and m x ceil(n / 128). */
 ortho_status rms_norm_fp8(ortho_mat X, const ortho_mat* Res, ortho_mat W, float eps,
                           const ortho_mat* Sum, const ortho_mat* Y, ortho_mat Q, ortho_mat S,
@@ -350,7 +354,8 @@ size_t ortho_rms_norm_backward_workspace_size(int64_t m, int64_t n);
  *   dSum  NULL, or m x n of X's dtype: the gradient that reaches Sum along the
  *         residual, added to dX.
  *   dX    m x n of X's dtype: the gradient of X and of Res.  May be the same
- *         memory as dY, X or dSum, with the same ld (else ORTHO_E_LAYOUT).
+ *         memory as dY, X or dSum, with the same ld; any other overlap is refused
+ *         (ORTHO_E_LAYOUT).
  *   dW    1 x n, ORTHO_F32, overwritten; the rows are added in a fixed order.
  *   ws    >= ortho_rms_norm_backward_workspace_size(m, n) bytes. */
 ortho_status rms_norm_backward(ortho_mat dY, ortho_mat X, ortho_mat W, float eps,
@@ -367,7 +372,8 @@ size_t ortho_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
  *   B, SB  n x k codes, and their scales likewise; SB has SA's dtype.
  *   C      m x n, ORTHO_F32 or ORTHO_BF16 (rounded to nearest even).
  *   Add    NULL, or m x n, ORTHO_F32 or ORTHO_BF16, added in fp32 before C is
- *          rounded (a residual, or a gradient being accumulated).  May be C.
+ *          rounded (a residual, or a gradient being accumulated).  May be C; any
+ *          other overlap with it is refused (ORTHO_E_LAYOUT).
  *   ws     >= ortho_fp8_matmul_workspace_size(m, n, k) bytes.
  * Products are accumulated in fp32, in an order that depends on the sizes and
  * layouts alone.  With an ORTHO_F32 C every product counts in full.  With an

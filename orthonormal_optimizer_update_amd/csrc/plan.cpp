@@ -4,6 +4,7 @@
 #include <math.h>
 
 #include <initializer_list>
+#include <numeric>
 
 namespace ortho {
 
@@ -464,9 +465,34 @@ ortho_status check_like(const ortho_mat* a, int32_t dtype, int64_t rows, int64_t
   return shape_is(*a, rows, cols) ? ORTHO_OK : ORTHO_E_SHAPE;
 }
 
-// An output that starts where an input does has to lie over it row by row.
+int64_t element_size(const ortho_mat& a) {
+  return a.dtype == ORTHO_F32 ? 4 : (a.dtype == ORTHO_BF16 ? 2 : 1);
+}
+
+// Whether two matrices share no byte.  Rows of one may lie in the gaps between the
+// other's: the places of both repeat with the common divisor of their pitches.
+bool apart(const ortho_mat& a, const ortho_mat& b) {
+  const int64_t ea = element_size(a), eb = element_size(b);
+  const int64_t pa = a.rows > 1 ? a.ld * ea : 0, pb = b.rows > 1 ? b.ld * eb : 0;
+  const int64_t wa = a.cols * ea, wb = b.cols * eb;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.data), bt = reinterpret_cast<uintptr_t>(b.data);
+  // (the largest descriptors' sizes pass 64 bits)
+  const __int128 na = static_cast<__int128>(a.rows - 1) * pa + wa, nb = static_cast<__int128>(b.rows - 1) * pb + wb;
+  if (at >= bt ? at - bt >= nb : bt - at >= na) return true;
+  const int64_t pitch = std::gcd(pa, pb);
+  if (pitch == 0) return false;
+  const uintptr_t p = static_cast<uintptr_t>(pitch);
+  const int64_t place = static_cast<int64_t>(at >= bt ? (at - bt) % p : (p - (bt - at) % p) % p);
+  return place >= wb && place + wa <= pitch;
+}
+
+// An output may be an input's memory, row by row, or lie apart from it: threads read
+// only what they write themselves.
 bool same_or_apart(const ortho_mat* out, const ortho_mat* in) {
-  return out == nullptr || in == nullptr || out->data != in->data || out->ld == in->ld || out->rows == 1;
+  if (out == nullptr || in == nullptr) return true;
+  const bool same = out->data == in->data && out->dtype == in->dtype && out->rows == in->rows &&
+                    out->cols == in->cols && (out->ld == in->ld || out->rows == 1);
+  return same || apart(*out, *in);
 }
 
 // Codes of a rows x cols matrix and the scales of its br x 128 blocks.
@@ -552,8 +578,8 @@ ortho_status validate_rms_norm_fp8(const ortho_mat& X, const ortho_mat* Res, con
   for (const ortho_mat* t : {Res, Sum, Y})
     if ((st = check_like(t, X.dtype, X.rows, X.cols)) != ORTHO_OK) return st;
   if (!same_or_apart(Sum, &X) || !same_or_apart(Sum, Res)) return ORTHO_E_LAYOUT;
-  if (Y && (Y->data == X.data || (Res && Y->data == Res->data) || (Sum && Y->data == Sum->data)))
-    return ORTHO_E_LAYOUT;
+  for (const ortho_mat* t : {&X, Res, Sum})
+    if (Y && t && !apart(*Y, *t)) return ORTHO_E_LAYOUT;
   return check_codes(Q, S, X.rows, X.cols, 1);
 }
 
@@ -590,8 +616,7 @@ ortho_status validate_fp8_matmul(const ortho_mat& A, const ortho_mat& SA, const 
   if (Add) {
     if ((st = check_any(*Add, kReal)) != ORTHO_OK) return st;
     if (!shape_is(*Add, C.rows, C.cols)) return ORTHO_E_SHAPE;
-    // in place only where each element is read by the thread that writes it
-    if (Add->data == C.data && (Add->dtype != C.dtype || Add->ld != C.ld)) return ORTHO_E_LAYOUT;
+    if (!same_or_apart(&C, Add)) return ORTHO_E_LAYOUT;
   }
   Fp8MatmulPlan plan;
   if (!plan_fp8_matmul(A.rows, B.rows, A.cols, &plan)) return ORTHO_E_SHAPE;
