@@ -389,7 +389,10 @@ def _call(fn: str, t, *args):
 def _check_ws(ws, t):
     if ws.get_device() != t.get_device():
         raise ValueError(f"expected a workspace on {t.device}, got {ws.device}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    count = ws.numel()
+    if not ws.is_contiguous():  # an expanded tensor has fewer elements than it shows
+        count = min(count, 1 + sum((n - 1) * step for n, step in zip(ws.shape, ws.stride())))
+    return ws.data_ptr(), count * ws.element_size()
 
 
 def _blocks(n: int) -> int:

@@ -3,6 +3,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from orthonormal_optimizer_update_amd import api
 from test_fp8_cpu import BF, C8, DTYPE, E8, F, FAKE, LAYOUT, M, SHAPE, WS, ref
@@ -92,3 +93,17 @@ def test_overlaps_of_the_largest_descriptors():
     x, w, q, s = M(m, n, F, ld=ld), M(1, n, F, data=FAKE - 4096), M(m, n, C8, data=FAKE - 8192), M(m, 2, F, data=FAKE)
     for off, want in ((0, SHAPE), (4, LAYOUT), (16, SHAPE), (4 * ld, LAYOUT), (4 * ld + 16, SHAPE)):
         assert L.rms_norm_fp8(x, None, w, 1e-6, ref(M(m, n, F, ld=ld, data=FAKE + off)), None, q, s, None) == want
+
+
+def test_workspace_counts_the_bytes_behind_its_address():
+    """A tensor that repeats its elements holds only those; a strided one at least
+    as many as it has."""
+    t = torch.zeros(4, 4)
+    ws = torch.zeros(1024, dtype=torch.uint8)
+    assert api._check_ws(ws, t) == (ws.data_ptr(), 1024)
+    assert api._check_ws(ws.view(torch.float32), t) == (ws.data_ptr(), 1024)
+    assert api._check_ws(ws.view(32, 32)[:, :8], t)[1] == 256
+    assert api._check_ws(ws[::2], t)[1] == 512
+    assert api._check_ws(ws[:1].expand(1 << 20), t)[1] == 1
+    assert api._check_ws(ws[:256].view(1, 256).expand(64, 256), t)[1] == 256
+    assert api._check_ws(ws[:0], t)[1] == 0
