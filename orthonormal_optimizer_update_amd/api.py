@@ -422,11 +422,12 @@ def fp8_quantize(X, Q=None, S=None, QT=None, ST=None, block_rows: int = 1, scale
     None for what is not written."""
     if Q is None and S is None and QT is None and ST is None:
         m, n = X.shape
+        rows = max(block_rows, 1)  # (the library refuses what is not 1 or 128)
         Q = fp8_codes(m, n, X.device)
-        S = fp8_scales(m, n, X.device, block_rows, scale_dtype)
+        S = fp8_scales(m, n, X.device, rows, scale_dtype)
         if transposed:
             QT = fp8_codes(n, m, X.device)
-            ST = fp8_scales(n, m, X.device, block_rows, scale_dtype)
+            ST = fp8_scales(n, m, X.device, rows, scale_dtype)
     x, q, s, qt, st = _mats(X, Q, S, QT, ST)
     _call("fp8_quantize", X, x, block_rows, _ref(q), _ref(s), _ref(qt), _ref(st))
     return Q, S, QT, ST

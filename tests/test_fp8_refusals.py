@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from orthonormal_optimizer_update_amd import api
-from test_fp8_cpu import BF, C8, DTYPE, E8, F, FAKE, LAYOUT, M, SHAPE, WS, ref
+from test_fp8_cpu import BF, C8, DTYPE, E8, F, FAKE, LAYOUT, M, PARAM, SHAPE, WS, ref
 
 
 def apart(i):
@@ -107,3 +107,19 @@ def test_workspace_counts_the_bytes_behind_its_address():
     assert api._check_ws(ws[:1].expand(1 << 20), t)[1] == 1
     assert api._check_ws(ws[:256].view(1, 256).expand(64, 256), t)[1] == 256
     assert api._check_ws(ws[:0], t)[1] == 0
+
+
+@pytest.mark.parametrize("block_rows", [0, -1, -128])
+def test_block_rows_below_one_reach_the_library(block_rows):
+    """(Where no outputs are given they are allocated first; then comes what is wrong
+    with the call: here the device, on a GPU block_rows.)"""
+    with pytest.raises(ValueError, match="GPU"):
+        api.fp8_quantize(torch.zeros(4, 256), block_rows=block_rows)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("block_rows", [0, -1, -128, 2, 64, 256])
+def test_block_rows_other_than_1_and_128(block_rows):
+    with pytest.raises(api.OrthoError) as e:
+        api.fp8_quantize(torch.zeros(4, 256, device="cuda"), block_rows=block_rows, transposed=True)
+    assert e.value.status == PARAM
