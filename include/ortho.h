@@ -87,10 +87,12 @@ typedef struct {
 typedef enum {
   ORTHO_OK = 0,
   ORTHO_E_NULL = 1,       /* a required pointer is NULL */
-  ORTHO_E_SHAPE = 2,      /* shapes disagree, or a dimension is < 1 */
+  ORTHO_E_SHAPE = 2,      /* shapes disagree, or a dimension is < 1 or beyond a limit (2^30
+                             rows or columns, and what a call states) */
   ORTHO_E_DTYPE = 3,      /* unsupported or mismatched dtype */
   ORTHO_E_RANK = 4,       /* r outside [1, min(m, n)] or r != Q.cols */
-  ORTHO_E_LAYOUT = 5,     /* ld < cols, or a size too large to index */
+  ORTHO_E_LAYOUT = 5,     /* ld < cols or above 2^40, or operands that overlap in a way that
+                             the call does not allow */
   ORTHO_E_WORKSPACE = 6,  /* ws is NULL or ws_bytes is below the required size */
   ORTHO_E_PARAM = 7,      /* mu outside [0,1], non-finite lr/scale/abc, steps < 0, batch < 1,
                              eps < 0 or non-finite, block_rows other than 1 and 128 */
@@ -316,7 +318,8 @@ ortho_status dion2_step(ortho_mat X, ortho_mat G, ortho_mat M, int32_t k, int32_
  *     ORTHO_F32   s = max(a / 448, 2^-126), code = x * (1 / s) to nearest even
  *     ORTHO_E8M0  s = the smallest power of two >= 2^-126 with a <= 448 s
  * and s = 1 for a = 0.  Infinite and NaN elements get the NaN code and do not
- * enter a, so they spoil no other element. */
+ * enter a, so they spoil no other element.  X has fewer than 2^24 blocks of
+ * 128 x 128 (else ORTHO_E_SHAPE). */
 ortho_status fp8_quantize(ortho_mat X, int32_t block_rows, const ortho_mat* Q, const ortho_mat* S,
                           const ortho_mat* QT, const ortho_mat* ST, void* stream);
 
@@ -375,12 +378,17 @@ size_t ortho_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
  *          rounded (a residual, or a gradient being accumulated).  May be C; any
  *          other overlap with it is refused (ORTHO_E_LAYOUT).
  *   ws     >= ortho_fp8_matmul_workspace_size(m, n, k) bytes.
+ * C has fewer than 2^24 tiles of 128 x 128 (else ORTHO_E_SHAPE, and a workspace
+ * size of 0).
  * Products are accumulated in fp32, in an order that depends on the sizes and
  * layouts alone.  With an ORTHO_F32 C every product counts in full.  With an
- * ORTHO_BF16 C of more than a few rows the 8-bit matrix instruction is used,
- * which cuts each product below 2^-13 of the largest of its group of eight
- * neighbours along k (about 1e-5 of the result, against the 2^-9 of C's
- * rounding).  The product of an element's two scales need not be an fp32 number,
+ * ORTHO_BF16 C of more than 32 rows (or 2^25 columns) the 8-bit matrix instruction
+ * is used, which cuts what the products of a group of eight neighbours along k have below 2^-13
+ * of the largest of them: an element is off by at most 7 * 2^-13 of each group's
+ * largest product, summed over the groups.  For normally distributed operands
+ * that is typically 1e-5 of the result (C's rounding is up to 2^-8 of it);
+ * where large products cancel it can be any part of it, and an ORTHO_F32 C is the
+ * one to ask for.  The product of an element's two scales need not be an fp32 number,
  * only the element.  A NaN code or scale reaches the elements of C that it enters
  * into, and no others. */
 ortho_status fp8_matmul(ortho_mat A, ortho_mat SA, ortho_mat B, ortho_mat SB, ortho_mat C,

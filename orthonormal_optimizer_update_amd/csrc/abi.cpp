@@ -874,7 +874,7 @@ const char* ortho_status_str(int32_t status) {
     case ORTHO_E_SHAPE: return "matrix shapes disagree or a dimension is out of range";
     case ORTHO_E_DTYPE: return "unsupported or mismatched dtype";
     case ORTHO_E_RANK: return "rank r outside [1, min(m, n)] or different from Q.cols";
-    case ORTHO_E_LAYOUT: return "leading dimension smaller than cols, or differs within a group";
+    case ORTHO_E_LAYOUT: return "leading dimension smaller than cols or too large, differs within a group, or operands overlap";
     case ORTHO_E_WORKSPACE: return "workspace missing, too small or not 256-byte aligned";
     case ORTHO_E_PARAM: return "invalid scalar parameter (mu, lr, scale, abc, steps, batch, eps or block_rows)";
     case ORTHO_E_HIP: return "a HIP launch failed";

@@ -123,3 +123,17 @@ def test_block_rows_other_than_1_and_128(block_rows):
     with pytest.raises(api.OrthoError) as e:
         api.fp8_quantize(torch.zeros(4, 256, device="cuda"), block_rows=block_rows, transposed=True)
     assert e.value.status == PARAM
+
+
+def test_limits_of_sizes():
+    """2^24 blocks or tiles of 128 x 128, and 2^30 rows or columns."""
+    L = api.lib()
+
+    need = api.fp8_matmul_workspace_size
+    assert need(1 << 30, 128, 1) > 0 and need(1 << 30, 256, 1) == 0 and need((1 << 30) + 1, 1, 1) == 0
+    m, n = 1 << 30, 256
+    got = L.fp8_matmul(M(m, 1, C8), M(m, 1, F, data=apart(1)), M(n, 1, C8, data=apart(2)), M(n, 1, F, data=apart(3)),
+                       M(m, n, BF, data=apart(4)), None, ctypes.c_void_p(FAKE), 1 << 40, None)
+    assert got == SHAPE
+    x, q, s = M(1 << 20, 1 << 18, F), M(1 << 20, 1 << 18, C8, data=apart(1)), M(1 << 20, 1 << 11, F, data=apart(2))
+    assert L.fp8_quantize(x, 1, ref(q), ref(s), None, None, None) == SHAPE   # 2^24 blocks
