@@ -22,8 +22,8 @@ namespace {
 // before the last chunk's products: the stage is then free, and the copies of
 // the tile after next have a whole tile's time to arrive.
 //
-// 8192 x 2048 x 8192 takes 310 us with fp32 scales, 0.89 PFLOP/s, 320 where B
-// has a scale per row, and 347 with e8m0 ones; the matrix cores are busy 41% of it.
+// 8192 x 2048 x 8192 takes 252 us with fp32 or e8m0 scales, 1.09 PFLOP/s, and 285
+// (e8m0 318) where B has a scale per row, with the matrix cores busy 43% of it.
 template <bool kE8m0, bool kRowB, bool kDma>
 __global__ __launch_bounds__(256, 2) void fp8_exact_kernel(Fp8GemmArgs p) {
   constexpr int BM = 128, BN = 128, kStage = (BM + BN) * 128, kCopies = 8;

@@ -158,8 +158,8 @@ void by_depth(const Fp8GemmArgs& a, hipStream_t s) {
 template <bool kE8m0>
 void by_rows(const Fp8GemmArgs& a, hipStream_t s) {
   // 16 or 32 rows of A per workgroup.  Where B's rows alone do not give every
-  // CU one, 16 (24 x 2048 x 8192: 15.0 us with 32 rows, 10.8 with 16;
-  // 32 x 8192 x 2048: 9.4 and 12.6 us).
+  // CU one, 16 (24 x 2048 x 8192: 14.9 us with 32 rows, 11.7 with 16;
+  // 32 x 8192 x 2048: 10.0 and 12.3 us).
   if (a.M <= 16) by_depth<kE8m0, 1, 4>(a, s);
   else if ((a.N + 15) / 16 >= 256) by_depth<kE8m0, 2, 2>(a, s);
   else by_depth<kE8m0, 1, 2>(a, s);

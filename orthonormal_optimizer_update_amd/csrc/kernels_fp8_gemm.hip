@@ -118,8 +118,9 @@ __device__ __forceinline__ void redo_rows(const Fp8GemmArgs& p, int m0, int n0, 
 // element: no alignment is needed).  C is
 // written straight from the accumulators, so the LDS is free at once for the
 // next copies, which overlap the stores.  (kWhole: M, N multiples of 256 and K of
-// 128.  8192 x 8192 x 2048 takes 136 us with fp32 scales, 2.02 PFLOP/s, and 126
-// with e8m0 ones; its C alone is 26 us of a copy's rate.)
+// 128.  8192 x 8192 x 2048 takes 135 us with fp32 scales, 2.04 PFLOP/s, and 123
+// with e8m0 ones; its C alone is 26 us of a copy's rate.  8190 rows, and with
+// them one tile per workgroup and checked rows, take 146 and 133.)
 //
 // A k tile is one block of 128: 128-byte LDS rows of eight 16-byte chunks, two
 // stages.  B's fragments and the scales of a tile sit in registers from its
@@ -577,10 +578,14 @@ void launch(const Fp8GemmArgs& a, hipStream_t s) {
 template <int kMode, bool kRowB>
 void by_tile(const Fp8GemmArgs& a, hipStream_t s) {
   const bool whole = a.M % 256 == 0 && a.N % 256 == 0 && a.K % kFp8Block == 0;
+  // (codes at any byte go through registers: 8192 x 8192 x 2047 150 us with rows at
+  // multiples of 16 bytes, 476 without)
   if (!a.dma || a.K < 16) return launch<kMode, kRowB, 2, 2, 4, 4, false, false>(a, s);
-  // 256 x 256 tiles from 160 of them on (below, the CUs without one cost more
-  // than twice the copies do: 4096 x 2048 x 2048 34.3 us with them, 27.5 on
-  // 128 x 128; 4096 x 2800 x 2048 40.8 and 49.3 us)
+  // 256 x 256 tiles from a C of 160 of them on (below, the CUs without one cost
+  // more than twice the copies do: 4096 x 2048 x 2048 32.7 us with them, 25.4 on
+  // 128 x 128; 4096 x 2800 x 2048 35.2 and 39.3 us, 8192^3 486 and 645).  The rule
+  // looks at the area alone: where M or N is under 256, parts of the tiles are
+  // empty (96 x 131072 x 2048: 77 us, 65 on 128 x 128).
   if ((int64_t)a.M * a.N >= 256 * 256 * 160) {
     if (whole) return launch<kMode, kRowB, 2, 4, 8, 4, true, true>(a, s);
     return launch<kMode, kRowB, 2, 4, 8, 4, true, false>(a, s);

@@ -1,9 +1,16 @@
 // Conversion to 8-bit codes with block scales, and the RMS norm around it: the
 // residual's addition, the 8-bit output and the gradient.  All are bound by
 // HBM traffic: each element is read once, held in registers, and written once
-// per output.  In bf16: quantisation by rows of 8192 x 4096 20.2 us (5.0 TB/s),
-// both orientations 31 (4.3); the norm with residual, sum and y 53 (5.7); the
-// gradient 48 (5.6).  In fp32, 4096 x 8192: 28 (6.0), 42 (4.8), 126 (4.5), 109 (4.9).
+// per output.  In bf16, with new operands in every call: quantisation by rows of
+// 8192 x 4096 24.0 us (4.2 TB/s), both orientations 34.8 (3.9); the norm with
+// residual, sum and y 58.6 (5.2); the gradient with dSum 59.9 (4.5).  In fp32, 4096 x
+// 8192: 30.1 (5.6), 47.6 (4.2), 124 (4.6), 117 (4.6).  (A copy of 1 GiB: 5.1.)
+//
+// Not so for the norms' longest rows: over 16384 columns (the fp32 gradient: over
+// 8192) a thread's pieces pass its 128 registers and go through scratch.  1024 x
+// 32768 in bf16: norm 164 us (66.8 as 2048 x 16384), gradient 232 (82.9); in fp32
+// 249 (126) and 383 (145).  Nor for rows of 128, which fill a quarter of a wave:
+// 131072 x 128 in bf16 takes 104 us (1.5 TB/s), its gradient 165.
 #include <type_traits>
 
 #include "fp8.h"
@@ -243,7 +250,7 @@ __device__ __forceinline__ void load_w8(const void* w, int w_bf, int c, int n, f
 
 // A workgroup takes the rows g, g + groups, ..., 8 kC elements per thread.  Up
 // to kC = 2 W stays in registers, and the next row's loads go out before this
-// row's sum is waited for; longer rows need the registers for themselves (so
+// row's sum is waited for; longer rows need more registers than there are (so
 // do fp32 rows of over 8192 in the gradient).
 //   r = round(x + res), t = 1 / sqrt(mean r^2 + eps), y = r t w
 // The sum is rounded to its storage type first and the rounded one is
@@ -256,7 +263,8 @@ __device__ __forceinline__ void load_w8(const void* w, int w_bf, int c, int n, f
 // fp32.  What is left are the roundings of max|u| (of the row's sum, with
 // power-of-two scales) and of the result before the one to e4m3: of the 33.5
 // million codes of 8192 x 4096 about 14 are on the other side of a tie (20
-// without the second fp32s, which cost 4% of the time in bf16).
+// without the second fp32s, which cost 4% of the time in bf16).  Blocks whose u is
+// no number that stands for y take the codes from y.
 template <typename T, bool kE8m0, int kThreads, int kC>
 __global__ __launch_bounds__(kThreads) void rms_norm_fp8_kernel(NormArgs a) {
   __shared__ float red[2][2][kThreads / 64];

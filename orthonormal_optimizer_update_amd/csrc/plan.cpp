@@ -531,8 +531,8 @@ bool plan_fp8_matmul(int64_t m, int64_t n, int64_t k, Fp8MatmulPlan* p) {
   // One workgroup per CU, of at least three blocks (its first copies take about
   // two blocks' time to arrive), and only where the blocks saved, about 1 us
   // each, outweigh the second launch and its traffic, about 6 us:
-  // 1000 x 1536 x 1024 takes 11.4 us whole and 17.9 in two, 65 x 2048 x 8192
-  // 57 us whole and 15 in 16.
+  // 1000 x 1536 x 1024 takes 11.1 us whole and 18.2 in two, 65 x 2048 x 8192
+  // 58 us whole, 34 in two and 15 in 16.
   int64_t splits = m <= kFewRowsMax ? 1 : kCus / tiles;
   if (splits > nkb / 3) splits = nkb / 3;
   if (splits < 1 || nkb - cdiv(nkb, splits) < 8) splits = 1;

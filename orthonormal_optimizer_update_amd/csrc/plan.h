@@ -155,14 +155,15 @@ ortho_status validate_muon(int32_t batch, const ortho_mat* X, const ortho_mat* G
 
 // 8-bit operators (fp8_quantize, rms_norm_fp8, rms_norm_backward, fp8_matmul).
 constexpr int64_t kFp8BlockSize = 128;
-// Longest row of the norms: it stays in one workgroup's registers.
+// Longest row of the norms: one workgroup of 1024 threads, 32 elements each (from
+// 16385 columns on through scratch memory).
 constexpr int64_t kNormMaxCols = 32768;
 
 // The product on 128 x 128 tiles of C splits K where there are fewer tiles than
 // CUs: `splits` ranges of `kchunk` blocks of 128, whose fp32 sums (rows
 // of ldp) meet in the workspace and are added in order.
-// Rows of A that take the kernel for few rows (48 x 8192 x 2048: 17.8 us with
-// it, 12.8 on tiles; 48 x 2048 x 8192: 21.5 and 13.5 us).
+// Rows of A that take the kernel for few rows (48 x 8192 x 2048: 17.3 us with
+// it, 12.6 on tiles; 48 x 2048 x 8192: 21.6 and 13.5 us).
 constexpr int64_t kFewRowsMax = 32;
 struct Fp8MatmulPlan {
   int splits, kchunk;
