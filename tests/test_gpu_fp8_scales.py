@@ -7,7 +7,7 @@ import torch
 import fp8_ref as ref
 from orthonormal_optimizer_update_amd import api
 from parity_util import note
-from test_gpu_fp8 import TYPES, check_product, group_tops, matmul_reference, upload
+from test_gpu_fp8 import TYPES, check_product, group_tops, matmul_reference, padded, upload
 
 pytestmark = pytest.mark.gpu
 
@@ -47,9 +47,9 @@ def operand(seed, rows, k, block_rows, patterns, dtype):
     return q, s
 
 
-def check(a, sa, bra, b, sb, brb, out):
+def check(a, sa, bra, b, sb, brb, out, place=upload):
     m, n, k = a.size(0), b.size(0), a.size(1)
-    c = api.fp8_matmul(upload(a), sa.cuda(), upload(b), sb.cuda(), out_dtype=out)
+    c = api.fp8_matmul(place(a), sa.cuda(), place(b), sb.cuda(), out_dtype=out)
     torch.cuda.synchronize()
     want, mags = matmul_reference(a, sa, bra, b, sb, brb)
     assert torch.all(mags < 3e38)
@@ -80,6 +80,19 @@ def test_products_of_scales_beyond_fp32(m, n, k, scale, out):
         b, sb = operand(2, n, k, brb, POWERS_B, dtype)
         note(f"fp8_matmul scales beyond fp32 {m}x{n}x{k} {scale} blocks {bra}/{brb} {out}")
         check(a, sa, bra, b, sb, brb, TYPES[out])
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("m,n,k", [(5, 300, 260), (300, 400, 520), (60, 390, 1701), (130, 260, 15), (40, 300, 3), (9, 100, 9)])
+def test_products_of_scales_beyond_fp32_with_codes_at_any_byte(m, n, k, scale, out):
+    """The same with rows of codes at any byte, and rows shorter than 16."""
+    dtype = torch.float32 if scale == "f32" else torch.float8_e8m0fnu
+    for bra, brb in ((1, 128), (1, 1)):
+        a, sa = operand(1, m, k, bra, POWERS_A, dtype)
+        b, sb = operand(2, n, k, brb, POWERS_B if k > 100 else POWERS_B[:1] + POWERS_B[2:], dtype)
+        note(f"fp8_matmul scales beyond fp32 at any byte {m}x{n}x{k} {scale} blocks {bra}/{brb} {out}")
+        check(a, sa, bra, b, sb, brb, TYPES[out], lambda t: padded(t, 3, 1)[0])
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
