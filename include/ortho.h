@@ -27,6 +27,12 @@
  *                  its products (the weight gradient G among them), the norm
  *                  before it and the conversion of its operands (declared
  *                  below, after the steps).
+ *   adamw_step, grad_norm
+ *                  AdamW over many tensors at once, for the parameters that take
+ *                  no orthonormal update, and the gradients' clipping.
+ *   expert_sort, expert_gather, expert_combine, expert_combine_backward
+ *                  tokens to the rows of a mixture-of-experts layer's products
+ *                  and back.
  *   newton_schulz  Muon's Newton-Schulz orthogonalisation, the full-rank
  *                  comparison path.  Same talk, passage contrasting SGD with an
  *                  orthonormal update (take U V^T of the SVD) and the passage on
@@ -95,7 +101,8 @@ typedef enum {
                              the call does not allow */
   ORTHO_E_WORKSPACE = 6,  /* ws is NULL or ws_bytes is below the required size */
   ORTHO_E_PARAM = 7,      /* mu outside [0,1], non-finite lr/scale/abc, steps < 0, batch < 1,
-                             eps < 0 or non-finite, block_rows other than 1 and 128 */
+                             eps < 0 or non-finite, block_rows other than 1 and 128, and what
+                             a call states */
   ORTHO_E_HIP = 8,        /* a HIP launch failed (no device, invalid stream, ...) */
   ORTHO_E_SCRATCH = 9     /* dion_step_noalloc: the problem needs more than
                              ORTHO_NOALLOC_SCRATCH_BYTES of workspace */
@@ -393,6 +400,168 @@ size_t ortho_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
  * into, and no others. */
 ortho_status fp8_matmul(ortho_mat A, ortho_mat SA, ortho_mat B, ortho_mat SB, ortho_mat C,
                         const ortho_mat* Add, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- parameters that take no orthonormal update ----------------------------
+ *
+ * Embeddings, heads, norms' weights, routers: AdamW over all of them in a few
+ * launches, and the gradients' norm by which a program clips.  The tensors of a
+ * call are HOST arrays of `count` descriptors, read during the call only, of any
+ * mix of shapes and dtypes; a vector is a matrix of one row.  A tensor has at most
+ * 2^40 elements (else ORTHO_E_SHAPE). */
+
+/* Bytes of device workspace for grad_norm on `count` tensors.  Returns 0 for
+ * count < 1.  256-byte alignment required. */
+size_t ortho_grad_norm_workspace_size(int32_t count);
+
+/* The length of all gradients together, and the factor that clips it:
+ *     out[0] = norm = sqrt(sum of the squares of all elements of all G)
+ *     out[1] = max_norm / norm where norm > max_norm, else 1;
+ *              NaN where an element is infinite or NaN
+ *   G         ORTHO_F32 or ORTHO_BF16 each; read only, and may overlap.
+ *   max_norm  > 0 (infinite: no clipping), else ORTHO_E_PARAM.
+ *   out       DEVICE array of two floats, apart from every G (else
+ *             ORTHO_E_LAYOUT).
+ *   ws        >= ortho_grad_norm_workspace_size(count) bytes.
+ * The squares are added in fp64, in an order that the sizes and layouts fix. */
+ortho_status grad_norm(int32_t count, const ortho_mat* G, double max_norm, float* out, void* ws,
+                       size_t ws_bytes, void* stream);
+
+typedef struct {
+  double lr;
+  double beta1, beta2;     /* in [0, 1) */
+  double eps;              /* >= 2^-126 */
+  double weight_decay;     /* >= 0 */
+  int64_t step;            /* t of the bias corrections: 1 at the first step */
+  uint64_t seed;           /* of the stochastic rounding */
+  int32_t stochastic;      /* 0: what is rounded to fewer bits goes to nearest even */
+  const float* lr_dev;     /* NULL, or a DEVICE float that is read in place of lr, */
+  const int64_t* step_dev; /* NULL, or a DEVICE int64 that is read in place of step (less than 1
+                              counts as 1): what a captured graph's replays see anew */
+  const float* factor;     /* NULL, or a DEVICE float that multiplies the gradients (grad_norm's
+                              out + 1, or what undoes a loss's scale).  NaN: the call leaves
+                              weights and states as they were */
+} ortho_adamw;
+
+/* One AdamW step, in place, on `count` tensors.  With g = G * factor, in fp32:
+ *     m  = beta1 m + (1 - beta1) g
+ *     v  = beta2 v + (1 - beta2) g^2
+ *     X  = (1 - lr weight_decay) X
+ *          - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *   X, G   ORTHO_F32 or ORTHO_BF16 each, of one shape.
+ *   M, V   of X's shape: both ORTHO_F32 (m and v), or both ORTHO_E4M3, the codes
+ *          of m and of sqrt(v) with a scale for each block of 1 x 128.  Tensors of
+ *          either kind may share a call.
+ *   SM, SV the scales of the tensors whose states are codes, ORTHO_F32, rows x
+ *          ceil(cols / 128); entries of other tensors are not looked at.  NULL
+ *          where no tensor has codes.
+ * States start at zero (any finite scale beside codes of 0).  X, M, V, SM and SV
+ * have memory of their own, apart from each other, from those of every other tensor
+ * and from every G (else ORTHO_E_LAYOUT; rows between another matrix's rows are
+ * apart): a weight that is listed twice is refused.
+ *
+ * The step uses m and v as computed; only what is kept for the next one is rounded.
+ * A block's scale is its largest finite |m| (or sqrt(v)) / 448, at least 2^-126, and
+ * 1 for a block of zeros; infinite and NaN values get the NaN code.  A v above 0
+ * never gets the code of 0 (the least code, 2^-9, in its place), so that no later
+ * step divides by nothing but eps.
+ *
+ * Stochastic rounding of bf16 weights and of codes: with u random bits out of
+ * 2^n, a value that lies a part p of the way from one number of the type to the
+ * next one away from zero goes there if u / 2^n + p >= 1, so that on the average
+ * what is small beside a step of the type still counts (codes: n = 20, of |value /
+ * scale| <= 448; weights: n = 16, the bits below bf16's as they are in fp32).  The
+ * bits come from (seed, t, index of the tensor in the call, index of the element
+ * row * cols + column) alone:
+ *     mix(h): h ^= h >> 16, h *= 0x7feb352d, h ^= h >> 15, h *= 0x846ca68b,
+ *             h ^= h >> 16                                          (32 bits)
+ *     key = mix(low word of seed); then key = mix(key ^ mix(word + 0x9e3779b9))
+ *           for the words seed's high, t's low, t's high, tensor
+ *     a = mix(element's low word ^ (key + 0x9e3779b9 * its high word))
+ *     b = mix(a + 0x9e3779b9)
+ *     m: a >> 12;   sqrt(v): b >> 12;   weight: (a & 4095) << 4 | (b & 15)
+ * ORTHO_E_PARAM: lr, eps or weight_decay not finite in fp32, or a value outside
+ * what is stated above. */
+ortho_status adamw_step(int32_t count, const ortho_mat* X, const ortho_mat* G, const ortho_mat* M,
+                        const ortho_mat* V, const ortho_mat* SM, const ortho_mat* SV,
+                        const ortho_adamw* h, void* stream);
+
+/* ---- tokens by expert --------------------------------------------------------
+ *
+ * A mixture-of-experts layer has one weight matrix of each kind per expert: a
+ * group for the batched steps above.  Each token (a row of x) goes to `choices`
+ * experts, and the rows of one expert are brought together for its products:
+ *     expert_sort                which row each (token, choice) gets
+ *     expert_gather              tokens to rows, in 16 or 32 bits, or as codes
+ *     (fp8_matmul on each expert's rows)
+ *     expert_combine             rows back to tokens, with weights applied
+ *     expert_combine_backward    its gradient
+ * The gradient of expert_gather is expert_combine without weights.
+ *
+ * What the calls share: `slot` is a DEVICE array of tokens x choices int32, the row
+ * of each pair, or -1; any value below 0 or from the number of rows on counts as -1
+ * and no other row is in it twice.  `offsets` (experts + 1 int32) and `counts`
+ * (experts) say where each expert's rows begin and how many there are: rows
+ * offsets[e] + counts[e] .. offsets[e + 1] - 1 are padding, and rows from
+ * offsets[experts] on belong to no one and are left as they were.  tokens * choices
+ * and the rows stay below 2^30, choices is 1 to 64, experts 1 to 1024. */
+
+/* Rows that `tokens` x `choices` pairs take at most: tokens * choices + experts *
+ * (align - 1).  0 for sizes that expert_sort refuses. */
+int64_t ortho_expert_rows(int64_t tokens, int32_t choices, int32_t experts, int32_t align);
+
+/* Bytes of device workspace for expert_sort.  Returns 0 for invalid sizes.
+ * 256-byte alignment required. */
+size_t ortho_expert_sort_workspace_size(int64_t tokens, int32_t choices, int32_t experts);
+
+/* Rows for the pairs, ordered by expert and within an expert by token, then
+ * choice; each expert's first row is a multiple of `align`.
+ *   chosen   DEVICE array of tokens x choices experts, int32 (chosen_bytes 4) or
+ *            int64 (8).  What is no expert's number (-1, say) takes no row.  An expert
+ *            may be there twice for a token.
+ *   align    1 to 4096; with 128, blocks of fp8_quantize along the rows never hold
+ *            two experts' rows.
+ *   slot     receives the rows (-1 for pairs without one).
+ *   source   NULL, or receives for each of ortho_expert_rows(...) rows the pair in it
+ *            (token * choices + choice), -1 for rows without one.
+ *   offsets, counts   as above.
+ * Outputs are apart from `chosen` and from each other (else ORTHO_E_LAYOUT). */
+ortho_status expert_sort(const void* chosen, int32_t chosen_bytes, int64_t tokens, int32_t choices,
+                         int32_t experts, int32_t align, int32_t* slot, int32_t* source,
+                         int32_t* offsets, int32_t* counts, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* Y[slot[t, j]] = X[t]; rows of padding become zeros (codes of 0 with a scale of 1).
+ *   X, S    tokens x n, ORTHO_F32, ORTHO_BF16 or ORTHO_E4M3; for codes with S, the
+ *           scales of their 1 x 128 blocks, else S = NULL.
+ *   Y, SY   rows x n of X's dtype, and for codes their scales of S's dtype.  Memory
+ *           of their own (else ORTHO_E_LAYOUT). */
+ortho_status expert_gather(ortho_mat X, const ortho_mat* S, const int32_t* slot, int32_t choices,
+                           const int32_t* offsets, const int32_t* counts, int32_t experts,
+                           ortho_mat Y, const ortho_mat* SY, void* stream);
+
+/* Out[t] = sum over j of W[t, j] Y[slot[t, j]] (+ Add[t]), summed in fp32 in the
+ * order of j, rounded once; pairs without a row add nothing.
+ *   Y     rows x n, ORTHO_F32 or ORTHO_BF16.
+ *   W     NULL (every weight 1), or tokens x choices, ORTHO_F32 or ORTHO_BF16.
+ *   Add   NULL, or tokens x n, ORTHO_F32 or ORTHO_BF16.  May be Out; any other
+ *         overlap with it is refused (ORTHO_E_LAYOUT).
+ *   Out   tokens x n of Y's dtype, apart from Y and W (else ORTHO_E_LAYOUT). */
+ortho_status expert_combine(ortho_mat Y, const int32_t* slot, int32_t choices, const ortho_mat* W,
+                            const ortho_mat* Add, ortho_mat Out, void* stream);
+
+/* Gradient of expert_combine:
+ *     dY[slot[t, j]] = W[t, j] dOut[t],  rows of padding 0
+ *     dW[t, j] = sum over the columns of dOut[t] Y[slot[t, j]], 0 without a row
+ *   dOut  tokens x n, ORTHO_F32 or ORTHO_BF16 (Add's gradient is dOut itself).
+ *   W     as in the forward call.
+ *   dY    rows x n of dOut's dtype.  May be the same memory as Y, with the same ld;
+ *         apart from dOut and W, and from Y otherwise (else ORTHO_E_LAYOUT).
+ *   Y, dW both NULL, or rows x n of dOut's dtype, and tokens x choices ORTHO_F32
+ *         (summed in fp32 in an order that n fixes), apart from the others. */
+ortho_status expert_combine_backward(ortho_mat dOut, const int32_t* slot, int32_t choices,
+                                     const ortho_mat* W, const int32_t* offsets,
+                                     const int32_t* counts, int32_t experts, ortho_mat dY,
+                                     const ortho_mat* Y, const ortho_mat* dW, void* stream);
 
 /* Static English description of a status code. */
 const char* ortho_status_str(int32_t status);

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -27,6 +28,13 @@ MUON_ABC = (3.4445, -4.7750, 2.0315)
 class OrthoMat(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
                 ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class OrthoAdamw(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("seed", ctypes.c_uint64), ("stochastic", ctypes.c_int32), ("lr_dev", ctypes.c_void_p),
+                ("step_dev", ctypes.c_void_p), ("factor", ctypes.c_void_p)]
 
 
 class OrthoError(RuntimeError):
@@ -93,6 +101,32 @@ _SIGS = {
     "fp8_matmul": (ctypes.c_int, [OrthoMat, OrthoMat, OrthoMat, OrthoMat, OrthoMat,
                                   ctypes.POINTER(OrthoMat), ctypes.c_void_p, ctypes.c_size_t,
                                   ctypes.c_void_p]),
+    "ortho_grad_norm_workspace_size": (ctypes.c_size_t, [ctypes.c_int32]),
+    "grad_norm": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(OrthoMat), ctypes.c_double,
+                                 ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "adamw_step": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(OrthoMat), ctypes.POINTER(OrthoMat),
+                                  ctypes.POINTER(OrthoMat), ctypes.POINTER(OrthoMat),
+                                  ctypes.POINTER(OrthoMat), ctypes.POINTER(OrthoMat),
+                                  ctypes.POINTER(OrthoAdamw), ctypes.c_void_p]),
+    "ortho_expert_rows": (ctypes.c_int64, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                           ctypes.c_int32]),
+    "ortho_expert_sort_workspace_size": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int32,
+                                                           ctypes.c_int32]),
+    "expert_sort": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
+                                   ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                   ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                   ctypes.c_void_p]),
+    "expert_gather": (ctypes.c_int, [OrthoMat, ctypes.POINTER(OrthoMat), ctypes.c_void_p,
+                                     ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                     OrthoMat, ctypes.POINTER(OrthoMat), ctypes.c_void_p]),
+    "expert_combine": (ctypes.c_int, [OrthoMat, ctypes.c_void_p, ctypes.c_int32,
+                                      ctypes.POINTER(OrthoMat), ctypes.POINTER(OrthoMat), OrthoMat,
+                                      ctypes.c_void_p]),
+    "expert_combine_backward": (ctypes.c_int, [OrthoMat, ctypes.c_void_p, ctypes.c_int32,
+                                               ctypes.POINTER(OrthoMat), ctypes.c_void_p,
+                                               ctypes.c_void_p, ctypes.c_int32, OrthoMat,
+                                               ctypes.POINTER(OrthoMat), ctypes.POINTER(OrthoMat),
+                                               ctypes.c_void_p]),
     "ortho_status_str": (ctypes.c_char_p, [ctypes.c_int32]),
     "ortho_abi_version": (ctypes.c_int32, []),
 }
@@ -336,11 +370,7 @@ _DTYPES = None
 def _mats(*tensors):
     """Descriptors of 2-D tensors on one GPU (None stays None), which may hold
     8-bit codes and scales."""
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.float32: ORTHO_F32, torch.bfloat16: ORTHO_BF16,
-                   torch.float8_e4m3fn: ORTHO_E4M3, torch.float8_e8m0fnu: ORTHO_E8M0}
+    _mats_dtypes()
     dtypes, device, out = _DTYPES, tensors[0].get_device(), []
     if device < 0:
         raise ValueError(f"expected tensors on a GPU, got {tensors[0].device}")
@@ -483,3 +513,303 @@ def fp8_matmul(A, SA, B, SB, out=None, add=None, ws=None, out_dtype=None):
     a, sa, b, sb, c, ad = _mats(A, SA, B, SB, out, add)
     _call("fp8_matmul", A, a, sa, b, sb, c, _ref(ad), *_check_ws(ws, A))
     return out
+
+
+# ---------------------------------------------------------------------------
+# AdamW over many tensors, and the gradients' norm
+# ---------------------------------------------------------------------------
+
+
+class MatList:
+    """Descriptors of a list of tensors, for calls over many of them; see ``mats``."""
+
+    __slots__ = ("tensors", "first", "array", "_pointers")
+
+    def __init__(self, tensors):
+        self.tensors = tuple(tensors)
+        self.first = next((t for t in self.tensors if t is not None), None)
+        if self.first is None:
+            raise ValueError("expected at least one tensor")
+        self._describe()
+
+    def _describe(self):
+        _mats_dtypes()
+        dtypes, device, fields, pointers = _DTYPES, self.first.get_device(), [], []
+        if device < 0:
+            raise ValueError(f"expected tensors on a GPU, got {self.first.device}")
+        for t in self.tensors:
+            if t is None:
+                pointers.append(0)
+                fields += (0, 0, 0, 0, 0)
+                continue
+            if t.get_device() != device:
+                raise ValueError(f"expected every tensor on {self.first.device}, got {t.device}")
+            dt = dtypes.get(t.dtype)
+            if dt is None:
+                raise ValueError(f"unsupported dtype {t.dtype}")
+            rows, cols, ld = _rows_of(t)
+            at = t.data_ptr()
+            pointers.append(at)
+            fields += (at, rows, cols, ld, dt)
+        count = len(pointers)
+        self.array = (OrthoMat * count)()
+        struct.pack_into("Pqqqi4x" * count, self.array, 0, *fields)
+        self._pointers = pointers
+
+    def __len__(self):
+        return len(self.tensors)
+
+    def current(self):
+        """The descriptors, taken anew if a tensor's memory is another one by now."""
+        if [0 if t is None else t.data_ptr() for t in self.tensors] != self._pointers:
+            self._describe()
+        return self.array
+
+
+def _mats_dtypes():
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float32: ORTHO_F32, torch.bfloat16: ORTHO_BF16,
+                   torch.float8_e4m3fn: ORTHO_E4M3, torch.float8_e8m0fnu: ORTHO_E8M0}
+
+
+def _rows_of(t):
+    """(rows, cols, ld) of a tensor as a matrix: its first dimension by the others; a vector is
+    one row."""
+    shape = t.shape
+    if len(shape) < 2:
+        n = t.numel()
+        if n > 1 and t.stride(0) != 1:
+            raise ValueError("expected unit stride along columns")
+        return 1, n, max(n, 1)
+    rows, cols, step = shape[0], 1, 1
+    strides = t.stride()
+    for d in range(len(shape) - 1, 0, -1):
+        if shape[d] != 1 and strides[d] != step:
+            raise ValueError("expected unit stride along columns")
+        step *= shape[d]
+        cols *= shape[d]
+    if rows <= 1:
+        return rows, cols, max(cols, 1)
+    if strides[0] < cols:
+        raise ValueError("expected rows that do not overlap")
+    return rows, cols, strides[0]
+
+
+def mats(tensors: Sequence) -> MatList:
+    """Descriptors of tensors of any shape on one GPU: the first dimension is a matrix's rows, the
+    others its columns, which lie without gaps; a vector is one row; None stands for no matrix.  The
+    calls over many tensors take a list of tensors, or what this returns, which a program may keep
+    for the lists that stay (weights, states).  It holds the tensors; their shapes, types and strides
+    stay as they are."""
+    return MatList(tensors)
+
+
+def _as_mats(tensors) -> MatList:
+    return tensors if isinstance(tensors, MatList) else MatList(tensors)
+
+
+def _scalar_ptr(t, dtype, like, what):
+    """Address of a tensor's one element."""
+    if t.dtype != dtype or t.numel() != 1:
+        raise ValueError(f"expected {what} as one {dtype}, got {t.numel()} of {t.dtype}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"expected {what} on {like.device}, got {t.device}")
+    return t.data_ptr()
+
+
+def _same_device(lists):
+    for other in lists[1:]:
+        if other.first.get_device() != lists[0].first.get_device():
+            raise ValueError(f"expected every tensor on {lists[0].first.device}, got {other.first.device}")
+        if len(other) != len(lists[0]):
+            raise ValueError(f"expected {len(lists[0])} tensors in each list, got {len(other)}")
+
+
+def grad_norm_workspace_size(count: int) -> int:
+    return int(lib().ortho_grad_norm_workspace_size(count))
+
+
+def grad_norm(G, max_norm: float = float("inf"), out=None, ws=None):
+    """The norm of all gradients together and the factor that clips it to max_norm (``grad_norm``
+    of ortho.h), as the two elements of a float32 tensor: ``out[1:]`` is ``adamw_step``'s factor."""
+    import torch
+    G = _as_mats(G)
+    first = G.first
+    if out is None:
+        out = torch.empty(2, dtype=torch.float32, device=first.device)
+    elif out.dtype != torch.float32 or out.numel() != 2 or not out.is_contiguous():
+        raise ValueError("expected out as two float32")
+    elif out.get_device() != first.get_device():
+        raise ValueError(f"expected out on {first.device}, got {out.device}")
+    if ws is None:
+        ws = workspace(grad_norm_workspace_size(len(G)), first.device)
+    _call("grad_norm", first, len(G), G.current(), max_norm, out.data_ptr(), *_check_ws(ws, first))
+    return out
+
+
+def adamw_states(X: Sequence, bits: int = 32):
+    """States of ``adamw_step`` for the tensors X, at the start: (M, V, SM, SV), lists of float32
+    zeros (bits 32; SM and SV are None), or of e4m3 codes of 0 with scales of 1 (bits 8)."""
+    import torch
+    if bits == 32:
+        return ([torch.zeros(x.shape, dtype=torch.float32, device=x.device) for x in X],
+                [torch.zeros(x.shape, dtype=torch.float32, device=x.device) for x in X], None, None)
+    if bits != 8:
+        raise ValueError(f"expected bits 8 or 32, got {bits}")
+    codes, scales = [], []
+    for x in X:
+        rows, cols = (1, x.numel()) if x.dim() < 2 else (x.shape[0], x[0].numel())
+        for _ in range(2):
+            codes.append(torch.zeros(x.shape, dtype=torch.uint8, device=x.device).view(torch.float8_e4m3fn))
+            scales.append(torch.ones(rows, _blocks(cols), dtype=torch.float32, device=x.device))
+    return codes[::2], codes[1::2], scales[::2], scales[1::2]
+
+
+def adamw_step(X, G, M, V, lr, step, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+               SM=None, SV=None, seed: Optional[int] = None, factor=None):
+    """One AdamW step in place on all tensors of the lists; see ``adamw_step`` in ortho.h.  M and V
+    are float32, or e4m3 codes with their scales in SM and SV (lists as long as X, None beside float32
+    states).  ``seed``: stochastic rounding of bf16 weights and of codes.
+    ``lr`` and ``step`` may be one-element tensors (float32, int64) on the GPU, read when the kernels
+    run; ``factor`` is one such float32 that multiplies the gradients, NaN to leave all as it was."""
+    import torch
+    lists = [_as_mats(t) for t in (X, G, M, V)]
+    if SM is not None:
+        lists.append(_as_mats(SM))
+    if SV is not None:
+        lists.append(_as_mats(SV))
+    _same_device(lists)
+    first = lists[0].first
+    h = OrthoAdamw(0.0, betas[0], betas[1], eps, weight_decay, 1, 0, 0, None, None, None)
+    if isinstance(lr, torch.Tensor):
+        h.lr_dev = _scalar_ptr(lr, torch.float32, first, "lr")
+    else:
+        h.lr = lr
+    if isinstance(step, torch.Tensor):
+        h.step_dev = _scalar_ptr(step, torch.int64, first, "step")
+    else:
+        h.step = step
+    if seed is not None:
+        h.stochastic, h.seed = 1, seed
+    if factor is not None:
+        h.factor = _scalar_ptr(factor, torch.float32, first, "factor")
+    x, g, m, v = (t.current() for t in lists[:4])
+    sm = lists[4].current() if SM is not None else None
+    sv = lists[-1].current() if SV is not None else None
+    _call("adamw_step", first, len(lists[0]), x, g, m, v, sm, sv, ctypes.byref(h))
+
+
+# ---------------------------------------------------------------------------
+# Tokens by expert
+# ---------------------------------------------------------------------------
+
+
+def _int32s(t, count, like, what):
+    """Address of an int32 array of `count` elements on like's device."""
+    import torch
+    if t.dtype != torch.int32 or t.numel() != count or not t.is_contiguous():
+        raise ValueError(f"expected {what} as {count} consecutive int32")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"expected {what} on {like.device}, got {t.device}")
+    return t.data_ptr()
+
+
+def expert_rows(tokens: int, choices: int, experts: int, align: int = 1) -> int:
+    """Rows that tokens x choices pairs take at most when sorted by expert."""
+    return int(lib().ortho_expert_rows(tokens, choices, experts, align))
+
+
+def expert_sort_workspace_size(tokens: int, choices: int, experts: int) -> int:
+    return int(lib().ortho_expert_sort_workspace_size(tokens, choices, experts))
+
+
+def expert_sort(chosen, experts: int, align: int = 1, slot=None, source=None, offsets=None, counts=None,
+                ws=None):
+    """Rows by expert for the experts that each token chose (tokens x choices, int32 or int64); see
+    ``expert_sort`` in ortho.h.  Returns (slot, source, offsets, counts), allocated where None."""
+    import torch
+    if chosen.dim() != 2 or not chosen.is_contiguous() or chosen.dtype not in (torch.int32, torch.int64):
+        raise ValueError("expected chosen as a contiguous tokens x choices tensor of int32 or int64")
+    if chosen.get_device() < 0:
+        raise ValueError(f"expected tensors on a GPU, got {chosen.device}")
+    tokens, choices = chosen.shape
+    rows = expert_rows(tokens, choices, experts, align)
+
+    def ints(*shape):
+        return torch.empty(shape, dtype=torch.int32, device=chosen.device)
+
+    slot = ints(tokens, choices) if slot is None else slot
+    source = ints(rows) if source is None else source
+    offsets = ints(max(experts, 0) + 1) if offsets is None else offsets
+    counts = ints(max(experts, 0)) if counts is None else counts
+    if ws is None:
+        ws = workspace(expert_sort_workspace_size(tokens, choices, experts), chosen.device)
+    args = (_int32s(slot, tokens * choices, chosen, "slot"), _int32s(source, rows, chosen, "source"),
+            _int32s(offsets, experts + 1, chosen, "offsets"), _int32s(counts, experts, chosen, "counts"))
+    _call("expert_sort", chosen, chosen.data_ptr(), chosen.element_size(), tokens, choices, experts, align,
+          *args, *_check_ws(ws, chosen))
+    return slot, source, offsets, counts
+
+
+def _slots(slot, tokens, like):
+    if slot.dim() != 2 or slot.shape[0] != tokens:
+        raise ValueError(f"expected slot with {tokens} rows")
+    return _int32s(slot, slot.numel(), like, "slot"), slot.shape[1]
+
+
+def _experts(offsets, counts, like):
+    experts = counts.numel()
+    return (_int32s(offsets, experts + 1, like, "offsets"), _int32s(counts, experts, like, "counts"),
+            experts)
+
+
+def expert_gather(X, slot, offsets, counts, Y=None, S=None, SY=None, rows: Optional[int] = None):
+    """X's rows to the rows that ``expert_sort`` gave them; see ``expert_gather`` in ortho.h.  X are
+    bf16, float32, or e4m3 codes with scales S.  Without Y, Y (and SY) of `rows` rows are allocated.
+    Returns (Y, SY)."""
+    import torch
+    if Y is None:
+        if rows is None:
+            raise ValueError("expected Y, or the number of its rows")
+        if S is None:
+            Y = torch.empty(rows, X.size(1), dtype=X.dtype, device=X.device)
+        else:
+            Y = fp8_codes(rows, X.size(1), X.device)
+    if S is not None and SY is None:
+        SY = torch.empty(Y.size(0), S.size(1), dtype=S.dtype, device=X.device)
+    x, s, y, sy = _mats(X, S, Y, SY)
+    at, choices = _slots(slot, x.rows, X)
+    _call("expert_gather", X, x, _ref(s), at, choices, *_experts(offsets, counts, X), y, _ref(sy))
+    return Y, SY
+
+
+def expert_combine(Y, slot, weights=None, add=None, out=None):
+    """Rows back to tokens, each token's added with its weights (tokens x choices; ones when None)
+    and `add` added; see ``expert_combine`` in ortho.h.  Returns out."""
+    import torch
+    if out is None:
+        out = torch.empty(slot.shape[0], Y.size(1), dtype=Y.dtype, device=Y.device)
+    y, w, ad, o = _mats(Y, weights, add, out)
+    at, choices = _slots(slot, o.rows, Y)
+    _call("expert_combine", Y, y, at, choices, _ref(w), _ref(ad), o)
+    return out
+
+
+def expert_combine_backward(dOut, slot, weights, offsets, counts, dY=None, Y=None, dW=None,
+                            rows: Optional[int] = None):
+    """Gradient of ``expert_combine``; see ortho.h.  Without dY it is allocated, with Y's rows or
+    `rows`.  With Y the weights' gradient is formed too.  Returns (dY, dW), dW None without Y."""
+    import torch
+    if dY is None:
+        if rows is None and Y is None:
+            raise ValueError("expected dY, Y or the number of rows")
+        dY = torch.empty(Y.size(0) if rows is None else rows, dOut.size(1), dtype=dOut.dtype, device=dOut.device)
+    if Y is not None and dW is None:
+        dW = torch.empty(slot.shape, dtype=torch.float32, device=dOut.device)
+    d, w, dy, y, dw = _mats(dOut, weights, dY, Y, dW)
+    at, choices = _slots(slot, d.rows, dOut)
+    _call("expert_combine_backward", dOut, d, at, choices, _ref(w), *_experts(offsets, counts, dOut), dy,
+          _ref(y), _ref(dw))
+    return dY, dW

@@ -21,8 +21,8 @@ LIB = os.path.join(HERE, "libortho.so")
 
 SOURCES = ["kernels_gemm.hip", "kernels_aux.hip", "kernels_stream.hip", "kernels_gram_ns.hip",
            "kernels_sweep.hip", "kernels_dion2.hip", "kernels_fp8_gemm.hip", "kernels_fp8_exact.hip",
-           "kernels_fp8_few.hip", "kernels_fp8_rows.hip",
-           "noalloc.hip", "abi.cpp", "abi_fp8.cpp", "plan.cpp"]
+           "kernels_fp8_few.hip", "kernels_fp8_rows.hip", "kernels_adamw.hip", "kernels_experts.hip",
+           "noalloc.hip", "abi.cpp", "abi_fp8.cpp", "abi_adamw.cpp", "abi_experts.cpp", "plan.cpp"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",

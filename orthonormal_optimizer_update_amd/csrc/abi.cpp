@@ -876,7 +876,7 @@ const char* ortho_status_str(int32_t status) {
     case ORTHO_E_RANK: return "rank r outside [1, min(m, n)] or different from Q.cols";
     case ORTHO_E_LAYOUT: return "leading dimension smaller than cols or too large, differs within a group, or operands overlap";
     case ORTHO_E_WORKSPACE: return "workspace missing, too small or not 256-byte aligned";
-    case ORTHO_E_PARAM: return "invalid scalar parameter (mu, lr, scale, abc, steps, batch, eps or block_rows)";
+    case ORTHO_E_PARAM: return "invalid scalar parameter (mu, lr, scale, abc, steps, batch, eps, block_rows or one that the call states)";
     case ORTHO_E_HIP: return "a HIP launch failed";
     case ORTHO_E_SCRATCH:
       return "the problem needs more scratch memory than the no-allocation entry point holds";

@@ -1,0 +1,429 @@
+// Tokens to rows by expert, and back.
+#include <type_traits>
+
+#include "experts.h"
+#include "fp8.h"
+
+namespace ortho {
+
+namespace {
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ---- the sort ----
+//
+// A stable counting sort.  Counts of each tile's experts meet in memory; then each
+// workgroup adds what it needs of them itself (32 tiles of 128 experts are 16 KB
+// from L2, less than another launch takes), and its 16 waves place their pairs, 64 at
+// a time, in order.  One tile needs no other's counts and no first launch.
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kExperts = 1024;
+
+__device__ __forceinline__ int expert_of(const ExpertSortArgs& a, int pair) {
+  if (pair >= a.pairs) return -1;
+  const int64_t e = a.wide ? static_cast<const int64_t*>(a.chosen)[pair]
+                           : static_cast<int64_t>(static_cast<const int32_t*>(a.chosen)[pair]);
+  return e >= 0 && e < a.experts ? static_cast<int>(e) : -1;
+}
+
+__global__ __launch_bounds__(kSortThreads) void expert_count_kernel(ExpertSortArgs a) {
+  __shared__ int32_t count[kExperts];
+  for (int e = threadIdx.x; e < a.experts; e += kSortThreads) count[e] = 0;
+  __syncthreads();
+  const int first = blockIdx.x * a.tile;
+  for (int i = threadIdx.x; i < a.tile; i += kSortThreads) {
+    const int e = expert_of(a, first + i);
+    if (e >= 0) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += kSortThreads) a.part[(int64_t)blockIdx.x * a.experts + e] = count[e];
+}
+
+// Lanes of the wave with this lane's expert, by one ballot per bit of its number
+// (bit `bits` is set for pairs without one).
+__device__ __forceinline__ uint64_t same_lanes(int expert, int bits) {
+  uint64_t same = ~uint64_t{0};
+  for (int b = 0; b <= bits; ++b) {
+    const bool set = expert >> b & 1;
+    const uint64_t with = __ballot(set);
+    same &= set ? with : ~with;
+  }
+  return same;
+}
+
+__global__ __launch_bounds__(kSortThreads) void expert_place_kernel(ExpertSortArgs a) {
+  __shared__ int32_t place[kSortWaves][kExperts];   // counts, then next rows, of each wave
+  __shared__ int32_t begin[kExperts + 1], total[kExperts];
+  __shared__ int32_t sums[kSortWaves];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int each = a.tile / kSortWaves, first = blockIdx.x * a.tile + wave * each;
+  for (int e = lane; e < a.experts; e += 64) place[wave][e] = 0;
+  __syncthreads();
+  for (int i = lane; i < each; i += 64) {
+    const int e = expert_of(a, first + i);
+    if (e >= 0) atomicAdd(&place[wave][e], 1);
+  }
+  __syncthreads();
+  // Expert t: all tiles' count, and that of the tiles before this one.
+  int all = 0, before = 0;
+  if (t < a.experts) {
+    if (a.tiles == 1) {
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) all += place[w][t];
+    } else {
+      const int32_t* const p = a.part + t;
+#pragma unroll 8
+      for (int i = 0; i < a.tiles; ++i) {
+        const int c = p[(int64_t)i * a.experts];
+        all += c;
+        before += i < static_cast<int>(blockIdx.x) ? c : 0;
+      }
+    }
+  }
+  // Where expert t begins: the padded counts before it.
+  const int padded = (all + a.align - 1) / a.align * a.align;
+  int up = padded;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(up, o, 64);
+    up += lane >= o ? v : 0;
+  }
+  if (lane == 63) sums[wave] = up;
+  __syncthreads();
+  int start = up - padded;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) start += w < wave ? sums[w] : 0;
+  if (t < a.experts) {
+    begin[t] = start;
+    total[t] = all;
+    if (t == a.experts - 1) begin[a.experts] = start + padded;
+    int at = start + before;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int c = place[w][t];
+      place[w][t] = at;
+      at += c;
+    }
+    if (blockIdx.x == 0) {
+      a.offsets[t] = start;
+      a.counts[t] = all;
+      if (t == a.experts - 1) a.offsets[a.experts] = start + padded;
+    }
+  }
+  __syncthreads();
+  int bits = 1;
+  while (1 << bits < a.experts) ++bits;
+  for (int i = lane; i < each && first + (i & ~63) < a.pairs; i += 64) {
+    const int pair = first + i, e = expert_of(a, pair);
+    const uint64_t same = same_lanes(e < 0 ? 1 << bits : e, bits);
+    const int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
+    const int base = e >= 0 ? place[wave][e] : 0;
+    // (the wave's own row of LDS, whose accesses keep their order)
+    __builtin_amdgcn_wave_barrier();
+    if (e >= 0 && rank == 0) place[wave][e] = base + __popcll(same);
+    __builtin_amdgcn_wave_barrier();
+    if (pair < a.pairs) {
+      a.slot[pair] = e >= 0 ? base + rank : -1;
+      if (a.source && e >= 0) a.source[base + rank] = pair;
+    }
+  }
+  if (a.source == nullptr) return;
+  // Rows without a pair: each expert's padding, and what lies behind the last.
+  for (int e = blockIdx.x * kSortWaves + wave; e < a.experts; e += gridDim.x * kSortWaves)
+    for (int r = begin[e] + total[e] + lane; r < begin[e + 1]; r += 64) a.source[r] = -1;
+  for (int64_t r = (int64_t)begin[a.experts] + blockIdx.x * kSortThreads + t; r < a.rows;
+       r += gridDim.x * kSortThreads)
+    a.source[r] = -1;
+}
+
+// ---- rows as bytes ----
+
+// 16 bytes of a row of at least 16, from byte 16 p on; a piece that the row's end
+// cuts starts earlier, so that it lies inside (its bytes are the same either way).
+__device__ __forceinline__ int64_t piece_at(int64_t p, int64_t bytes) {
+  return p * 16 + 16 <= bytes ? p * 16 : bytes - 16;
+}
+
+__device__ __forceinline__ void copy_piece(uint8_t* dst, const uint4& u, int64_t p, int64_t bytes) {
+  if (bytes >= 16) {
+    __builtin_memcpy(dst + piece_at(p, bytes), &u, 16);
+    return;
+  }
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (j < bytes) dst[j] = static_cast<uint8_t>(w[j >> 2] >> 8 * (j & 3));
+}
+
+__device__ __forceinline__ uint4 load_piece(const uint8_t* src, int64_t p, int64_t bytes) {
+  uint4 u;
+  if (bytes >= 16) {
+    __builtin_memcpy(&u, src + piece_at(p, bytes), 16);
+    return u;
+  }
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (j < bytes) w[j >> 2] |= static_cast<uint32_t>(src[j]) << 8 * (j & 3);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Zeros in the rows of padding of expert e's part `part` of `parts`, `pieces` of
+// `bytes` each.
+__device__ __forceinline__ void clear_padding(const ExpertRowsArgs& r, int e, int part, int parts, uint8_t* y,
+                                              int64_t pitch, int64_t bytes, uint8_t* s, int64_t pitch_s, int blocks,
+                                              int scale_bytes) {
+  const int64_t from = max(0, r.offsets[e]) + static_cast<int64_t>(max(0, r.counts[e]));
+  const int64_t to = min(static_cast<int64_t>(r.offsets[e + 1]), r.rows);
+  const int64_t pieces = (bytes + 15) >> 4;
+  for (int64_t row = from + part; row < to; row += parts) {
+    for (int64_t p = threadIdx.x; p < pieces; p += 256) copy_piece(y + row * pitch, make_uint4(0, 0, 0, 0), p, bytes);
+    if (s)
+      for (int i = threadIdx.x; i < blocks; i += 256) {
+        if (scale_bytes == 4) reinterpret_cast<float*>(s + row * pitch_s)[i] = 1.f;
+        else s[row * pitch_s + i] = 127;
+      }
+  }
+}
+
+constexpr int kPadParts = 4;   // workgroups per expert's padding
+
+// The row of a pair, or -1.
+__device__ __forceinline__ int64_t row_of(const ExpertRowsArgs& r, int64_t pair) {
+  const int s = r.slot[pair];
+  return s >= 0 && s < r.rows ? s : -1;
+}
+
+// A token's row is read once and written `choices` times.  A workgroup's unit is
+// 256 >> lanes tokens by 1 << lanes pieces of 16 bytes.
+__global__ __launch_bounds__(256) void expert_gather_kernel(ExpertGatherArgs a, int lanes, int across, int64_t units) {
+  if (blockIdx.x >= gridDim.x - a.r.experts * kPadParts) {
+    const int at = blockIdx.x - (gridDim.x - a.r.experts * kPadParts);
+    clear_padding(a.r, at / kPadParts, at % kPadParts, kPadParts, a.y, a.pitch_y, a.bytes, a.sy, a.pitch_sy, a.blocks,
+                  a.scale_bytes);
+    return;
+  }
+  const int64_t pieces = (a.bytes + 15) >> 4;
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x - a.r.experts * kPadParts) {
+    const int64_t down = unit / across;
+    const int col = static_cast<int>(unit - down * across);
+    const int64_t token = (down << (8 - lanes)) + (threadIdx.x >> lanes);
+    const int64_t p = ((int64_t)col << lanes) + (threadIdx.x & ((1 << lanes) - 1));
+    if (token >= a.r.tokens) continue;
+    const int64_t pair = token * a.r.choices;
+    if (p < pieces) {
+      const uint4 u = load_piece(a.x + token * a.pitch_x, p, a.bytes);
+#pragma unroll 4
+      for (int j = 0; j < a.r.choices; ++j) {
+        const int64_t row = row_of(a.r, pair + j);
+        if (row >= 0) copy_piece(a.y + row * a.pitch_y, u, p, a.bytes);
+      }
+    }
+    if (a.s == nullptr) continue;
+    // the scales of the pieces at hand: one for each 8 pieces
+    if ((p & 7) != 0 || p >> 3 >= a.blocks) continue;
+    const uint8_t* const src = a.s + token * a.pitch_s;
+    const int64_t b = p >> 3;
+    const float f = a.scale_bytes == 4 ? reinterpret_cast<const float*>(src)[b] : 0.f;
+    const uint8_t e = a.scale_bytes == 4 ? 0 : src[b];
+#pragma unroll 4
+    for (int j = 0; j < a.r.choices; ++j) {
+      const int64_t row = row_of(a.r, pair + j);
+      if (row < 0) continue;
+      if (a.scale_bytes == 4) reinterpret_cast<float*>(a.sy + row * a.pitch_sy)[b] = f;
+      else a.sy[row * a.pitch_sy + b] = e;
+    }
+  }
+}
+
+// ---- back to tokens ----
+
+__device__ __forceinline__ float weight_of(const void* w, int w_bf, int64_t at) {
+  if (w == nullptr) return 1.f;
+  return w_bf ? bf16_bits_to_f32(static_cast<const uint16_t*>(w)[at]) : static_cast<const float*>(w)[at];
+}
+
+// kAtOnce choices' loads are under way together.
+template <typename T, int kAtOnce>
+__global__ __launch_bounds__(256) void expert_combine_kernel(ExpertCombineArgs a, int lanes, int across,
+                                                             int64_t units) {
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int64_t down = unit / across;
+    const int col = static_cast<int>(unit - down * across);
+    const int64_t token = (down << (8 - lanes)) + (threadIdx.x >> lanes);
+    const int c = ((col << lanes) + (threadIdx.x & ((1 << lanes) - 1))) * 8;
+    if (token >= a.r.tokens || c >= a.n) continue;
+    float sum[8] = {};
+    for (int j0 = 0; j0 < a.r.choices; j0 += kAtOnce) {
+      Raw8<T> y[kAtOnce];
+      float w[kAtOnce];
+      bool has[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int at = min(j0 + j, a.r.choices - 1);
+        const int64_t row = row_of(a.r, token * a.r.choices + at);
+        has[j] = row >= 0 && j0 + j < a.r.choices;
+        w[j] = weight_of(a.w, a.w_bf, token * a.ldw + at);
+        // (row 0 for pairs without one: no load depends on a branch)
+        y[j] = load_raw8(static_cast<const T*>(a.y) + max(row, (int64_t)0) * a.ldy, c, a.n);
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        float v[8];
+        unpack8(y[j], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = has[j] ? fmaf(w[j], v[e], sum[e]) : sum[e];
+      }
+    }
+    if (a.add) {
+      float v[8];
+      if (a.add_bf) load8(static_cast<const uint16_t*>(a.add) + token * a.ldadd, c, a.n, v);
+      else load8(static_cast<const float*>(a.add) + token * a.ldadd, c, a.n, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += v[e];
+    }
+    store8(static_cast<T*>(a.out) + token * a.ldout, c, a.n, sum);
+  }
+}
+
+// kThreads threads per token, kAtOnce choices at a time: their rows of Y are read, the
+// products with dOut summed, and their rows of dY written.
+template <typename T, int kThreads, int kAtOnce>
+__global__ __launch_bounds__(256) void expert_combine_grad_kernel(ExpertCombineGradArgs a, int64_t groups) {
+  __shared__ float red[2][4][kAtOnce];
+  if (blockIdx.x >= gridDim.x - a.r.experts * kPadParts) {
+    const int at = blockIdx.x - (gridDim.x - a.r.experts * kPadParts);
+    clear_padding(a.r, at / kPadParts, at % kPadParts, kPadParts, static_cast<uint8_t*>(a.dy), a.lddy * sizeof(T),
+                  (int64_t)a.n * sizeof(T), nullptr, 0, 0, 0);
+    return;
+  }
+  constexpr int kTokens = 256 / kThreads;
+  const int t = threadIdx.x % kThreads;
+  int turn = 0;
+  for (int64_t group = blockIdx.x; group < groups; group += gridDim.x - a.r.experts * kPadParts) {
+    const int64_t token = group * kTokens + threadIdx.x / kThreads;
+    if (token >= a.r.tokens) continue;   // (whole waves; with 256 threads the workgroup)
+    for (int j0 = 0; j0 < a.r.choices; j0 += kAtOnce) {
+      int64_t row[kAtOnce];
+      float w[kAtOnce], dot[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int at = min(j0 + j, a.r.choices - 1);
+        row[j] = j0 + j < a.r.choices ? row_of(a.r, token * a.r.choices + at) : -1;
+        w[j] = weight_of(a.w, a.w_bf, token * a.ldw + at);
+        dot[j] = 0.f;
+      }
+      for (int c = t * 8; c < a.n; c += kThreads * 8) {
+        const Raw8<T> rd = load_raw8(static_cast<const T*>(a.dout) + token * a.lddout, c, a.n);
+        float d[8];
+        if (a.y) {
+          Raw8<T> y[kAtOnce];
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j)
+            y[j] = load_raw8(static_cast<const T*>(a.y) + max(row[j], (int64_t)0) * a.ldy, c, a.n);
+          unpack8(rd, d);
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+            float v[8];
+            unpack8(y[j], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot[j] = fmaf(d[e], v[e], dot[j]);
+          }
+        } else {
+          unpack8(rd, d);
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          if (row[j] < 0) continue;
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = w[j] * d[e];
+          store8(static_cast<T*>(a.dy) + row[j] * a.lddy, c, a.n, v);
+        }
+      }
+      if (a.y == nullptr) continue;
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) {
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) dot[j] += __shfl_xor(dot[j], o, 64);
+      }
+      if constexpr (kThreads > 64) {
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) red[turn][threadIdx.x >> 6][j] = dot[j];
+        }
+        __syncthreads();
+        if (t < kAtOnce && j0 + t < a.r.choices) {
+          const float sum = red[turn][0][t] + red[turn][1][t] + red[turn][2][t] + red[turn][3][t];
+          a.dw[token * a.lddw + j0 + t] = row_of(a.r, token * a.r.choices + j0 + t) >= 0 ? sum : 0.f;
+        }
+        turn ^= 1;   // the next sums go to the other buffer: one barrier between uses
+      } else if (t == 0) {
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+          if (j0 + j < a.r.choices) a.dw[token * a.lddw + j0 + j] = row[j] >= 0 ? dot[j] : 0.f;
+      }
+    }
+  }
+}
+
+constexpr int64_t kMostGroups = 1 << 20;   // workgroups of a launch; more units are walked
+
+}  // namespace
+
+hipError_t launch_expert_sort(const ExpertSortArgs& a, hipStream_t s) {
+  if (a.tiles > 1) {
+    hipLaunchKernelGGL(expert_count_kernel, dim3(a.tiles), dim3(kSortThreads), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(expert_place_kernel, dim3(a.tiles), dim3(kSortThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_gather(const ExpertGatherArgs& a, int lanes, int64_t across, int64_t units, hipStream_t s) {
+  const int64_t groups = units < kMostGroups ? units : kMostGroups;
+  const dim3 grid(static_cast<uint32_t>(groups + a.r.experts * kPadParts));
+  hipLaunchKernelGGL(expert_gather_kernel, grid, dim3(256), 0, s, a, lanes, static_cast<int>(across), units);
+  return hipGetLastError();
+}
+
+// f(choices at once): the least power of two that holds them, at most eight.
+template <class F>
+hipError_t by_choices(int choices, F f) {
+  if (choices <= 1) f(std::integral_constant<int, 1>{});
+  else if (choices <= 2) f(std::integral_constant<int, 2>{});
+  else if (choices <= 4) f(std::integral_constant<int, 4>{});
+  else f(std::integral_constant<int, 8>{});
+  return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t combine(const ExpertCombineArgs& a, int lanes, int64_t across, int64_t units, hipStream_t s) {
+  const dim3 grid(static_cast<uint32_t>(units < kMostGroups ? units : kMostGroups));
+  return by_choices(a.r.choices, [&](auto k) {
+    hipLaunchKernelGGL((expert_combine_kernel<T, decltype(k)::value>), grid, dim3(256), 0, s, a, lanes,
+                       static_cast<int>(across), units);
+  });
+}
+
+template <typename T, int kThreads>
+static hipError_t combine_grad(const ExpertCombineGradArgs& a, hipStream_t s) {
+  const int64_t units = cdiv(a.r.tokens, 256 / kThreads);
+  const dim3 grid(static_cast<uint32_t>((units < kMostGroups ? units : kMostGroups) + a.r.experts * kPadParts));
+  return by_choices(a.r.choices, [&](auto k) {
+    hipLaunchKernelGGL((expert_combine_grad_kernel<T, kThreads, decltype(k)::value>), grid, dim3(256), 0, s, a, units);
+  });
+}
+
+hipError_t launch_expert_combine(const ExpertCombineArgs& a, bool bf, int lanes, int64_t across, int64_t units,
+                                 hipStream_t s) {
+  return bf ? combine<uint16_t>(a, lanes, across, units, s) : combine<float>(a, lanes, across, units, s);
+}
+
+hipError_t launch_expert_combine_grad(const ExpertCombineGradArgs& a, bool bf, hipStream_t s) {
+  // a wave per token up to 1024 columns, else a workgroup
+  if (a.n <= 1024) return bf ? combine_grad<uint16_t, 64>(a, s) : combine_grad<float, 64>(a, s);
+  return bf ? combine_grad<uint16_t, 256>(a, s) : combine_grad<float, 256>(a, s);
+}
+
+}  // namespace ortho

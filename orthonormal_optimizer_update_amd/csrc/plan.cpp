@@ -3,6 +3,10 @@
 
 #include <math.h>
 
+#include <float.h>
+#include <stdlib.h>
+
+#include <algorithm>
 #include <initializer_list>
 #include <numeric>
 
@@ -621,6 +625,266 @@ ortho_status validate_fp8_matmul(const ortho_mat& A, const ortho_mat& SA, const 
   Fp8MatmulPlan plan;
   if (!plan_fp8_matmul(A.rows, B.rows, A.cols, &plan)) return ORTHO_E_SHAPE;
   return check_ws(ws, ws_bytes, plan.total_bytes);
+}
+
+namespace {
+
+// The bytes from a matrix's first to its last element.
+struct Extent {
+  uintptr_t begin;
+  __int128 size;
+  const ortho_mat* a;
+  bool written;
+};
+
+Extent extent(const ortho_mat& a, bool written) {
+  const int64_t e = element_size(a), pitch = a.rows > 1 ? a.ld * e : 0;
+  return {reinterpret_cast<uintptr_t>(a.data), static_cast<__int128>(a.rows - 1) * pitch + a.cols * e, &a, written};
+}
+
+// Whether of `count` matrices every written one is apart from all others.  Sorted by
+// address, a matrix can only meet those that begin before the furthest end so far.
+bool all_apart(Extent* x, size_t count) {
+  const auto before = [](const Extent& a, const Extent& b) { return a.begin < b.begin; };
+  if (!std::is_sorted(x, x + count, before)) std::sort(x, x + count, before);
+  size_t open = 0;   // the first that may reach as far as the one at hand
+  __int128 reach = 0;   // the furthest end of x[open ..]
+  for (size_t i = 0; i < count; ++i) {
+    if (i == open || reach <= static_cast<__int128>(x[i].begin)) {
+      open = i;
+      reach = x[i].begin + x[i].size;
+      continue;
+    }
+    for (size_t j = open; j < i; ++j)
+      if ((x[i].written || x[j].written) && !apart(*x[i].a, *x[j].a)) return false;
+    reach = std::max(reach, x[i].begin + x[i].size);
+  }
+  return true;
+}
+
+// An array of `count` elements of `bytes` as a matrix of one row of bytes.
+ortho_mat array_of(const void* p, int64_t count, int64_t bytes) {
+  return {const_cast<void*>(p), 1, count * bytes, count * bytes, ORTHO_E4M3};
+}
+
+bool small_enough(const ortho_mat& a) { return a.rows <= kMaxElements / a.cols; }
+
+}  // namespace
+
+size_t grad_norm_ws_bytes(int32_t count) {
+  if (count < 1) return 0;
+  return align_up(static_cast<size_t>(cdiv(count, kNormPerLaunch)) * kNormGroups * sizeof(double));
+}
+
+ortho_status validate_grad_norm(int32_t count, const ortho_mat* G, double max_norm, const float* out,
+                                const void* ws, size_t ws_bytes) {
+  if (count < 1 || !(max_norm > 0.0)) return ORTHO_E_PARAM;
+  if (G == nullptr || out == nullptr) return ORTHO_E_NULL;
+  const ortho_mat o = array_of(out, 2, 4);
+  for (int32_t i = 0; i < count; ++i) {
+    const ortho_status st = check_any(G[i], kReal);
+    if (st != ORTHO_OK) return st;
+    if (!small_enough(G[i])) return ORTHO_E_SHAPE;
+    if (!apart(G[i], o)) return ORTHO_E_LAYOUT;
+  }
+  return check_ws(ws, ws_bytes, grad_norm_ws_bytes(count));
+}
+
+ortho_status validate_adamw(int32_t count, const ortho_mat* X, const ortho_mat* G, const ortho_mat* M,
+                            const ortho_mat* V, const ortho_mat* SM, const ortho_mat* SV,
+                            const ortho_adamw* h) {
+  if (count < 1) return ORTHO_E_PARAM;
+  if (X == nullptr || G == nullptr || M == nullptr || V == nullptr || h == nullptr) return ORTHO_E_NULL;
+  const float eps = static_cast<float>(h->eps);
+  if (!finite(static_cast<float>(h->lr)) || !finite(static_cast<float>(h->weight_decay)) ||
+      !(h->weight_decay >= 0.0) || !(h->beta1 >= 0.0 && h->beta1 < 1.0) ||
+      !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !finite(eps) || !(eps >= FLT_MIN) ||
+      (h->step < 1 && h->step_dev == nullptr))
+    return ORTHO_E_PARAM;
+  size_t codes = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    ortho_status st;
+    if ((st = check_any(X[i], kReal)) != ORTHO_OK) return st;
+    if ((st = check_any(G[i], kReal)) != ORTHO_OK) return st;
+    if ((st = check_any(M[i], 1u << ORTHO_F32 | kCodes)) != ORTHO_OK) return st;
+    if ((st = check_any(V[i], 1u << M[i].dtype)) != ORTHO_OK) return st;
+    for (const ortho_mat* t : {&G[i], &M[i], &V[i]})
+      if (!shape_is(*t, X[i].rows, X[i].cols)) return ORTHO_E_SHAPE;
+    if (!small_enough(X[i])) return ORTHO_E_SHAPE;
+    if (M[i].dtype != ORTHO_E4M3) continue;
+    ++codes;
+    if (SM == nullptr || SV == nullptr) return ORTHO_E_NULL;
+    for (const ortho_mat* t : {&SM[i], &SV[i]})
+      if ((st = check_like(t, ORTHO_F32, X[i].rows, cdiv(X[i].cols, kFp8BlockSize))) != ORTHO_OK) return st;
+  }
+  Extent few[64], *all = few;
+  const size_t most = 4 * static_cast<size_t>(count) + 2 * codes;
+  if (most > sizeof(few) / sizeof(few[0])) {
+    all = static_cast<Extent*>(malloc(most * sizeof(Extent)));
+    if (all == nullptr) return ORTHO_E_WORKSPACE;
+  }
+  size_t n = 0;
+  for (int32_t i = 0; i < count; ++i) all[n++] = extent(X[i], true);
+  for (int32_t i = 0; i < count; ++i) all[n++] = extent(G[i], false);
+  for (int32_t i = 0; i < count; ++i) all[n++] = extent(M[i], true);
+  for (int32_t i = 0; i < count; ++i) all[n++] = extent(V[i], true);
+  for (int32_t i = 0; i < count; ++i) {
+    if (M[i].dtype != ORTHO_E4M3) continue;
+    all[n++] = extent(SM[i], true);
+    all[n++] = extent(SV[i], true);
+  }
+  const bool ok = all_apart(all, n);
+  if (all != few) free(all);
+  return ok ? ORTHO_OK : ORTHO_E_LAYOUT;
+}
+
+Deal deal(int64_t rows, int64_t cols, int64_t piece) {
+  // The widest that pads rows by at most an eighth more than the narrowest does.
+  Deal best{};
+  int64_t least = 0;
+  for (int lanes = 4; lanes <= 8; ++lanes) {
+    const int64_t wide = piece << lanes, across = cdiv(cols, wide);
+    if (lanes == 4) least = across * wide;
+    if (across * wide > least + least / 8) continue;
+    best = {lanes, across, across * cdiv(rows, 256 >> lanes)};
+  }
+  return best;
+}
+
+int64_t expert_rows(int64_t tokens, int32_t choices, int32_t experts, int32_t align) {
+  if (tokens < 1 || choices < 1 || choices > kMaxChoices || experts < 1 || experts > kMaxExperts || align < 1 ||
+      align > kMaxAlign || tokens >= kMaxDim)
+    return 0;
+  const int64_t rows = tokens * choices + static_cast<int64_t>(experts) * (align - 1);
+  return rows < kMaxDim ? rows : 0;
+}
+
+bool plan_expert_sort(int64_t tokens, int32_t choices, int32_t experts, ExpertSortPlan* p) {
+  if (expert_rows(tokens, choices, experts, 1) == 0) return false;
+  p->pairs = tokens * choices;
+  // 4096 pairs per workgroup (256 per wave), more where that would be over 1024 tiles
+  const int64_t tile = std::max<int64_t>(4096, cdiv(cdiv(p->pairs, 1024), 1024) * 1024);
+  p->tile = static_cast<int>(tile);
+  p->tiles = static_cast<int>(cdiv(p->pairs, tile));
+  p->total_bytes = p->tiles == 1 ? kWsAlign : align_up(static_cast<size_t>(p->tiles) * experts * 4);
+  return true;
+}
+
+ortho_status validate_expert_sort(const void* chosen, int32_t chosen_bytes, int64_t tokens, int32_t choices,
+                                  int32_t experts, int32_t align, const int32_t* slot, const int32_t* source,
+                                  const int32_t* offsets, const int32_t* counts, const void* ws, size_t ws_bytes) {
+  if (chosen == nullptr || slot == nullptr || offsets == nullptr || counts == nullptr) return ORTHO_E_NULL;
+  if (chosen_bytes != 4 && chosen_bytes != 8) return ORTHO_E_DTYPE;
+  const int64_t rows = expert_rows(tokens, choices, experts, align);
+  ExpertSortPlan plan;
+  if (rows == 0 || !plan_expert_sort(tokens, choices, experts, &plan)) return ORTHO_E_SHAPE;
+  const ortho_mat in = array_of(chosen, plan.pairs, chosen_bytes);
+  const ortho_mat outs[] = {array_of(slot, plan.pairs, 4), array_of(offsets, experts + 1, 4),
+                            array_of(counts, experts, 4), array_of(source ? source : slot, source ? rows : 0, 4)};
+  for (int i = 0; i < (source ? 4 : 3); ++i) {
+    if (!apart(outs[i], in)) return ORTHO_E_LAYOUT;
+    for (int j = 0; j < i; ++j)
+      if (!apart(outs[i], outs[j])) return ORTHO_E_LAYOUT;
+  }
+  return check_ws(ws, ws_bytes, plan.total_bytes);
+}
+
+namespace {
+
+// What the calls on rows share: slot and, where padding is written, the experts' rows.
+ortho_status check_slots(int64_t tokens, const int32_t* slot, int32_t choices, int64_t rows) {
+  if (slot == nullptr) return ORTHO_E_NULL;
+  if (choices < 1 || choices > kMaxChoices || tokens * choices >= kMaxDim || rows >= kMaxDim) return ORTHO_E_SHAPE;
+  return ORTHO_OK;
+}
+
+ortho_status check_experts(const int32_t* offsets, const int32_t* counts, int32_t experts) {
+  if (offsets == nullptr || counts == nullptr) return ORTHO_E_NULL;
+  return experts < 1 || experts > kMaxExperts ? ORTHO_E_SHAPE : ORTHO_OK;
+}
+
+// An output against the integer arrays that a call reads.
+bool apart_from_slots(const ortho_mat& out, const int32_t* slot, int64_t pairs, const int32_t* offsets,
+                      const int32_t* counts, int32_t experts) {
+  return apart(out, array_of(slot, pairs, 4)) &&
+         (offsets == nullptr || (apart(out, array_of(offsets, experts + 1, 4)) &&
+                                 apart(out, array_of(counts, experts, 4))));
+}
+
+ortho_status check_weights(const ortho_mat* W, int64_t tokens, int32_t choices) {
+  if (W == nullptr) return ORTHO_OK;
+  const ortho_status st = check_any(*W, kReal);
+  if (st != ORTHO_OK) return st;
+  return shape_is(*W, tokens, choices) ? ORTHO_OK : ORTHO_E_SHAPE;
+}
+
+}  // namespace
+
+ortho_status validate_expert_gather(const ortho_mat& X, const ortho_mat* S, const int32_t* slot, int32_t choices,
+                                    const int32_t* offsets, const int32_t* counts, int32_t experts,
+                                    const ortho_mat& Y, const ortho_mat* SY) {
+  ortho_status st;
+  if ((st = check_any(X, kReal | kCodes)) != ORTHO_OK) return st;
+  if ((st = check_any(Y, 1u << X.dtype)) != ORTHO_OK) return st;
+  if (Y.cols != X.cols) return ORTHO_E_SHAPE;
+  if ((st = check_slots(X.rows, slot, choices, Y.rows)) != ORTHO_OK) return st;
+  if ((st = check_experts(offsets, counts, experts)) != ORTHO_OK) return st;
+  const bool codes = X.dtype == ORTHO_E4M3;
+  if (codes != (S != nullptr) || codes != (SY != nullptr)) return codes ? ORTHO_E_NULL : ORTHO_E_DTYPE;
+  const int64_t pairs = X.rows * choices;
+  if (codes) {
+    if ((st = check_codes(X, *S, X.rows, X.cols, 1)) != ORTHO_OK) return st;
+    if ((st = check_like(SY, S->dtype, Y.rows, S->cols)) != ORTHO_OK) return st;
+    if (!apart(*SY, X) || !apart(*SY, *S) || !apart(*SY, Y) || !apart(Y, *S) ||
+        !apart_from_slots(*SY, slot, pairs, offsets, counts, experts))
+      return ORTHO_E_LAYOUT;
+  }
+  if (!apart(Y, X) || !apart_from_slots(Y, slot, pairs, offsets, counts, experts)) return ORTHO_E_LAYOUT;
+  return ORTHO_OK;
+}
+
+ortho_status validate_expert_combine(const ortho_mat& Y, const int32_t* slot, int32_t choices, const ortho_mat* W,
+                                     const ortho_mat* Add, const ortho_mat& Out) {
+  ortho_status st;
+  if ((st = check_any(Y, kReal)) != ORTHO_OK) return st;
+  if ((st = check_any(Out, 1u << Y.dtype)) != ORTHO_OK) return st;
+  if (Out.cols != Y.cols) return ORTHO_E_SHAPE;
+  if ((st = check_slots(Out.rows, slot, choices, Y.rows)) != ORTHO_OK) return st;
+  if ((st = check_weights(W, Out.rows, choices)) != ORTHO_OK) return st;
+  if (Add) {
+    if ((st = check_any(*Add, kReal)) != ORTHO_OK) return st;
+    if (!shape_is(*Add, Out.rows, Out.cols)) return ORTHO_E_SHAPE;
+    if (!same_or_apart(&Out, Add)) return ORTHO_E_LAYOUT;
+  }
+  if (!apart(Out, Y) || (W && !apart(Out, *W)) ||
+      !apart_from_slots(Out, slot, Out.rows * choices, nullptr, nullptr, 0))
+    return ORTHO_E_LAYOUT;
+  return ORTHO_OK;
+}
+
+ortho_status validate_expert_combine_backward(const ortho_mat& dOut, const int32_t* slot, int32_t choices,
+                                              const ortho_mat* W, const int32_t* offsets, const int32_t* counts,
+                                              int32_t experts, const ortho_mat& dY, const ortho_mat* Y,
+                                              const ortho_mat* dW) {
+  ortho_status st;
+  if ((st = check_any(dOut, kReal)) != ORTHO_OK) return st;
+  if ((st = check_any(dY, 1u << dOut.dtype)) != ORTHO_OK) return st;
+  if (dY.cols != dOut.cols) return ORTHO_E_SHAPE;
+  if ((st = check_slots(dOut.rows, slot, choices, dY.rows)) != ORTHO_OK) return st;
+  if ((st = check_experts(offsets, counts, experts)) != ORTHO_OK) return st;
+  if ((st = check_weights(W, dOut.rows, choices)) != ORTHO_OK) return st;
+  if ((Y == nullptr) != (dW == nullptr)) return ORTHO_E_NULL;
+  const int64_t pairs = dOut.rows * choices;
+  if (Y) {
+    if ((st = check_like(Y, dOut.dtype, dY.rows, dY.cols)) != ORTHO_OK) return st;
+    if ((st = check_like(dW, ORTHO_F32, dOut.rows, choices)) != ORTHO_OK) return st;
+    if (!same_or_apart(&dY, Y) || !apart(*dW, *Y) || !apart(*dW, dY) || !apart(*dW, dOut) ||
+        (W && !apart(*dW, *W)) || !apart_from_slots(*dW, slot, pairs, offsets, counts, experts))
+      return ORTHO_E_LAYOUT;
+  }
+  if (!apart(dY, dOut) || (W && !apart(dY, *W)) || !apart_from_slots(dY, slot, pairs, offsets, counts, experts))
+    return ORTHO_E_LAYOUT;
+  return ORTHO_OK;
 }
 
 }  // namespace ortho

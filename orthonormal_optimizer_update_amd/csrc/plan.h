@@ -192,4 +192,47 @@ ortho_status validate_fp8_matmul(const ortho_mat& A, const ortho_mat& SA, const 
                                  const ortho_mat& SB, const ortho_mat& C, const ortho_mat* Add,
                                  const void* ws, size_t ws_bytes);
 
+// AdamW and the gradients' norm.
+constexpr int64_t kMaxElements = int64_t{1} << 40;   // of one tensor
+// Workgroups of one launch over gradients, each with an fp64 sum in the workspace.
+constexpr int kNormGroups = 1024;
+constexpr int kNormPerLaunch = 64;                   // must match NormParts::kMost
+size_t grad_norm_ws_bytes(int32_t count);
+ortho_status validate_grad_norm(int32_t count, const ortho_mat* G, double max_norm, const float* out,
+                                const void* ws, size_t ws_bytes);
+ortho_status validate_adamw(int32_t count, const ortho_mat* X, const ortho_mat* G, const ortho_mat* M,
+                            const ortho_mat* V, const ortho_mat* SM, const ortho_mat* SV,
+                            const ortho_adamw* h);
+
+// How a kernel deals a rows x cols matrix to workgroups of 256 threads: 1 << lanes
+// threads (16 to 256) side by side in a row, `piece` elements each.
+struct Deal {
+  int lanes;
+  int64_t across, units;     // units along the columns, and in all
+};
+Deal deal(int64_t rows, int64_t cols, int64_t piece);
+
+// Tokens by expert.  The pairs are cut into `tiles` of `tile` pairs, one workgroup
+// each; a tile's counts (one per expert) meet in the workspace.
+constexpr int kMaxExperts = 1024, kMaxChoices = 64, kMaxAlign = 4096;
+struct ExpertSortPlan {
+  int64_t pairs;
+  int tiles, tile;
+  size_t total_bytes;
+};
+bool plan_expert_sort(int64_t tokens, int32_t choices, int32_t experts, ExpertSortPlan* out);
+int64_t expert_rows(int64_t tokens, int32_t choices, int32_t experts, int32_t align);
+ortho_status validate_expert_sort(const void* chosen, int32_t chosen_bytes, int64_t tokens, int32_t choices,
+                                  int32_t experts, int32_t align, const int32_t* slot, const int32_t* source,
+                                  const int32_t* offsets, const int32_t* counts, const void* ws, size_t ws_bytes);
+ortho_status validate_expert_gather(const ortho_mat& X, const ortho_mat* S, const int32_t* slot, int32_t choices,
+                                    const int32_t* offsets, const int32_t* counts, int32_t experts,
+                                    const ortho_mat& Y, const ortho_mat* SY);
+ortho_status validate_expert_combine(const ortho_mat& Y, const int32_t* slot, int32_t choices, const ortho_mat* W,
+                                     const ortho_mat* Add, const ortho_mat& Out);
+ortho_status validate_expert_combine_backward(const ortho_mat& dOut, const int32_t* slot, int32_t choices,
+                                              const ortho_mat* W, const int32_t* offsets, const int32_t* counts,
+                                              int32_t experts, const ortho_mat& dY, const ortho_mat* Y,
+                                              const ortho_mat* dW);
+
 }  // namespace ortho
