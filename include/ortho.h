@@ -456,14 +456,16 @@ typedef struct {
  *          where no tensor has codes.
  * States start at zero (any finite scale beside codes of 0).  X, M, V, SM and SV
  * have memory of their own, apart from each other, from those of every other tensor
- * and from every G (else ORTHO_E_LAYOUT; rows between another matrix's rows are
- * apart): a weight that is listed twice is refused.
+ * and from every G (else ORTHO_E_LAYOUT; rows between another matrix's rows of the
+ * same pitch are apart): a weight that is listed twice is refused.  So is a leading
+ * dimension from 2^32 on.
  *
  * The step uses m and v as computed; only what is kept for the next one is rounded.
  * A block's scale is its largest finite |m| (or sqrt(v)) / 448, at least 2^-126, and
- * 1 for a block of zeros; infinite and NaN values get the NaN code.  A v above 0
- * never gets the code of 0 (the least code, 2^-9, in its place), so that no later
- * step divides by nothing but eps.
+ * 1 for a block of zeros; infinite and NaN values get the NaN code, but a v beyond
+ * fp32's range counts as its largest number.  A v above 0 never gets the code of 0
+ * (the least code, 2^-9, in its place), so that no later step divides by nothing but
+ * eps.
  *
  * Stochastic rounding of bf16 weights and of codes: with u random bits out of
  * 2^n, a value that lies a part p of the way from one number of the type to the

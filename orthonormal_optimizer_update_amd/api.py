@@ -10,6 +10,7 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import struct
 from typing import Optional, Sequence
@@ -523,47 +524,57 @@ def fp8_matmul(A, SA, B, SB, out=None, add=None, ws=None, out_dtype=None):
 class MatList:
     """Descriptors of a list of tensors, for calls over many of them; see ``mats``."""
 
-    __slots__ = ("tensors", "first", "array", "_pointers")
+    __slots__ = ("tensors", "first", "array", "_held", "_pointers")
 
     def __init__(self, tensors):
         self.tensors = tuple(tensors)
-        self.first = next((t for t in self.tensors if t is not None), None)
-        if self.first is None:
+        self._held = [t for t in self.tensors if t is not None]
+        if not self._held:
             raise ValueError("expected at least one tensor")
+        self.first = self._held[0]
         self._describe()
 
     def _describe(self):
+        import torch
         _mats_dtypes()
-        dtypes, device, fields, pointers = _DTYPES, self.first.get_device(), [], []
-        if device < 0:
+        T, held = torch.Tensor, self._held
+        devices = list(map(T.get_device, held))
+        if devices[0] < 0:
             raise ValueError(f"expected tensors on a GPU, got {self.first.device}")
-        for t in self.tensors:
-            if t is None:
-                pointers.append(0)
-                fields += (0, 0, 0, 0, 0)
-                continue
-            if t.get_device() != device:
-                raise ValueError(f"expected every tensor on {self.first.device}, got {t.device}")
-            dt = dtypes.get(t.dtype)
-            if dt is None:
-                raise ValueError(f"unsupported dtype {t.dtype}")
-            rows, cols, ld = _rows_of(t)
-            at = t.data_ptr()
-            pointers.append(at)
-            fields += (at, rows, cols, ld, dt)
-        count = len(pointers)
+        if devices.count(devices[0]) != len(devices):
+            other = next(t for t in held if t.get_device() != devices[0])
+            raise ValueError(f"expected every tensor on {self.first.device}, got {other.device}")
+        self._pointers = pointers = list(map(T.data_ptr, held))
+        # (a tensor often has the shape, strides and type of the one before)
+        fields, last_shape, last_stride, last_dtype, matrix = [], None, None, None, None
+        for at, shape, stride, dtype in zip(pointers, map(T.size, held), map(T.stride, held), map(_DTYPE, held)):
+            if dtype is not last_dtype or stride != last_stride or shape != last_shape:
+                code = _DTYPES.get(dtype)
+                if code is None:
+                    raise ValueError(f"unsupported dtype {dtype}")
+                matrix = (*_rows_of(shape, stride), code)
+                last_shape, last_stride, last_dtype = shape, stride, dtype
+            fields += (at, *matrix)
+        count = len(self.tensors)
+        if len(held) != count:
+            some, fields = iter(fields), []
+            for t in self.tensors:
+                fields += (0,) * 5 if t is None else (next(some), next(some), next(some), next(some), next(some))
         self.array = (OrthoMat * count)()
         struct.pack_into("Pqqqi4x" * count, self.array, 0, *fields)
-        self._pointers = pointers
 
     def __len__(self):
         return len(self.tensors)
 
     def current(self):
         """The descriptors, taken anew if a tensor's memory is another one by now."""
-        if [0 if t is None else t.data_ptr() for t in self.tensors] != self._pointers:
+        import torch
+        if list(map(torch.Tensor.data_ptr, self._held)) != self._pointers:
             self._describe()
         return self.array
+
+
+_DTYPE = operator.attrgetter("dtype")
 
 
 def _mats_dtypes():
@@ -574,21 +585,18 @@ def _mats_dtypes():
                    torch.float8_e4m3fn: ORTHO_E4M3, torch.float8_e8m0fnu: ORTHO_E8M0}
 
 
-def _rows_of(t):
+def _rows_of(shape, strides):
     """(rows, cols, ld) of a tensor as a matrix: its first dimension by the others; a vector is
     one row."""
-    shape = t.shape
     if len(shape) < 2:
-        n = t.numel()
-        if n > 1 and t.stride(0) != 1:
+        n = shape[0] if shape else 1
+        if n > 1 and strides[0] != 1:
             raise ValueError("expected unit stride along columns")
         return 1, n, max(n, 1)
-    rows, cols, step = shape[0], 1, 1
-    strides = t.stride()
+    rows, cols = shape[0], 1
     for d in range(len(shape) - 1, 0, -1):
-        if shape[d] != 1 and strides[d] != step:
+        if shape[d] != 1 and strides[d] != cols:
             raise ValueError("expected unit stride along columns")
-        step *= shape[d]
         cols *= shape[d]
     if rows <= 1:
         return rows, cols, max(cols, 1)

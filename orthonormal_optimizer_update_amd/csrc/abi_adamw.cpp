@@ -16,6 +16,8 @@ hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 bool consecutive(const ortho_mat& a) { return a.rows == 1 || a.ld == a.cols; }
 
+uint32_t pitch(const ortho_mat& a) { return a.rows == 1 ? 0 : static_cast<uint32_t>(a.ld); }
+
 constexpr int64_t kMaxUnits = int64_t{1} << 30;  // of one launch over more than one tensor
 
 AdamwScalars scalars(const ortho_adamw& h) {
@@ -96,7 +98,7 @@ ortho_status grad_norm(int32_t count, const ortho_mat* G, double max_norm, float
   for (int32_t i = 0; i < count; ++i) {
     const bool flat = consecutive(G[i]);
     const int64_t rows = flat ? 1 : G[i].rows, cols = flat ? G[i].rows * G[i].cols : G[i].cols;
-    const Deal d = deal(rows, cols, 32);
+    const Deal d = deal(rows, cols, G[i].dtype == ORTHO_BF16 ? 32 : 16);
     if (!f.fits(d.units) && flush() != hipSuccess) return ORTHO_E_HIP;
     f.add(d.units) = {G[i].data, G[i].ld, cols, static_cast<int32_t>(rows), static_cast<int32_t>(d.across),
                       d.lanes, G[i].dtype == ORTHO_BF16};
@@ -146,15 +148,15 @@ ortho_status adamw_step(int32_t count, const ortho_mat* X, const ortho_mat* G, c
     t.g = G[i].data;
     t.m = M[i].data;
     t.v = V[i].data;
-    t.ldx = X[i].ld;
-    t.ldg = G[i].ld;
-    t.ldm = M[i].ld;
-    t.ldv = V[i].ld;
+    t.ldx = pitch(X[i]);
+    t.ldg = pitch(G[i]);
+    t.ldm = pitch(M[i]);
+    t.ldv = pitch(V[i]);
     if (codes) {
       t.sm = static_cast<float*>(SM[i].data);
       t.sv = static_cast<float*>(SV[i].data);
-      t.ldsm = SM[i].ld;
-      t.ldsv = SV[i].ld;
+      t.ldsm = pitch(SM[i]);
+      t.ldsv = pitch(SV[i]);
     }
     t.rows = static_cast<int32_t>(X[i].rows);
     t.cols = static_cast<int32_t>(X[i].cols);

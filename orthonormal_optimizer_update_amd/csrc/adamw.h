@@ -57,21 +57,21 @@ struct RowTensor {
   const void* g;
   void *m, *v;
   float *sm, *sv;                // null: states in 32 bits
-  int64_t ldx, ldg, ldm, ldv, ldsm, ldsv;
+  uint32_t ldx, ldg, ldm, ldv, ldsm, ldsv;
   int32_t rows, cols;
   int32_t across;                // units next to each other along the columns
   int32_t lanes;
   int32_t index, kind;
 };
 struct AdamwRows {
-  static constexpr int kMost = 28;
+  static constexpr int kMost = 38;   // 96 bytes each
   AdamwScalars h;
   RowTensor t[kMost];
   int32_t first[kLanes];
   int32_t units;
 };
 
-// Gradients: units of 256 >> lanes rows of 32 << lanes columns.
+// Gradients: units of 256 >> lanes rows of 4 << lanes pieces of 16 bytes.
 struct NormTensor {
   const void* g;
   int64_t ld, cols;

@@ -3,7 +3,10 @@
 #include "fp8.h"
 
 // Products and sums join where the code says so and nowhere else: a tensor comes
-// out the same whichever kernel its layout picks.
+// out the same whichever kernel its layout picks.  m and v take the separate
+// roundings of the formula written in elementary operations, so that their codes
+// are the same as such a form's: a code that goes the other way at a tie can be its
+// block's largest, and then the next step's scale differs.
 #pragma clang fp contract(off)
 
 namespace ortho {
@@ -29,31 +32,48 @@ __device__ __forceinline__ uint32_t tensor_key(const AdamwScalars& h, int64_t st
   return mix(key ^ mix(static_cast<uint32_t>(index) + kStride));
 }
 
+// The bits of the elements from `element` on, as seeds of the conversion
+// instructions, which take a seed's top 20 (e4m3) and 16 bits (bf16).
 struct Bits {
-  uint32_t a, b;
-  __device__ __forceinline__ Bits(uint32_t key, int64_t element) {
-    const uint64_t e = static_cast<uint64_t>(element);
-    a = mix(static_cast<uint32_t>(e) ^ (key + kStride * static_cast<uint32_t>(e >> 32)));
+  uint32_t low, key, next;   // next: the key behind a multiple of 2^32
+  __device__ __forceinline__ Bits(uint32_t tensor, int64_t element) {
+    low = static_cast<uint32_t>(element);
+    key = tensor + kStride * static_cast<uint32_t>(static_cast<uint64_t>(element) >> 32);
+    next = key + kStride;
+  }
+  // m's seed, and sqrt(v)'s.
+  __device__ __forceinline__ void at(int j, uint32_t& a, uint32_t& b) const {
+    const uint32_t e = low + j;
+    a = mix(e ^ (e < low ? next : key));
     b = mix(a + kStride);
   }
-  __device__ __forceinline__ uint32_t m() const { return a >> 12; }
-  __device__ __forceinline__ uint32_t v() const { return b >> 12; }
-  __device__ __forceinline__ uint32_t x() const { return (a & 4095u) << 4 | (b & 15u); }
+  // The weight's: a's low 12 bits, then b's low 4.
+  static __device__ __forceinline__ uint32_t weight(uint32_t a, uint32_t b) {
+    return __builtin_amdgcn_alignbit(a, b << 28, 12);
+  }
 };
 
-// x with `bits` added below its bit kFrom and cut there; infinities and NaN stay.
-template <int kFrom>
-__device__ __forceinline__ float cut(float x, uint32_t bits) {
-  const uint32_t u = (__float_as_uint(x) + bits) & ~((1u << kFrom) - 1);
-  return __builtin_fabsf(x) < __builtin_inff() ? __uint_as_float(u) : x;
-}
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-// |q| <= 448 to a value that e4m3 holds: below 2^-6 its steps are 2^-9, which are
-// fp32's bit 20 after 2^-6 is added.
-__device__ __forceinline__ float cut_e4m3(float q, uint32_t bits) {
-  const float a = __builtin_fabsf(q), shift = a < 0x1p-6f ? 0x1p-6f : 0.f;
-  const float c = cut<20>(a + shift, bits) - shift;
-  return __builtin_copysignf(c, q);
+// Eight weights to column c of a row of `limit`, rounded by their seeds.
+__device__ __forceinline__ void store_weights8(uint16_t* row, int c, int limit, const float (&x)[8],
+                                               const uint32_t (&seed)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    bf16x2 p = {0, 0};
+    p = __builtin_amdgcn_cvt_sr_bf16_f32(p, x[2 * j], seed[2 * j], false);
+    p = __builtin_amdgcn_cvt_sr_bf16_f32(p, x[2 * j + 1], seed[2 * j + 1], true);
+    w[j] = __builtin_bit_cast(uint32_t, p);
+  }
+  if (c + 8 <= limit) {
+    const uint4 u = make_uint4(w[0], w[1], w[2], w[3]);
+    __builtin_memcpy(row + c, &u, 16);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j < limit) row[c + j] = static_cast<uint16_t>(w[j >> 1] >> 16 * (j & 1));
 }
 
 // ---- the step ----
@@ -82,13 +102,20 @@ __device__ __forceinline__ StepScalars step_scalars(const AdamwScalars& h) {
 }
 
 // m and v are fp32 from here to the next step's start; only storage rounds them.
-__device__ __forceinline__ void adamw(const AdamwScalars& h, const StepScalars& s, float& x, float g, float& m,
-                                      float& v) {
+// Returns sqrt(v).  The weight takes the reciprocal's rounding (one unit in the last
+// place) in place of a division's.
+//
+// kLimited: v beyond fp32's range is its largest number (NaN stays).
+template <bool kLimited>
+__device__ __forceinline__ float adamw(const AdamwScalars& h, const StepScalars& s, float& x, float g, float& m,
+                                       float& v) {
   g *= s.factor;
-  m = fmaf(h.b1, m, h.c1 * g);
-  v = fmaf(h.b2, v, h.c2 * (g * g));
-  const float down = fmaf(__builtin_sqrtf(v), s.root, h.eps);
-  x = fmaf(s.keep, x, -(s.size * (m / down)));
+  m = h.b1 * m + h.c1 * g;
+  v = h.b2 * v + h.c2 * (g * g);
+  if constexpr (kLimited) v = __builtin_elementwise_minimum(v, __FLT_MAX__);
+  const float root = __builtin_sqrtf(v);
+  x = fmaf(-s.size, m * __builtin_amdgcn_rcpf(fmaf(root, s.root, h.eps)), s.keep * x);
+  return root;
 }
 
 // The tensor of a unit; `first` is this lane's.
@@ -123,13 +150,21 @@ __device__ __forceinline__ void flat_unit(const AdamwScalars& h, const StepScala
   unpack8(rm, mv);
   unpack8(rv, vv);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) adamw(h, s, xv[j], gv[j], mv[j], vv[j]);
-  if constexpr (kStochastic && sizeof(TX) == 2) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) xv[j] = cut<16>(xv[j], Bits(key, base + c + j).x());
-  }
+  for (int j = 0; j < 8; ++j) adamw<false>(h, s, xv[j], gv[j], mv[j], vv[j]);
   if constexpr (kWhole) limit = kUnit;
-  store8(x, c, limit, xv);
+  if constexpr (kStochastic && sizeof(TX) == 2) {
+    const Bits bits(key, base + c);
+    uint32_t seed[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t a, b;
+      bits.at(j, a, b);
+      seed[j] = Bits::weight(a, b);
+    }
+    store_weights8(x, c, limit, xv, seed);
+  } else {
+    store8(x, c, limit, xv);
+  }
   store8(m, c, limit, mv);
   store8(v, c, limit, vv);
 }
@@ -185,70 +220,112 @@ __device__ __forceinline__ void values8(uint2 u, float scale, float (&v)[8]) {
   v[4] = c[0] * scale; v[5] = c[1] * scale; v[6] = d[0] * scale; v[7] = d[1] * scale;
 }
 
+// The largest of 16 lanes' values (a row of the wave), NaN if there is one.
+template <int kRotate>
+__device__ __forceinline__ float rotated(float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x120 + kRotate, 0xf, 0xf, false));
+}
 __device__ __forceinline__ float max_of_16_lanes(float v) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
+  v = __builtin_elementwise_maximum(v, rotated<8>(v));
+  v = __builtin_elementwise_maximum(v, rotated<4>(v));
+  v = __builtin_elementwise_maximum(v, rotated<2>(v));
+  return __builtin_elementwise_maximum(v, rotated<1>(v));
 }
 
-// Codes of a block's eight elements here, the 16 lanes of a block together.
+// Codes of a block's eight elements here, the 16 lanes of a block together.  A block
+// with an infinity or NaN (its largest magnitude says so) looks at its finite
+// elements once more.
 template <bool kStochastic, bool kPositive>
-__device__ __forceinline__ uint2 to_codes8(const float (&v)[8], const uint32_t (&bits)[8], float& scale) {
-  float top = 0.f, f;
+__device__ __forceinline__ uint2 to_codes8(const float (&v)[8], const uint32_t (&seed)[8], float& scale) {
+  float top = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_abs(v[j]));
-  block_scale<false>(max_of_16_lanes(top), scale, f);
+  for (int j = 0; j < 8; ++j) top = __builtin_elementwise_maximum(top, kPositive ? v[j] : __builtin_fabsf(v[j]));
+  top = max_of_16_lanes(top);
+  const bool finite = top < __builtin_inff();
+  if (!finite) {
+    top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_abs(v[j]));
+    top = max_of_16_lanes(top);
+  }
+  const float s = fmaxf(top * (1.f / kFp8Top), 0x1p-126f);
+  scale = top == 0.f ? 1.f : s;
+  const float f = 1.f / scale;
   float q[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     q[j] = v[j] * f;
-    if constexpr (kStochastic) {
-      // (the largest may come out a rounding above 448; infinities and NaN stay)
-      const float in = __builtin_fabsf(q[j]) < 512.f ? __builtin_copysignf(fminf(__builtin_fabsf(q[j]), kFp8Top), q[j]) : q[j];
-      q[j] = cut_e4m3(in, bits[j]);
-    }
-    if constexpr (kPositive) q[j] = v[j] > 0.f && q[j] < 0x1p-9f ? 0x1p-9f : q[j];
+    // (the largest may come out a rounding above 448)
+    if constexpr (kPositive) q[j] = __builtin_amdgcn_fmed3f(q[j], q[j] > 0.f ? 0x1p-9f : 0.f, kFp8Top);
+    else if constexpr (kStochastic) q[j] = __builtin_amdgcn_fmed3f(q[j], -kFp8Top, kFp8Top);
   }
-  return make_uint2(pack_e4m3x4(q[0], q[1], q[2], q[3]), pack_e4m3x4(q[4], q[5], q[6], q[7]));
+  if (!finite) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (!(__builtin_fabsf(v[j]) < __builtin_inff())) q[j] = __builtin_nanf("");
+  }
+  if constexpr (kStochastic) {
+    uint32_t u[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      int w = 0;
+      w = __builtin_amdgcn_cvt_sr_fp8_f32(q[4 * i], seed[4 * i], w, 0);
+      w = __builtin_amdgcn_cvt_sr_fp8_f32(q[4 * i + 1], seed[4 * i + 1], w, 1);
+      w = __builtin_amdgcn_cvt_sr_fp8_f32(q[4 * i + 2], seed[4 * i + 2], w, 2);
+      w = __builtin_amdgcn_cvt_sr_fp8_f32(q[4 * i + 3], seed[4 * i + 3], w, 3);
+      u[i] = static_cast<uint32_t>(w);
+    }
+    return make_uint2(u[0], u[1]);
+  } else {
+    return make_uint2(pack_e4m3x4(q[0], q[1], q[2], q[3]), pack_e4m3x4(q[4], q[5], q[6], q[7]));
+  }
 }
 
-template <typename TX, typename TG, bool kStochastic>
-__device__ __forceinline__ void row_unit(const AdamwScalars& h, const StepScalars& s, const RowTensor& t, int at,
-                                         uint32_t key) {
-  const int lanes = t.lanes, across = t.across, cols = t.cols, down = at / across;
-  const int row = (down << (8 - lanes)) + (threadIdx.x >> lanes);
-  const int c = (((at - down * across) << lanes) + (threadIdx.x & ((1 << lanes) - 1))) * 8;
-  // (the 16 lanes of a block share the row)
-  if (row >= t.rows || (c & ~127) >= cols) return;
-  TX* const x = static_cast<TX*>(t.x) + row * t.ldx;
-  const TG* const g = static_cast<const TG*>(t.g) + row * t.ldg;
-  const int64_t element = (int64_t)row * cols + c;
+// Eight codes at c of a row of `cols`.
+template <bool kWhole>
+__device__ __forceinline__ uint2 unit_load_codes(const uint8_t* row, int c, int cols) {
+  if constexpr (!kWhole) return load_codes8(row, c, cols);
+  uint2 u;
+  __builtin_memcpy(&u, row + c, 8);
+  return u;
+}
+
+// One thread's eight elements of a row.  kWhole: all inside.
+template <typename TX, typename TG, bool kStochastic, bool kWhole>
+__device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScalars& s, const RowTensor& t, int row, int c,
+                                          uint32_t key) {
+  int cols = t.cols;
+  TX* const x = static_cast<TX*>(t.x) + static_cast<uint64_t>(t.ldx) * row;
+  const TG* const g = static_cast<const TG*>(t.g) + static_cast<uint64_t>(t.ldg) * row;
   float xv[8], gv[8], mv[8], vv[8];
-  const auto rx = load_raw8(x, c, cols);
-  const auto rg = load_raw8(g, c, cols);
+  const auto rx = unit_load<kWhole>(x, c, cols);
+  const auto rg = unit_load<kWhole>(g, c, cols);
+  const Bits bits(key, static_cast<int64_t>(row) * cols + c);
+  uint32_t seed_m[8] = {}, seed_v[8] = {};
   if (t.sm == nullptr) {
-    float* const m = static_cast<float*>(t.m) + row * t.ldm;
-    float* const v = static_cast<float*>(t.v) + row * t.ldv;
-    const auto rm = load_raw8(m, c, cols);
-    const auto rv = load_raw8(v, c, cols);
+    float* const m = static_cast<float*>(t.m) + static_cast<uint64_t>(t.ldm) * row;
+    float* const v = static_cast<float*>(t.v) + static_cast<uint64_t>(t.ldv) * row;
+    const auto rm = unit_load<kWhole>(m, c, cols);
+    const auto rv = unit_load<kWhole>(v, c, cols);
     unpack8(rx, xv);
     unpack8(rg, gv);
     unpack8(rm, mv);
     unpack8(rv, vv);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) adamw(h, s, xv[j], gv[j], mv[j], vv[j]);
+    for (int j = 0; j < 8; ++j) adamw<false>(h, s, xv[j], gv[j], mv[j], vv[j]);
     if constexpr (kStochastic && sizeof(TX) == 2) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) xv[j] = cut<16>(xv[j], Bits(key, element + j).x());
+      for (int j = 0; j < 8; ++j) bits.at(j, seed_m[j], seed_v[j]);
     }
+    if constexpr (kWhole) cols = c + 8;
     store8(m, c, cols, mv);
     store8(v, c, cols, vv);
   } else {
-    uint8_t* const m = static_cast<uint8_t*>(t.m) + row * t.ldm;
-    uint8_t* const v = static_cast<uint8_t*>(t.v) + row * t.ldv;
-    float* const sm = t.sm + row * t.ldsm + (c >> 7);
-    float* const sv = t.sv + row * t.ldsv + (c >> 7);
-    const uint2 qm = load_codes8(m, c, cols), qv = load_codes8(v, c, cols);
+    uint8_t* const m = static_cast<uint8_t*>(t.m) + static_cast<uint64_t>(t.ldm) * row;
+    uint8_t* const v = static_cast<uint8_t*>(t.v) + static_cast<uint64_t>(t.ldv) * row;
+    float* const sm = t.sm + static_cast<uint64_t>(t.ldsm) * row + (c >> 7);
+    float* const sv = t.sv + static_cast<uint64_t>(t.ldsv) * row + (c >> 7);
+    const uint2 qm = unit_load_codes<kWhole>(m, c, cols), qv = unit_load_codes<kWhole>(v, c, cols);
     const float ms = *sm, vs = *sv;
     unpack8(rx, xv);
     unpack8(rg, gv);
@@ -257,29 +334,22 @@ __device__ __forceinline__ void row_unit(const AdamwScalars& h, const StepScalar
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       vv[j] *= vv[j];
-      adamw(h, s, xv[j], gv[j], mv[j], vv[j]);
-      // (its code could not say infinite)
-      vv[j] = __builtin_sqrtf(vv[j] > __FLT_MAX__ ? __FLT_MAX__ : vv[j]);
+      vv[j] = adamw<true>(h, s, xv[j], gv[j], mv[j], vv[j]);
     }
-    uint32_t bm[8] = {}, bv[8] = {};
     if constexpr (kStochastic) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const Bits r(key, element + j);
-        bm[j] = r.m();
-        bv[j] = r.v();
-        if constexpr (sizeof(TX) == 2) xv[j] = cut<16>(xv[j], r.x());
-      }
+      for (int j = 0; j < 8; ++j) bits.at(j, seed_m[j], seed_v[j]);
     }
     // past the row's end: zeros, which enter no maximum
-    if (c + 8 > cols) {
+    if constexpr (!kWhole) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (c + j >= cols) mv[j] = vv[j] = 0.f;
     }
     float ms2, vs2;
-    const uint2 um = to_codes8<kStochastic, false>(mv, bm, ms2);
-    const uint2 uv = to_codes8<kStochastic, true>(vv, bv, vs2);
+    const uint2 um = to_codes8<kStochastic, false>(mv, seed_m, ms2);
+    const uint2 uv = to_codes8<kStochastic, true>(vv, seed_v, vs2);
+    if constexpr (kWhole) cols = c + 8;
     store_codes8(m, c, cols, um);
     store_codes8(v, c, cols, uv);
     if ((threadIdx.x & 15) == 0) {
@@ -287,11 +357,30 @@ __device__ __forceinline__ void row_unit(const AdamwScalars& h, const StepScalar
       *sv = vs2;
     }
   }
-  store8(x, c, cols, xv);
+  if constexpr (kStochastic && sizeof(TX) == 2) {
+    uint32_t seed[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) seed[j] = Bits::weight(seed_m[j], seed_v[j]);
+    store_weights8(x, c, cols, xv, seed);
+  } else {
+    store8(x, c, cols, xv);
+  }
+}
+
+template <typename TX, typename TG, bool kStochastic>
+__device__ __forceinline__ void row_unit(const AdamwScalars& h, const StepScalars& s, const RowTensor& t, int at,
+                                         uint32_t key) {
+  const int lanes = t.lanes, across = t.across, down = at / across;
+  const int row = (down << (8 - lanes)) + (threadIdx.x >> lanes);
+  const int c = (((at - down * across) << lanes) + (threadIdx.x & ((1 << lanes) - 1))) * 8;
+  // (the 16 lanes of a block share the row)
+  if (row >= t.rows || (c & ~127) >= t.cols) return;
+  if (__all(c + 8 <= t.cols)) row_piece<TX, TG, kStochastic, true>(h, s, t, row, c, key);
+  else row_piece<TX, TG, kStochastic, false>(h, s, t, row, c, key);
 }
 
 template <bool kStochastic>
-__global__ __launch_bounds__(256) void adamw_rows_kernel(AdamwRows a) {
+__global__ __launch_bounds__(256, 5) void adamw_rows_kernel(AdamwRows a) {
   const int first = a.first[threadIdx.x & (kLanes - 1)];
   const StepScalars s = step_scalars(a.h);
   if (s.skip) return;
@@ -317,49 +406,69 @@ __device__ __forceinline__ double sum_of_wave(double x) {
   return x;
 }
 
+// A thread's four pieces of 16 bytes of a unit.
+struct Pieces {
+  uint4 u[4];
+  int bf;
+};
+
 template <typename T>
-__device__ __forceinline__ double squares(const T* row, int64_t c, int64_t cols, int step) {
-  Raw8<T> r[4];
-  if (c + 3 * step + 8 <= cols) {
+__device__ __forceinline__ void load_pieces(const NormTensor& t, int64_t row, int64_t at, uint4 (&u)[4]) {
+  constexpr int kN = 16 / sizeof(T);
+  const T* const p = static_cast<const T*>(t.g) + row * t.ld;
+  const int step = kN << t.lanes;
+  const int64_t c = at * kN;
+  if (row < t.rows && c + 3 * step + kN <= t.cols) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) r[q] = load_raw8(row + c + q * step, 0, 8);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t at = c + q * step, left = cols - at;
-      r[q] = left > 0 ? load_raw8(row + at, 0, left < 8 ? static_cast<int>(left) : 8) : Raw8<T>{};
-    }
+    for (int q = 0; q < 4; ++q) __builtin_memcpy(&u[q], p + c + q * step, 16);
+    return;
   }
-  double sum = 0.0;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    float v[8];
-    unpack8(r[q], v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const double d = static_cast<double>(v[j]);
-      sum = fma(d, d, sum);
-    }
+    const int64_t left = row < t.rows ? t.cols - (c + q * step) : 0;
+    u[q] = left > 0 ? load16(p + c + q * step, 0, left < kN ? static_cast<int>(left) : kN) : make_uint4(0, 0, 0, 0);
   }
-  return sum;
 }
 
+__device__ __forceinline__ Pieces load_unit(const NormParts& a, int64_t first, int64_t unit) {
+  const int i = tensor_of(first, unit);
+  const NormTensor& t = a.t[i];
+  const int lanes = t.lanes, at = static_cast<int>(unit - a.first[i]), across = t.across;
+  const int down = at / across;
+  const int64_t row = ((int64_t)down << (8 - lanes)) + (threadIdx.x >> lanes);
+  const int64_t c = ((int64_t)(at - down * across) << (lanes + 2)) + (threadIdx.x & ((1 << lanes) - 1));
+  Pieces p;
+  p.bf = t.bf;
+  if (p.bf) load_pieces<uint16_t>(t, row, c, p.u);
+  else load_pieces<float>(t, row, c, p.u);
+  return p;
+}
+
+__device__ __forceinline__ double add_square(double sum, uint32_t bits) {
+  const double d = static_cast<double>(__uint_as_float(bits));
+  return fma(d, d, sum);
+}
+
+// The next unit's loads are under way while this one's squares are added.
 __global__ __launch_bounds__(256) void grad_norm_parts_kernel(NormParts a) {
   __shared__ double red[4];
   const int64_t first = a.first[threadIdx.x & (kLanes - 1)];
-  double sum = 0.0;
+  double part[4] = {};
+  Pieces p = load_unit(a, first, blockIdx.x);   // (no more workgroups than units)
   for (int64_t unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
-    const int i = tensor_of(first, unit);
-    const NormTensor& t = a.t[i];
-    const int lanes = t.lanes, at = static_cast<int>(unit - a.first[i]), across = t.across;
-    const int down = at / across;
-    const int64_t row = ((int64_t)down << (8 - lanes)) + (threadIdx.x >> lanes);
-    const int64_t c = ((int64_t)(at - down * across) << (lanes + 5)) + (threadIdx.x & ((1 << lanes) - 1)) * 8;
-    if (row < t.rows) {
-      if (t.bf) sum += squares(static_cast<const uint16_t*>(t.g) + row * t.ld, c, t.cols, 8 << lanes);
-      else sum += squares(static_cast<const float*>(t.g) + row * t.ld, c, t.cols, 8 << lanes);
+    const Pieces now = p;
+    if (unit + gridDim.x < a.units) p = load_unit(a, first, unit + gridDim.x);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t w[4] = {now.u[q].x, now.u[q].y, now.u[q].z, now.u[q].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (now.bf) part[q] = add_square(part[q], w[j] << 16);
+        part[q] = add_square(part[q], now.bf ? w[j] & 0xffff0000u : w[j]);
+      }
     }
   }
+  double sum = (part[0] + part[1]) + (part[2] + part[3]);
   sum = sum_of_wave(sum);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
   __syncthreads();
@@ -386,10 +495,10 @@ __global__ __launch_bounds__(1024) void grad_norm_join_kernel(const double* part
   }
 }
 
-// Workgroups of 256 that the chip holds at once; more units than that are walked.
-constexpr int kResident = 2048;
+// A workgroup per unit, as far as a launch goes (2^32 threads); more are walked.
+constexpr int kMostGroups = (1 << 24) - 1;
 
-inline dim3 grid_of(int units) { return dim3(units < kResident ? units : kResident); }
+inline dim3 grid_of(int units) { return dim3(units < kMostGroups ? units : kMostGroups); }
 
 }  // namespace
 

@@ -629,17 +629,19 @@ ortho_status validate_fp8_matmul(const ortho_mat& A, const ortho_mat& SA, const 
 
 namespace {
 
-// The bytes from a matrix's first to its last element.
+// The addresses from a matrix's first byte to behind its last.
 struct Extent {
-  uintptr_t begin;
-  __int128 size;
+  uintptr_t begin, end;
   const ortho_mat* a;
   bool written;
 };
 
 Extent extent(const ortho_mat& a, bool written) {
   const int64_t e = element_size(a), pitch = a.rows > 1 ? a.ld * e : 0;
-  return {reinterpret_cast<uintptr_t>(a.data), static_cast<__int128>(a.rows - 1) * pitch + a.cols * e, &a, written};
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.data);
+  // (the largest descriptors' sizes pass 64 bits)
+  const __int128 end = static_cast<__int128>(a.rows - 1) * pitch + a.cols * e + at;
+  return {at, end > static_cast<__int128>(UINTPTR_MAX) ? UINTPTR_MAX : static_cast<uintptr_t>(end), &a, written};
 }
 
 // Whether of `count` matrices every written one is apart from all others.  Sorted by
@@ -647,17 +649,17 @@ Extent extent(const ortho_mat& a, bool written) {
 bool all_apart(Extent* x, size_t count) {
   const auto before = [](const Extent& a, const Extent& b) { return a.begin < b.begin; };
   if (!std::is_sorted(x, x + count, before)) std::sort(x, x + count, before);
-  size_t open = 0;   // the first that may reach as far as the one at hand
-  __int128 reach = 0;   // the furthest end of x[open ..]
+  size_t open = 0;       // the first that may reach as far as the one at hand
+  uintptr_t reach = 0;   // the furthest end of x[open ..]
   for (size_t i = 0; i < count; ++i) {
-    if (i == open || reach <= static_cast<__int128>(x[i].begin)) {
+    if (i == open || reach <= x[i].begin) {
       open = i;
-      reach = x[i].begin + x[i].size;
+      reach = x[i].end;
       continue;
     }
     for (size_t j = open; j < i; ++j)
       if ((x[i].written || x[j].written) && !apart(*x[i].a, *x[j].a)) return false;
-    reach = std::max(reach, x[i].begin + x[i].size);
+    reach = std::max(reach, x[i].end);
   }
   return true;
 }
@@ -668,6 +670,7 @@ ortho_mat array_of(const void* p, int64_t count, int64_t bytes) {
 }
 
 bool small_enough(const ortho_mat& a) { return a.rows <= kMaxElements / a.cols; }
+bool near_rows(const ortho_mat& a) { return a.rows == 1 || a.ld < int64_t{1} << 32; }
 
 }  // namespace
 
@@ -711,11 +714,14 @@ ortho_status validate_adamw(int32_t count, const ortho_mat* X, const ortho_mat* 
     for (const ortho_mat* t : {&G[i], &M[i], &V[i]})
       if (!shape_is(*t, X[i].rows, X[i].cols)) return ORTHO_E_SHAPE;
     if (!small_enough(X[i])) return ORTHO_E_SHAPE;
+    for (const ortho_mat* t : {&X[i], &G[i], &M[i], &V[i]})
+      if (!near_rows(*t)) return ORTHO_E_LAYOUT;
     if (M[i].dtype != ORTHO_E4M3) continue;
     ++codes;
     if (SM == nullptr || SV == nullptr) return ORTHO_E_NULL;
     for (const ortho_mat* t : {&SM[i], &SV[i]})
       if ((st = check_like(t, ORTHO_F32, X[i].rows, cdiv(X[i].cols, kFp8BlockSize))) != ORTHO_OK) return st;
+    if (!near_rows(SM[i]) || !near_rows(SV[i])) return ORTHO_E_LAYOUT;
   }
   Extent few[64], *all = few;
   const size_t most = 4 * static_cast<size_t>(count) + 2 * codes;

@@ -195,7 +195,7 @@ ortho_status validate_fp8_matmul(const ortho_mat& A, const ortho_mat& SA, const 
 // AdamW and the gradients' norm.
 constexpr int64_t kMaxElements = int64_t{1} << 40;   // of one tensor
 // Workgroups of one launch over gradients, each with an fp64 sum in the workspace.
-constexpr int kNormGroups = 1024;
+constexpr int kNormGroups = 2048;
 constexpr int kNormPerLaunch = 64;                   // must match NormParts::kMost
 size_t grad_norm_ws_bytes(int32_t count);
 ortho_status validate_grad_norm(int32_t count, const ortho_mat* G, double max_norm, const float* out,

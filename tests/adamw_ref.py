@@ -74,9 +74,10 @@ def step(x, g, m, v, lr, t, betas, eps, decay, factor=1.0):
     size, root = lr / (1 - b1 ** t), 1 / (1 - b2 ** t) ** 0.5
     low = (v2 - ev).clamp(min=0).sqrt() * root + eps       # smallest divisor
     down = v2.sqrt() * root + eps
-    # sqrt 1, root 2, eps 1, sum 1, quotient 1, size 2: eight roundings of the update
+    # sqrt 1, root 2, eps 1, sum 1, reciprocal 2 (one unit in the last place), product 1, size 2: ten
+    # roundings of the update (a quotient in place of reciprocal and product would be eight)
     update = size * m2 / down
-    eu = size * ((m2.abs() + em) / low - m2.abs() / down) + 8 * U * size * (m2.abs() + em) / low
+    eu = size * ((m2.abs() + em) / low - m2.abs() / down) + 10 * U * size * (m2.abs() + em) / low
     keep = 1 - lr * decay
     ex = 3 * U * (keep * x).abs() + eu + U * update.abs()
     return (keep * x - update, ex * 1.01), (m2, em * 1.01), (v2, ev * 1.01)

@@ -62,6 +62,13 @@ def test_adamw_refuses(kw, want):
     assert adamw([tensor(1), tensor(0, bits=8, **kw), tensor(2)]) == want
 
 
+def test_adamw_refuses_far_rows():
+    for k in ("X", "G", "M", "V", "SM", "SV"):
+        t = tensor(0, bits=8)
+        t[k] = M(t[k].rows, t[k].cols, t[k].dtype, ld=1 << 32, data=t[k].data)
+        assert adamw([t]) == LAYOUT
+
+
 def test_adamw_refuses_missing_lists():
     t = tensor(0, bits=8)
     assert adamw([t], scales=False) == NULL
@@ -117,10 +124,10 @@ def test_a_tensor_twice_or_partly_in_another_is_refused(bits):
 
 @pytest.mark.parametrize("args,want", [
     (dict(count=0), PARAM), (dict(most=0.0), PARAM), (dict(most=-1.0), PARAM), (dict(most=math.nan), PARAM), (dict(out=None), NULL),
-    (dict(g=None), NULL), (dict(out=at(0, 8)), LAYOUT), (dict(ws=None), WS), (dict(size=8191), WS), (dict(ws=at(8, 8)), WS),
+    (dict(g=None), NULL), (dict(out=at(0, 8)), LAYOUT), (dict(ws=None), WS), (dict(size=16383), WS), (dict(ws=at(8, 8)), WS),
     (dict(dtype=C8), DTYPE)])
 def test_grad_norm_refuses(args, want):
-    a = dict(count=2, most=1.0, out=at(5), ws=at(8), size=8192, g=0, dtype=BF)
+    a = dict(count=2, most=1.0, out=at(5), ws=at(8), size=16384, g=0, dtype=BF)
     a.update(args)
     g = None if a["g"] is None else array(M(5, 9, a["dtype"], data=at(0)), M(1, 7, F, data=at(1)))
     assert api.lib().grad_norm(a["count"], g, a["most"], a["out"], a["ws"], a["size"], None) == want
@@ -128,7 +135,7 @@ def test_grad_norm_refuses(args, want):
 
 def test_grad_norm_workspace():
     size = api.grad_norm_workspace_size
-    assert size(0) == 0 and size(-1) == 0 and size(1) == 8192 and size(64) == 8192 and size(65) == 16384
+    assert size(0) == 0 and size(-1) == 0 and size(1) == 16384 and size(64) == 16384 and size(65) == 32768
 
 
 # ---- tokens by expert ----
@@ -230,7 +237,7 @@ def test_expert_combine_backward_refuses(kw, want):
 
 
 def test_tensors_as_matrices():
-    f = api._rows_of
+    f = lambda x: api._rows_of(x.shape, x.stride())
     t = torch.zeros(4, 6, 8)
     assert f(torch.zeros(())) == (1, 1, 1) and f(torch.zeros(7)) == (1, 7, 7) and f(t) == (4, 48, 48)
     assert f(t[:, 0]) == (4, 8, 48) and f(t[1:2]) == (1, 48, 48)
@@ -266,5 +273,5 @@ def test_states_of_any_shape():
     M_, V, SM, SV = api.adamw_states([torch.zeros(s) for s in shapes], 8)
     for s, m, v, a, b in zip(shapes, M_, V, SM, SV):
         assert m.shape == v.shape == torch.Size(s) and m.dtype == torch.float8_e4m3fn
-        rows, cols, _ = api._rows_of(torch.zeros(s))
+        rows, cols, _ = api._rows_of(s, torch.zeros(s).stride())
         assert a.shape == b.shape == (rows, -(-cols // 128)) and bool((a == 1).all())
