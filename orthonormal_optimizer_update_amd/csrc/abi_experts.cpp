@@ -78,6 +78,7 @@ ortho_status expert_gather(ortho_mat X, const ortho_mat* S, const int32_t* slot,
     a.pitch_sy = SY->ld * esz(*SY);
     a.blocks = static_cast<int>(S->cols);
     a.scale_bytes = static_cast<int>(esz(*S));
+    while (a.scale_lanes < 8 && 1 << a.scale_lanes < a.blocks) ++a.scale_lanes;
   }
   const Deal d = deal(X.rows, (a.bytes + 15) / 16, 1);
   return done(launch_expert_gather(a, d.lanes, d.across, d.units, as_stream(stream)));

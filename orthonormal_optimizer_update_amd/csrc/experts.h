@@ -33,6 +33,7 @@ struct ExpertGatherArgs {
   uint8_t* sy;
   int64_t pitch_s, pitch_sy;
   int blocks, scale_bytes;       // scales per row, and the bytes of one
+  int scale_lanes;               // 1 << scale_lanes threads per row of scales
 };
 hipError_t launch_expert_gather(const ExpertGatherArgs& a, int lanes, int64_t across, int64_t units, hipStream_t s);
 

@@ -194,7 +194,11 @@ __device__ __forceinline__ int64_t row_of(const ExpertRowsArgs& r, int64_t pair)
 }
 
 // A token's row is read once and written `choices` times.  A workgroup's unit is
-// 256 >> lanes tokens by 1 << lanes pieces of 16 bytes.
+// 256 >> lanes tokens by 1 << lanes pieces of 16 bytes.  Bound by the writes: 8192
+// tokens x 2048 codes to 8 of 64 experts (rows padded to 128) take 36.1 us, 4.5 TB/s,
+// of which the scales, scattered in pieces of 64 bytes, are 4 us (6 written beside
+// each 128 codes by the thread that has them).  A wave per token with scalar rows
+// took 46 us, a thread row per (token, choice), which reads the token anew, 78.
 __global__ __launch_bounds__(256) void expert_gather_kernel(ExpertGatherArgs a, int lanes, int across, int64_t units) {
   if (blockIdx.x >= gridDim.x - a.r.experts * kPadParts) {
     const int at = blockIdx.x - (gridDim.x - a.r.experts * kPadParts);
@@ -209,28 +213,31 @@ __global__ __launch_bounds__(256) void expert_gather_kernel(ExpertGatherArgs a, 
     const int64_t token = (down << (8 - lanes)) + (threadIdx.x >> lanes);
     const int64_t p = ((int64_t)col << lanes) + (threadIdx.x & ((1 << lanes) - 1));
     if (token >= a.r.tokens) continue;
+    if (p >= pieces) continue;
     const int64_t pair = token * a.r.choices;
-    if (p < pieces) {
-      const uint4 u = load_piece(a.x + token * a.pitch_x, p, a.bytes);
-#pragma unroll 4
-      for (int j = 0; j < a.r.choices; ++j) {
-        const int64_t row = row_of(a.r, pair + j);
-        if (row >= 0) copy_piece(a.y + row * a.pitch_y, u, p, a.bytes);
-      }
-    }
-    if (a.s == nullptr) continue;
-    // the scales of the pieces at hand: one for each 8 pieces
-    if ((p & 7) != 0 || p >> 3 >= a.blocks) continue;
-    const uint8_t* const src = a.s + token * a.pitch_s;
-    const int64_t b = p >> 3;
-    const float f = a.scale_bytes == 4 ? reinterpret_cast<const float*>(src)[b] : 0.f;
-    const uint8_t e = a.scale_bytes == 4 ? 0 : src[b];
+    const uint4 u = load_piece(a.x + token * a.pitch_x, p, a.bytes);
 #pragma unroll 4
     for (int j = 0; j < a.r.choices; ++j) {
       const int64_t row = row_of(a.r, pair + j);
-      if (row < 0) continue;
-      if (a.scale_bytes == 4) reinterpret_cast<float*>(a.sy + row * a.pitch_sy)[b] = f;
-      else a.sy[row * a.pitch_sy + b] = e;
+      if (row >= 0) copy_piece(a.y + row * a.pitch_y, u, p, a.bytes);
+    }
+  }
+  if (a.s == nullptr) return;
+  const int wide = a.scale_lanes;
+  const int64_t step = (int64_t)(gridDim.x - a.r.experts * kPadParts) << (8 - wide);
+  for (int64_t token = ((int64_t)blockIdx.x << (8 - wide)) + (threadIdx.x >> wide); token < a.r.tokens; token += step) {
+    const int64_t pair = token * a.r.choices;
+    const uint8_t* const src = a.s + token * a.pitch_s;
+    for (int b = threadIdx.x & ((1 << wide) - 1); b < a.blocks; b += 1 << wide) {
+      const uint32_t scale = a.scale_bytes == 4 ? reinterpret_cast<const uint32_t*>(src)[b] : src[b];
+#pragma unroll 4
+      for (int j = 0; j < a.r.choices; ++j) {
+        const int64_t row = row_of(a.r, pair + j);
+        if (row < 0) continue;
+        uint8_t* const to = a.sy + row * a.pitch_sy;
+        if (a.scale_bytes == 4) reinterpret_cast<uint32_t*>(to)[b] = scale;
+        else to[b] = static_cast<uint8_t>(scale);
+      }
     }
   }
 }
@@ -244,7 +251,7 @@ __device__ __forceinline__ float weight_of(const void* w, int w_bf, int64_t at) 
 
 // kAtOnce choices' loads are under way together.
 template <typename T, int kAtOnce>
-__global__ __launch_bounds__(256) void expert_combine_kernel(ExpertCombineArgs a, int lanes, int across,
+__global__ __launch_bounds__(256) void expert_combine_narrow_kernel(ExpertCombineArgs a, int lanes, int across,
                                                              int64_t units) {
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int64_t down = unit / across;
@@ -285,84 +292,178 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(ExpertCombineArgs a
   }
 }
 
-// kThreads threads per token, kAtOnce choices at a time: their rows of Y are read, the
-// products with dOut summed, and their rows of dY written.
-template <typename T, int kThreads, int kAtOnce>
+// ---- a wave for 512 elements of a token ----
+//
+// Lane j holds the row and the weight of choice j; readlane makes them scalars, so
+// that a row's address is scalar too.  All lanes go through all of it: past a row's
+// end they read zeros and write nothing.
+struct Choices {
+  int row;       // -1: none
+  float weight;
+};
+__device__ __forceinline__ Choices lane_choices(const ExpertRowsArgs& r, int64_t token, const void* w, int w_bf, int64_t ldw) {
+  Choices c = {-1, 0.f};
+  const int lane = threadIdx.x & 63;
+  if (lane < r.choices) {
+    const int s = r.slot[token * r.choices + lane];
+    c.row = s >= 0 && s < r.rows ? s : -1;
+    c.weight = weight_of(w, w_bf, token * ldw + lane);
+  }
+  return c;
+}
+__device__ __forceinline__ int scalar_row(const Choices& c, int j) { return __builtin_amdgcn_readlane(c.row, j); }
+__device__ __forceinline__ float scalar_weight(const Choices& c, int j) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(c.weight), j));
+}
+
+constexpr int kWaveColumns = 512;
+
+// Eight elements at c of a row of n; kWhole: inside.
+template <bool kWhole, typename T>
+__device__ __forceinline__ Raw8<T> piece8(const T* row, int c, int n) {
+  if constexpr (!kWhole) return load_raw8(row, c, n);
+  Raw8<T> r;
+  __builtin_memcpy(&r, row + c, sizeof(r));
+  return r;
+}
+
+template <typename T, int kAtOnce, bool kWhole>
+__device__ __forceinline__ void combine_chunk(const ExpertCombineArgs& a, int64_t token, const Choices& ch, int c) {
+  float sum[8] = {};
+  for (int j0 = 0; j0 < a.r.choices; j0 += kAtOnce) {
+    Raw8<T> y[kAtOnce];
+    int row[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      row[j] = j0 + j < a.r.choices ? scalar_row(ch, j0 + j) : -1;
+      y[j] = piece8<kWhole>(static_cast<const T*>(a.y) + max(row[j], 0) * a.ldy, c, a.n);
+    }
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      if (row[j] < 0) continue;
+      const float w = scalar_weight(ch, j0 + j);
+      float v[8];
+      unpack8(y[j], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] = fmaf(w, v[e], sum[e]);
+    }
+  }
+  if (a.add) {
+    float v[8];
+    if (a.add_bf) unpack8(piece8<kWhole>(static_cast<const uint16_t*>(a.add) + token * a.ldadd, c, a.n), v);
+    else unpack8(piece8<kWhole>(static_cast<const float*>(a.add) + token * a.ldadd, c, a.n), v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += v[e];
+  }
+  store8(static_cast<T*>(a.out) + token * a.ldout, c, kWhole ? c + 8 : a.n, sum);
+}
+
+// Bound by HBM: 8192 tokens x 2048 bf16 from 8 experts each 59.4 us (5.1 TB/s), 66.9
+// with the rows' addresses in vector registers.
+template <typename T, int kAtOnce>
+__global__ __launch_bounds__(256) void expert_combine_kernel(ExpertCombineArgs a, int chunks, int64_t tasks) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int64_t task = (int64_t)blockIdx.x * 4 + wave; task < tasks; task += 4 * (int64_t)gridDim.x) {
+    const int64_t token = task / chunks;
+    const int c0 = static_cast<int>(task - token * chunks) * kWaveColumns, c = c0 + lane * 8;
+    const Choices ch = lane_choices(a.r, token, a.w, a.w_bf, a.ldw);
+    if (c0 + kWaveColumns <= a.n) combine_chunk<T, kAtOnce, true>(a, token, ch, c);
+    else combine_chunk<T, kAtOnce, false>(a, token, ch, c);
+  }
+}
+
+template <int kRotate>
+__device__ __forceinline__ float turned(float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x120 + kRotate, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float sum_of_wave(float v) {
+  v += turned<8>(v);
+  v += turned<4>(v);
+  v += turned<2>(v);
+  v += turned<1>(v);
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+template <typename T, int kAtOnce, bool kWhole>
+__device__ __forceinline__ void grad_chunk(const ExpertCombineGradArgs& a, int64_t token, const int (&row)[kAtOnce],
+                                           const float (&w)[kAtOnce], float (&dot)[kAtOnce], int c) {
+  const Raw8<T> rd = piece8<kWhole>(static_cast<const T*>(a.dout) + token * a.lddout, c, a.n);
+  float d[8];
+  if (a.y) {
+    Raw8<T> y[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) y[j] = piece8<kWhole>(static_cast<const T*>(a.y) + max(row[j], 0) * a.ldy, c, a.n);
+    unpack8(rd, d);
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      float v[8];
+      unpack8(y[j], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dot[j] = fmaf(d[e], v[e], dot[j]);
+    }
+  } else {
+    unpack8(rd, d);
+  }
+#pragma unroll
+  for (int j = 0; j < kAtOnce; ++j) {
+    if (row[j] < 0) continue;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = w[j] * d[e];
+    store8(static_cast<T*>(a.dy) + row[j] * a.lddy, c, kWhole ? c + 8 : a.n, v);
+  }
+}
+
+// kWaves waves per token, kAtOnce choices at a time: their rows of Y are read, the
+// products with dOut summed, their rows of dY written.  Bound by HBM: 8192 tokens x
+// 2048 bf16, 8 choices 115 us (5.0 TB/s).
+template <typename T, int kAtOnce, int kWaves>
 __global__ __launch_bounds__(256) void expert_combine_grad_kernel(ExpertCombineGradArgs a, int64_t groups) {
-  __shared__ float red[2][4][kAtOnce];
+  __shared__ float red[2][4][64];
   if (blockIdx.x >= gridDim.x - a.r.experts * kPadParts) {
     const int at = blockIdx.x - (gridDim.x - a.r.experts * kPadParts);
     clear_padding(a.r, at / kPadParts, at % kPadParts, kPadParts, static_cast<uint8_t*>(a.dy), a.lddy * sizeof(T),
                   (int64_t)a.n * sizeof(T), nullptr, 0, 0, 0);
     return;
   }
-  constexpr int kTokens = 256 / kThreads;
-  const int t = threadIdx.x % kThreads;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int turn = 0;
   for (int64_t group = blockIdx.x; group < groups; group += gridDim.x - a.r.experts * kPadParts) {
-    const int64_t token = group * kTokens + threadIdx.x / kThreads;
-    if (token >= a.r.tokens) continue;   // (whole waves; with 256 threads the workgroup)
+    const int64_t token = kWaves == 1 ? group * 4 + wave : group;
+    if (token >= a.r.tokens) continue;
+    const Choices ch = lane_choices(a.r, token, a.w, a.w_bf, a.ldw);
+    float mine = 0.f;   // lane j: choice j's sum
     for (int j0 = 0; j0 < a.r.choices; j0 += kAtOnce) {
-      int64_t row[kAtOnce];
+      int row[kAtOnce];
       float w[kAtOnce], dot[kAtOnce];
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
-        const int at = min(j0 + j, a.r.choices - 1);
-        row[j] = j0 + j < a.r.choices ? row_of(a.r, token * a.r.choices + at) : -1;
-        w[j] = weight_of(a.w, a.w_bf, token * a.ldw + at);
+        row[j] = j0 + j < a.r.choices ? scalar_row(ch, j0 + j) : -1;
+        w[j] = scalar_weight(ch, min(j0 + j, 63));
         dot[j] = 0.f;
       }
-      for (int c = t * 8; c < a.n; c += kThreads * 8) {
-        const Raw8<T> rd = load_raw8(static_cast<const T*>(a.dout) + token * a.lddout, c, a.n);
-        float d[8];
-        if (a.y) {
-          Raw8<T> y[kAtOnce];
-#pragma unroll
-          for (int j = 0; j < kAtOnce; ++j)
-            y[j] = load_raw8(static_cast<const T*>(a.y) + max(row[j], (int64_t)0) * a.ldy, c, a.n);
-          unpack8(rd, d);
-#pragma unroll
-          for (int j = 0; j < kAtOnce; ++j) {
-            float v[8];
-            unpack8(y[j], v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dot[j] = fmaf(d[e], v[e], dot[j]);
-          }
-        } else {
-          unpack8(rd, d);
-        }
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-          if (row[j] < 0) continue;
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = w[j] * d[e];
-          store8(static_cast<T*>(a.dy) + row[j] * a.lddy, c, a.n, v);
-        }
+      for (int c0 = kWaves == 1 ? 0 : wave * kWaveColumns; c0 < a.n; c0 += kWaves * kWaveColumns) {
+        const int c = c0 + lane * 8;
+        if (c0 + kWaveColumns <= a.n) grad_chunk<T, kAtOnce, true>(a, token, row, w, dot, c);
+        else grad_chunk<T, kAtOnce, false>(a, token, row, w, dot, c);
       }
       if (a.y == nullptr) continue;
 #pragma unroll
-      for (int o = 32; o > 0; o >>= 1) {
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) dot[j] += __shfl_xor(dot[j], o, 64);
-      }
-      if constexpr (kThreads > 64) {
-        if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-          for (int j = 0; j < kAtOnce; ++j) red[turn][threadIdx.x >> 6][j] = dot[j];
-        }
-        __syncthreads();
-        if (t < kAtOnce && j0 + t < a.r.choices) {
-          const float sum = red[turn][0][t] + red[turn][1][t] + red[turn][2][t] + red[turn][3][t];
-          a.dw[token * a.lddw + j0 + t] = row_of(a.r, token * a.r.choices + j0 + t) >= 0 ? sum : 0.f;
-        }
-        turn ^= 1;   // the next sums go to the other buffer: one barrier between uses
-      } else if (t == 0) {
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j)
-          if (j0 + j < a.r.choices) a.dw[token * a.lddw + j0 + j] = row[j] >= 0 ? dot[j] : 0.f;
+      for (int j = 0; j < kAtOnce; ++j) {
+        const float sum = sum_of_wave(dot[j]);
+        mine = lane == j0 + j ? sum : mine;
       }
     }
+    if (a.y == nullptr) continue;
+    if constexpr (kWaves > 1) {
+      red[turn][wave][lane] = mine;
+      __syncthreads();
+      mine = red[turn][0][lane] + red[turn][1][lane] + red[turn][2][lane] + red[turn][3][lane];
+      turn ^= 1;
+      if (wave != 0) continue;
+    }
+    if (lane < a.r.choices) a.dw[token * a.lddw + lane] = ch.row >= 0 ? mine : 0.f;
   }
 }
 
@@ -401,29 +502,45 @@ template <typename T>
 static hipError_t combine(const ExpertCombineArgs& a, int lanes, int64_t across, int64_t units, hipStream_t s) {
   const dim3 grid(static_cast<uint32_t>(units < kMostGroups ? units : kMostGroups));
   return by_choices(a.r.choices, [&](auto k) {
-    hipLaunchKernelGGL((expert_combine_kernel<T, decltype(k)::value>), grid, dim3(256), 0, s, a, lanes,
+    hipLaunchKernelGGL((expert_combine_narrow_kernel<T, decltype(k)::value>), grid, dim3(256), 0, s, a, lanes,
                        static_cast<int>(across), units);
   });
 }
 
-template <typename T, int kThreads>
+template <typename T>
+static hipError_t combine_wide(const ExpertCombineArgs& a, hipStream_t s) {
+  const int64_t chunks = cdiv(a.n, kWaveColumns), tasks = chunks * a.r.tokens, groups = cdiv(tasks, 4);
+  const dim3 grid(static_cast<uint32_t>(groups < kMostGroups ? groups : kMostGroups));
+  return by_choices(a.r.choices, [&](auto k) {
+    hipLaunchKernelGGL((expert_combine_kernel<T, decltype(k)::value>), grid, dim3(256), 0, s, a,
+                       static_cast<int>(chunks), tasks);
+  });
+}
+
+template <typename T, int kWaves>
 static hipError_t combine_grad(const ExpertCombineGradArgs& a, hipStream_t s) {
-  const int64_t units = cdiv(a.r.tokens, 256 / kThreads);
+  const int64_t units = cdiv(a.r.tokens, 4 / kWaves);
   const dim3 grid(static_cast<uint32_t>((units < kMostGroups ? units : kMostGroups) + a.r.experts * kPadParts));
   return by_choices(a.r.choices, [&](auto k) {
-    hipLaunchKernelGGL((expert_combine_grad_kernel<T, kThreads, decltype(k)::value>), grid, dim3(256), 0, s, a, units);
+    hipLaunchKernelGGL((expert_combine_grad_kernel<T, decltype(k)::value, kWaves>), grid, dim3(256), 0, s, a, units);
   });
 }
 
 hipError_t launch_expert_combine(const ExpertCombineArgs& a, bool bf, int lanes, int64_t across, int64_t units,
                                  hipStream_t s) {
-  return bf ? combine<uint16_t>(a, lanes, across, units, s) : combine<float>(a, lanes, across, units, s);
+  // rows that fill less than half of a wave share it (bf16, 8 choices: 16384 x 128
+  // 8.6 us, 12.0 a wave each; x 256 14.6 both ways; x 384 29.2 and 24.3)
+  if (a.n < kWaveColumns / 2)
+    return bf ? combine<uint16_t>(a, lanes, across, units, s) : combine<float>(a, lanes, across, units, s);
+  return bf ? combine_wide<uint16_t>(a, s) : combine_wide<float>(a, s);
 }
 
 hipError_t launch_expert_combine_grad(const ExpertCombineGradArgs& a, bool bf, hipStream_t s) {
-  // a wave per token up to 1024 columns, else a workgroup
-  if (a.n <= 1024) return bf ? combine_grad<uint16_t, 64>(a, s) : combine_grad<float, 64>(a, s);
-  return bf ? combine_grad<uint16_t, 256>(a, s) : combine_grad<float, 256>(a, s);
+  // one wave per token below 1024 columns (bf16, 8 choices: 16384 x 512 60 us, 78 with
+  // four; x 768 89 and 94; x 1024 117 and 113; 8192 x 2048 131 and 115; 64 x 8192 26
+  // and 11)
+  if (a.n < 1024) return bf ? combine_grad<uint16_t, 1>(a, s) : combine_grad<float, 1>(a, s);
+  return bf ? combine_grad<uint16_t, 4>(a, s) : combine_grad<float, 4>(a, s);
 }
 
 }  // namespace ortho
