@@ -13,9 +13,10 @@ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // ---- the sort ----
 //
 // A stable counting sort.  Counts of each tile's experts meet in memory; then each
-// workgroup adds what it needs of them itself (32 tiles of 128 experts are 16 KB
+// workgroup adds what it needs of them itself (64 tiles of 128 experts are 32 KB
 // from L2, less than another launch takes), and its 16 waves place their pairs, 64 at
-// a time, in order.  One tile needs no other's counts and no first launch.
+// a time, in order.  One tile needs no other's counts and no first launch.  Bound by
+// latency: 16384 x 8 pairs, 128 experts take 2.8 and 6.8 us, 33 x 8 pairs 4.2.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kExperts = 1024;
 
 __device__ __forceinline__ int expert_of(const ExpertSortArgs& a, int pair) {
@@ -50,32 +51,61 @@ __device__ __forceinline__ uint64_t same_lanes(int expert, int bits) {
   return same;
 }
 
+// kBatch x 64 pairs of a wave's `each`, from pair `first` + i0 on: their experts, all
+// loads under way together.
+constexpr int kBatch = 2;
+__device__ __forceinline__ void load_experts(const ExpertSortArgs& a, int first, int i0, int each, int (&e)[kBatch]) {
+#pragma unroll
+  for (int q = 0; q < kBatch; ++q) {
+    const int i = i0 + q * 64 + (threadIdx.x & 63);
+    e[q] = i < each ? expert_of(a, first + i) : -1;
+  }
+}
+
 __global__ __launch_bounds__(kSortThreads) void expert_place_kernel(ExpertSortArgs a) {
   __shared__ int32_t place[kSortWaves][kExperts];   // counts, then next rows, of each wave
   __shared__ int32_t begin[kExperts + 1], total[kExperts];
   __shared__ int32_t sums[kSortWaves];
+  __shared__ int32_t parts[2][kSortThreads];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int each = a.tile / kSortWaves, first = blockIdx.x * a.tile + wave * each;
   for (int e = lane; e < a.experts; e += 64) place[wave][e] = 0;
-  __syncthreads();
-  for (int i = lane; i < each; i += 64) {
-    const int e = expert_of(a, first + i);
-    if (e >= 0) atomicAdd(&place[wave][e], 1);
+  // All tiles' counts of expert t mod 2^k, and those of the tiles before this one: the
+  // tiles are dealt to the 2^(10 - k) threads that have the same expert.
+  int log = 6;
+  while (1 << log < a.experts) ++log;
+  if (a.tiles > 1) {
+    const int e = t & ((1 << log) - 1), group = t >> log, groups = kSortThreads >> log;
+    int all = 0, before = 0;
+    if (e < a.experts) {
+#pragma unroll 8
+      for (int i = group; i < a.tiles; i += groups) {
+        const int c = a.part[(int64_t)i * a.experts + e];
+        all += c;
+        before += i < static_cast<int>(blockIdx.x) ? c : 0;
+      }
+    }
+    parts[0][t] = all;
+    parts[1][t] = before;
   }
   __syncthreads();
-  // Expert t: all tiles' count, and that of the tiles before this one.
+  int es[kBatch];
+  for (int i0 = 0; i0 < each; i0 += kBatch * 64) {
+    load_experts(a, first, i0, each, es);
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q)
+      if (es[q] >= 0) atomicAdd(&place[wave][es[q]], 1);
+  }
+  __syncthreads();
   int all = 0, before = 0;
   if (t < a.experts) {
     if (a.tiles == 1) {
 #pragma unroll
       for (int w = 0; w < kSortWaves; ++w) all += place[w][t];
     } else {
-      const int32_t* const p = a.part + t;
-#pragma unroll 8
-      for (int i = 0; i < a.tiles; ++i) {
-        const int c = p[(int64_t)i * a.experts];
-        all += c;
-        before += i < static_cast<int>(blockIdx.x) ? c : 0;
+      for (int i = t; i < kSortThreads; i += 1 << log) {
+        all += parts[0][i];
+        before += parts[1][i];
       }
     }
   }
@@ -112,18 +142,22 @@ __global__ __launch_bounds__(kSortThreads) void expert_place_kernel(ExpertSortAr
   __syncthreads();
   int bits = 1;
   while (1 << bits < a.experts) ++bits;
-  for (int i = lane; i < each && first + (i & ~63) < a.pairs; i += 64) {
-    const int pair = first + i, e = expert_of(a, pair);
-    const uint64_t same = same_lanes(e < 0 ? 1 << bits : e, bits);
-    const int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
-    const int base = e >= 0 ? place[wave][e] : 0;
-    // (the wave's own row of LDS, whose accesses keep their order)
-    __builtin_amdgcn_wave_barrier();
-    if (e >= 0 && rank == 0) place[wave][e] = base + __popcll(same);
-    __builtin_amdgcn_wave_barrier();
-    if (pair < a.pairs) {
-      a.slot[pair] = e >= 0 ? base + rank : -1;
-      if (a.source && e >= 0) a.source[base + rank] = pair;
+  for (int i0 = 0; i0 < each && first + i0 < a.pairs; i0 += kBatch * 64) {
+    if (each > kBatch * 64) load_experts(a, first, i0, each, es);   // (else they are here)
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int e = es[q], i = i0 + q * 64 + lane, pair = first + i;
+      const uint64_t same = same_lanes(e < 0 ? 1 << bits : e, bits);
+      const int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
+      const int base = e >= 0 ? place[wave][e] : 0;
+      // (the wave's own row of LDS, whose accesses keep their order)
+      __builtin_amdgcn_wave_barrier();
+      if (e >= 0 && rank == 0) place[wave][e] = base + __popcll(same);
+      __builtin_amdgcn_wave_barrier();
+      if (i < each && pair < a.pairs) {
+        a.slot[pair] = e >= 0 ? base + rank : -1;
+        if (a.source && e >= 0) a.source[base + rank] = pair;
+      }
     }
   }
   if (a.source == nullptr) return;

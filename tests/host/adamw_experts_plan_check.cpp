@@ -136,11 +136,13 @@ int main() {
   }
   EXPECT(refused > 300 && taken > 300, "refused %ld, taken %ld", refused, taken);
   // the largest descriptors: extents beyond 64 bits
-  const ortho_mat big = mat(0x10000, 1 << 30, 4, int64_t{1} << 40, ORTHO_F32);
-  const ortho_mat far = mat(0x20000, 1 << 30, 4, int64_t{1} << 40, ORTHO_F32), m = mat(0x30000, 1 << 30, 4, int64_t{1} << 40, ORTHO_F32),
-                  v = mat(0x40000, 1 << 30, 4, int64_t{1} << 40, ORTHO_F32);
+  const ortho_mat big = mat(0x10000, 1 << 30, 4, (int64_t{1} << 32) - 64, ORTHO_F32);
+  const ortho_mat far = mat(0x20000, 1 << 30, 4, (int64_t{1} << 32) - 64, ORTHO_F32), m = mat(0x30000, 1 << 30, 4, (int64_t{1} << 32) - 64, ORTHO_F32),
+                  v = mat(0x40000, 1 << 30, 4, (int64_t{1} << 32) - 64, ORTHO_F32);
   EXPECT(validate_adamw(1, &big, &far, &m, &v, nullptr, nullptr, &h) == ORTHO_OK, "far");
   EXPECT(validate_adamw(1, &big, &far, &m, &far, nullptr, nullptr, &h) == ORTHO_E_LAYOUT, "far");
+  const ortho_mat further = mat(0x20000, 1 << 30, 4, int64_t{1} << 32, ORTHO_F32);
+  EXPECT(validate_adamw(1, &big, &further, &m, &v, nullptr, nullptr, &h) == ORTHO_E_LAYOUT, "further");
   printf("%ld checks, %d failures\n", checks, failures);
   return failures != 0;
 }

@@ -148,7 +148,7 @@ def test_expert_rows_and_workspace():
                 (1 << 30, 1, 1, 1), (1 << 25, 32, 1, 1), ((1 << 30) - 1, 1, 1024, 4096), (1 << 62, 64, 1, 1), (-1, 1, 1, 1)):
         assert rows(*bad) == 0, bad
     assert rows((1 << 30) - 1, 1, 1, 1) == (1 << 30) - 1 and rows((1 << 24) - 1, 64, 1, 1) == 64 * ((1 << 24) - 1)
-    assert ws(0, 1, 1) == 0 and ws(1, 1, 1025) == 0 and ws(4096, 1, 64) == 256 and ws(4097, 1, 64) == 2 * 64 * 4
+    assert ws(0, 1, 1) == 0 and ws(1, 1, 1025) == 0 and ws(2048, 1, 64) == 256 and ws(2049, 1, 64) == 2 * 64 * 4
     assert ws((1 << 30) - 1, 1, 1024) <= 1024 * 1024 * 4
 
 
