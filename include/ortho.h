@@ -457,8 +457,9 @@ typedef struct {
  * States start at zero (any finite scale beside codes of 0).  X, M, V, SM and SV
  * have memory of their own, apart from each other, from those of every other tensor
  * and from every G (else ORTHO_E_LAYOUT; rows between another matrix's rows of the
- * same pitch are apart): a weight that is listed twice is refused.  So is a leading
- * dimension from 2^32 on.
+ * same pitch are apart), from lr_dev, step_dev and factor too: a weight that is
+ * listed twice is refused.  So is a leading dimension from 2^32 on.  (Where the host
+ * has no memory left to look: ORTHO_E_WORKSPACE.)
  *
  * The step uses m and v as computed; only what is kept for the next one is rounded.
  * A block's scale is its largest finite |m| (or sqrt(v)) / 448, at least 2^-126, and

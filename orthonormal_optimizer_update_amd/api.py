@@ -365,7 +365,7 @@ def dion2_step(X, G, M, k: int, mu: float, lr: float, scale: float = 1.0, steps:
 # 8-bit matrices: e4m3 codes with a scale for each block of 128
 # ---------------------------------------------------------------------------
 
-_DTYPES = None
+_DTYPES = _INT32 = None
 
 
 def _mats(*tensors):
@@ -408,7 +408,7 @@ def _call(fn: str, t, *args):
     current."""
     import torch
     device = t.get_device()
-    if device == torch.cuda.current_device():
+    if device == torch._C._cuda_getDevice():   # (t is on a GPU, so there is a current one)
         status = getattr(lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
@@ -578,9 +578,10 @@ _DTYPE = operator.attrgetter("dtype")
 
 
 def _mats_dtypes():
-    global _DTYPES
+    global _DTYPES, _INT32
     if _DTYPES is None:
         import torch
+        _INT32 = torch.int32
         _DTYPES = {torch.float32: ORTHO_F32, torch.bfloat16: ORTHO_BF16,
                    torch.float8_e4m3fn: ORTHO_E4M3, torch.float8_e8m0fnu: ORTHO_E8M0}
 
@@ -714,13 +715,12 @@ def adamw_step(X, G, M, V, lr, step, betas=(0.9, 0.999), eps: float = 1e-8, weig
 # ---------------------------------------------------------------------------
 
 
-def _int32s(t, count, like, what):
-    """Address of an int32 array of `count` elements on like's device."""
-    import torch
-    if t.dtype != torch.int32 or t.numel() != count or not t.is_contiguous():
+def _int32s(t, count, device, what):
+    """Address of an int32 array of `count` elements on the GPU of that number."""
+    if t.dtype is not _INT32 or t.numel() != count or not t.is_contiguous():
         raise ValueError(f"expected {what} as {count} consecutive int32")
-    if t.get_device() != like.get_device():
-        raise ValueError(f"expected {what} on {like.device}, got {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"expected {what} on cuda:{device}, got {t.device}")
     return t.data_ptr()
 
 
@@ -740,8 +740,10 @@ def expert_sort(chosen, experts: int, align: int = 1, slot=None, source=None, of
     import torch
     if chosen.dim() != 2 or not chosen.is_contiguous() or chosen.dtype not in (torch.int32, torch.int64):
         raise ValueError("expected chosen as a contiguous tokens x choices tensor of int32 or int64")
-    if chosen.get_device() < 0:
+    device = chosen.get_device()
+    if device < 0:
         raise ValueError(f"expected tensors on a GPU, got {chosen.device}")
+    _mats_dtypes()
     tokens, choices = chosen.shape
     rows = expert_rows(tokens, choices, experts, align)
 
@@ -754,22 +756,23 @@ def expert_sort(chosen, experts: int, align: int = 1, slot=None, source=None, of
     counts = ints(max(experts, 0)) if counts is None else counts
     if ws is None:
         ws = workspace(expert_sort_workspace_size(tokens, choices, experts), chosen.device)
-    args = (_int32s(slot, tokens * choices, chosen, "slot"), _int32s(source, rows, chosen, "source"),
-            _int32s(offsets, experts + 1, chosen, "offsets"), _int32s(counts, experts, chosen, "counts"))
+    args = (_int32s(slot, tokens * choices, device, "slot"), _int32s(source, rows, device, "source"),
+            _int32s(offsets, experts + 1, device, "offsets"), _int32s(counts, experts, device, "counts"))
     _call("expert_sort", chosen, chosen.data_ptr(), chosen.element_size(), tokens, choices, experts, align,
           *args, *_check_ws(ws, chosen))
     return slot, source, offsets, counts
 
 
-def _slots(slot, tokens, like):
-    if slot.dim() != 2 or slot.shape[0] != tokens:
+def _slots(slot, tokens, device):
+    shape = slot.shape
+    if len(shape) != 2 or shape[0] != tokens:
         raise ValueError(f"expected slot with {tokens} rows")
-    return _int32s(slot, slot.numel(), like, "slot"), slot.shape[1]
+    return _int32s(slot, tokens * shape[1], device, "slot"), shape[1]
 
 
-def _experts(offsets, counts, like):
+def _experts(offsets, counts, device):
     experts = counts.numel()
-    return (_int32s(offsets, experts + 1, like, "offsets"), _int32s(counts, experts, like, "counts"),
+    return (_int32s(offsets, experts + 1, device, "offsets"), _int32s(counts, experts, device, "counts"),
             experts)
 
 
@@ -777,30 +780,32 @@ def expert_gather(X, slot, offsets, counts, Y=None, S=None, SY=None, rows: Optio
     """X's rows to the rows that ``expert_sort`` gave them; see ``expert_gather`` in ortho.h.  X are
     bf16, float32, or e4m3 codes with scales S.  Without Y, Y (and SY) of `rows` rows are allocated.
     Returns (Y, SY)."""
-    import torch
     if Y is None:
         if rows is None:
             raise ValueError("expected Y, or the number of its rows")
+        import torch
         if S is None:
             Y = torch.empty(rows, X.size(1), dtype=X.dtype, device=X.device)
         else:
             Y = fp8_codes(rows, X.size(1), X.device)
     if S is not None and SY is None:
+        import torch
         SY = torch.empty(Y.size(0), S.size(1), dtype=S.dtype, device=X.device)
     x, s, y, sy = _mats(X, S, Y, SY)
-    at, choices = _slots(slot, x.rows, X)
-    _call("expert_gather", X, x, _ref(s), at, choices, *_experts(offsets, counts, X), y, _ref(sy))
+    device = X.get_device()
+    at, choices = _slots(slot, x.rows, device)
+    _call("expert_gather", X, x, _ref(s), at, choices, *_experts(offsets, counts, device), y, _ref(sy))
     return Y, SY
 
 
 def expert_combine(Y, slot, weights=None, add=None, out=None):
     """Rows back to tokens, each token's added with its weights (tokens x choices; ones when None)
     and `add` added; see ``expert_combine`` in ortho.h.  Returns out."""
-    import torch
     if out is None:
+        import torch
         out = torch.empty(slot.shape[0], Y.size(1), dtype=Y.dtype, device=Y.device)
     y, w, ad, o = _mats(Y, weights, add, out)
-    at, choices = _slots(slot, o.rows, Y)
+    at, choices = _slots(slot, o.rows, Y.get_device())
     _call("expert_combine", Y, y, at, choices, _ref(w), _ref(ad), o)
     return out
 
@@ -809,15 +814,17 @@ def expert_combine_backward(dOut, slot, weights, offsets, counts, dY=None, Y=Non
                             rows: Optional[int] = None):
     """Gradient of ``expert_combine``; see ortho.h.  Without dY it is allocated, with Y's rows or
     `rows`.  With Y the weights' gradient is formed too.  Returns (dY, dW), dW None without Y."""
-    import torch
     if dY is None:
         if rows is None and Y is None:
             raise ValueError("expected dY, Y or the number of rows")
+        import torch
         dY = torch.empty(Y.size(0) if rows is None else rows, dOut.size(1), dtype=dOut.dtype, device=dOut.device)
     if Y is not None and dW is None:
+        import torch
         dW = torch.empty(slot.shape, dtype=torch.float32, device=dOut.device)
     d, w, dy, y, dw = _mats(dOut, weights, dY, Y, dW)
-    at, choices = _slots(slot, d.rows, dOut)
-    _call("expert_combine_backward", dOut, d, at, choices, _ref(w), *_experts(offsets, counts, dOut), dy,
+    device = dOut.get_device()
+    at, choices = _slots(slot, d.rows, device)
+    _call("expert_combine_backward", dOut, d, at, choices, _ref(w), *_experts(offsets, counts, device), dy,
           _ref(y), _ref(dw))
     return dY, dW

@@ -724,7 +724,7 @@ ortho_status validate_adamw(int32_t count, const ortho_mat* X, const ortho_mat* 
     if (!near_rows(SM[i]) || !near_rows(SV[i])) return ORTHO_E_LAYOUT;
   }
   Extent few[64], *all = few;
-  const size_t most = 4 * static_cast<size_t>(count) + 2 * codes;
+  const size_t most = 4 * static_cast<size_t>(count) + 2 * codes + 3;
   if (most > sizeof(few) / sizeof(few[0])) {
     all = static_cast<Extent*>(malloc(most * sizeof(Extent)));
     if (all == nullptr) return ORTHO_E_WORKSPACE;
@@ -739,6 +739,9 @@ ortho_status validate_adamw(int32_t count, const ortho_mat* X, const ortho_mat* 
     all[n++] = extent(SM[i], true);
     all[n++] = extent(SV[i], true);
   }
+  const ortho_mat read[] = {array_of(h->lr_dev, 1, 4), array_of(h->step_dev, 1, 8), array_of(h->factor, 1, 4)};
+  for (const ortho_mat& t : read)
+    if (t.data != nullptr) all[n++] = extent(t, false);
   const bool ok = all_apart(all, n);
   if (all != few) free(all);
   return ok ? ORTHO_OK : ORTHO_E_LAYOUT;

@@ -69,6 +69,14 @@ def test_adamw_refuses_far_rows():
         assert adamw([t]) == LAYOUT
 
 
+def test_adamw_refuses_scalars_inside_the_tensors():
+    t = tensor(0, bits=8)
+    for k in ("X", "M", "V", "SM", "SV"):
+        assert adamw([t], hyper(factor=t[k].data + 8)) == LAYOUT
+        assert adamw([t], hyper(lr_dev=t[k].data + 8)) == LAYOUT
+        assert adamw([t], hyper(step_dev=t[k].data - 4)) == LAYOUT
+
+
 def test_adamw_refuses_missing_lists():
     t = tensor(0, bits=8)
     assert adamw([t], scales=False) == NULL
