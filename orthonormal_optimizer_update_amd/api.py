@@ -10,13 +10,12 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
-import operator
 import os
-import struct
 from typing import Optional, Sequence
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libortho.so")
+BINDING_PATH = os.path.join(HERE, "_binding.so")
 
 ORTHO_F32, ORTHO_BF16, ORTHO_E4M3, ORTHO_E8M0 = 0, 1, 2, 3
 FP8_BLOCK = 128
@@ -365,13 +364,17 @@ def dion2_step(X, G, M, k: int, mu: float, lr: float, scale: float = 1.0, steps:
 # 8-bit matrices: e4m3 codes with a scale for each block of 128
 # ---------------------------------------------------------------------------
 
-_DTYPES = _INT32 = None
+_DTYPES = None
 
 
 def _mats(*tensors):
     """Descriptors of 2-D tensors on one GPU (None stays None), which may hold
     8-bit codes and scales."""
-    _mats_dtypes()
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float32: ORTHO_F32, torch.bfloat16: ORTHO_BF16,
+                   torch.float8_e4m3fn: ORTHO_E4M3, torch.float8_e8m0fnu: ORTHO_E8M0}
     dtypes, device, out = _DTYPES, tensors[0].get_device(), []
     if device < 0:
         raise ValueError(f"expected tensors on a GPU, got {tensors[0].device}")
@@ -408,7 +411,7 @@ def _call(fn: str, t, *args):
     current."""
     import torch
     device = t.get_device()
-    if device == torch._C._cuda_getDevice():   # (t is on a GPU, so there is a current one)
+    if device == torch.cuda.current_device():
         status = getattr(lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
@@ -518,143 +521,76 @@ def fp8_matmul(A, SA, B, SB, out=None, add=None, ws=None, out_dtype=None):
 
 # ---------------------------------------------------------------------------
 # AdamW over many tensors, and the gradients' norm
+#
+# From here on the descriptors are made in csrc/binding.cpp: for a list of small
+# tensors, and for calls of a few microseconds, making them here takes longer than
+# the work.
 # ---------------------------------------------------------------------------
 
-
-class MatList:
-    """Descriptors of a list of tensors, for calls over many of them; see ``mats``."""
-
-    __slots__ = ("tensors", "first", "array", "_held", "_pointers")
-
-    def __init__(self, tensors):
-        self.tensors = tuple(tensors)
-        self._held = [t for t in self.tensors if t is not None]
-        if not self._held:
-            raise ValueError("expected at least one tensor")
-        self.first = self._held[0]
-        self._describe()
-
-    def _describe(self):
-        import torch
-        _mats_dtypes()
-        T, held = torch.Tensor, self._held
-        devices = list(map(T.get_device, held))
-        if devices[0] < 0:
-            raise ValueError(f"expected tensors on a GPU, got {self.first.device}")
-        if devices.count(devices[0]) != len(devices):
-            other = next(t for t in held if t.get_device() != devices[0])
-            raise ValueError(f"expected every tensor on {self.first.device}, got {other.device}")
-        self._pointers = pointers = list(map(T.data_ptr, held))
-        # (a tensor often has the shape, strides and type of the one before)
-        fields, last_shape, last_stride, last_dtype, matrix = [], None, None, None, None
-        for at, shape, stride, dtype in zip(pointers, map(T.size, held), map(T.stride, held), map(_DTYPE, held)):
-            if dtype is not last_dtype or stride != last_stride or shape != last_shape:
-                code = _DTYPES.get(dtype)
-                if code is None:
-                    raise ValueError(f"unsupported dtype {dtype}")
-                matrix = (*_rows_of(shape, stride), code)
-                last_shape, last_stride, last_dtype = shape, stride, dtype
-            fields += (at, *matrix)
-        count = len(self.tensors)
-        if len(held) != count:
-            some, fields = iter(fields), []
-            for t in self.tensors:
-                fields += (0,) * 5 if t is None else (next(some), next(some), next(some), next(some), next(some))
-        self.array = (OrthoMat * count)()
-        struct.pack_into("Pqqqi4x" * count, self.array, 0, *fields)
-
-    def __len__(self):
-        return len(self.tensors)
-
-    def current(self):
-        """The descriptors, taken anew if a tensor's memory is another one by now."""
-        import torch
-        if list(map(torch.Tensor.data_ptr, self._held)) != self._pointers:
-            self._describe()
-        return self.array
+_binding = None
 
 
-_DTYPE = operator.attrgetter("dtype")
+def binding():
+    """The compiled binding (once).  Raises if it has not been built."""
+    global _binding
+    if _binding is None:
+        import torch  # noqa: F401  (whose libraries it uses)
+        lib()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
+                               "`python -m orthonormal_optimizer_update_amd.build`")
+        from . import _binding as built
+        _binding = built
+    return _binding
 
 
-def _mats_dtypes():
-    global _DTYPES, _INT32
-    if _DTYPES is None:
-        import torch
-        _INT32 = torch.int32
-        _DTYPES = {torch.float32: ORTHO_F32, torch.bfloat16: ORTHO_BF16,
-                   torch.float8_e4m3fn: ORTHO_E4M3, torch.float8_e8m0fnu: ORTHO_E8M0}
+def _run(name: str, like, *args):
+    """The binding's call on the current stream of like's GPU, with that GPU current."""
+    import torch
+    fn = getattr(binding(), name)
+    device = like.get_device()
+    if device < 0:
+        raise ValueError(f"expected tensors on a GPU, got {like.device}")
+    if device == torch._C._cuda_getDevice():   # (like is on a GPU, so there is a current one)
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    if status != 0:
+        _check(name, status)
 
 
-def _rows_of(shape, strides):
-    """(rows, cols, ld) of a tensor as a matrix: its first dimension by the others; a vector is
-    one row."""
-    if len(shape) < 2:
-        n = shape[0] if shape else 1
-        if n > 1 and strides[0] != 1:
-            raise ValueError("expected unit stride along columns")
-        return 1, n, max(n, 1)
-    rows, cols = shape[0], 1
-    for d in range(len(shape) - 1, 0, -1):
-        if shape[d] != 1 and strides[d] != cols:
-            raise ValueError("expected unit stride along columns")
-        cols *= shape[d]
-    if rows <= 1:
-        return rows, cols, max(cols, 1)
-    if strides[0] < cols:
-        raise ValueError("expected rows that do not overlap")
-    return rows, cols, strides[0]
+def _first(tensors):
+    t = next((t for t in tensors if t is not None), None)
+    if t is None:
+        raise ValueError("expected at least one tensor")
+    return t
 
 
-def mats(tensors: Sequence) -> MatList:
-    """Descriptors of tensors of any shape on one GPU: the first dimension is a matrix's rows, the
-    others its columns, which lie without gaps; a vector is one row; None stands for no matrix.  The
-    calls over many tensors take a list of tensors, or what this returns, which a program may keep
-    for the lists that stay (weights, states).  It holds the tensors; their shapes, types and strides
-    stay as they are."""
-    return MatList(tensors)
-
-
-def _as_mats(tensors) -> MatList:
-    return tensors if isinstance(tensors, MatList) else MatList(tensors)
-
-
-def _scalar_ptr(t, dtype, like, what):
-    """Address of a tensor's one element."""
-    if t.dtype != dtype or t.numel() != 1:
-        raise ValueError(f"expected {what} as one {dtype}, got {t.numel()} of {t.dtype}")
-    if t.get_device() != like.get_device():
-        raise ValueError(f"expected {what} on {like.device}, got {t.device}")
-    return t.data_ptr()
-
-
-def _same_device(lists):
-    for other in lists[1:]:
-        if other.first.get_device() != lists[0].first.get_device():
-            raise ValueError(f"expected every tensor on {lists[0].first.device}, got {other.first.device}")
-        if len(other) != len(lists[0]):
-            raise ValueError(f"expected {len(lists[0])} tensors in each list, got {len(other)}")
+def mats(tensors: Sequence):
+    """The tensors as a tuple, looked over: all on one GPU, of types that the library knows, each a
+    matrix whose rows are its first dimension and whose columns, the other dimensions, lie without
+    gaps (a vector is one row; None stands for no matrix)."""
+    tensors = tuple(tensors)
+    _first(tensors)
+    binding().check(tensors)
+    return tensors
 
 
 def grad_norm_workspace_size(count: int) -> int:
     return int(lib().ortho_grad_norm_workspace_size(count))
 
 
-def grad_norm(G, max_norm: float = float("inf"), out=None, ws=None):
+def grad_norm(G: Sequence, max_norm: float = float("inf"), out=None, ws=None):
     """The norm of all gradients together and the factor that clips it to max_norm (``grad_norm``
     of ortho.h), as the two elements of a float32 tensor: ``out[1:]`` is ``adamw_step``'s factor."""
-    import torch
-    G = _as_mats(G)
-    first = G.first
+    first = _first(G)
     if out is None:
+        import torch
         out = torch.empty(2, dtype=torch.float32, device=first.device)
-    elif out.dtype != torch.float32 or out.numel() != 2 or not out.is_contiguous():
-        raise ValueError("expected out as two float32")
-    elif out.get_device() != first.get_device():
-        raise ValueError(f"expected out on {first.device}, got {out.device}")
     if ws is None:
         ws = workspace(grad_norm_workspace_size(len(G)), first.device)
-    _call("grad_norm", first, len(G), G.current(), max_norm, out.data_ptr(), *_check_ws(ws, first))
+    _run("grad_norm", first, G, max_norm, out, ws)
     return out
 
 
@@ -676,52 +612,22 @@ def adamw_states(X: Sequence, bits: int = 32):
     return codes[::2], codes[1::2], scales[::2], scales[1::2]
 
 
-def adamw_step(X, G, M, V, lr, step, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
-               SM=None, SV=None, seed: Optional[int] = None, factor=None):
-    """One AdamW step in place on all tensors of the lists; see ``adamw_step`` in ortho.h.  M and V
-    are float32, or e4m3 codes with their scales in SM and SV (lists as long as X, None beside float32
-    states).  ``seed``: stochastic rounding of bf16 weights and of codes.
-    ``lr`` and ``step`` may be one-element tensors (float32, int64) on the GPU, read when the kernels
-    run; ``factor`` is one such float32 that multiplies the gradients, NaN to leave all as it was."""
-    import torch
-    lists = [_as_mats(t) for t in (X, G, M, V)]
-    if SM is not None:
-        lists.append(_as_mats(SM))
-    if SV is not None:
-        lists.append(_as_mats(SV))
-    _same_device(lists)
-    first = lists[0].first
-    h = OrthoAdamw(0.0, betas[0], betas[1], eps, weight_decay, 1, 0, 0, None, None, None)
-    if isinstance(lr, torch.Tensor):
-        h.lr_dev = _scalar_ptr(lr, torch.float32, first, "lr")
-    else:
-        h.lr = lr
-    if isinstance(step, torch.Tensor):
-        h.step_dev = _scalar_ptr(step, torch.int64, first, "step")
-    else:
-        h.step = step
-    if seed is not None:
-        h.stochastic, h.seed = 1, seed
-    if factor is not None:
-        h.factor = _scalar_ptr(factor, torch.float32, first, "factor")
-    x, g, m, v = (t.current() for t in lists[:4])
-    sm = lists[4].current() if SM is not None else None
-    sv = lists[-1].current() if SV is not None else None
-    _call("adamw_step", first, len(lists[0]), x, g, m, v, sm, sv, ctypes.byref(h))
+def adamw_step(X: Sequence, G: Sequence, M: Sequence, V: Sequence, lr, step, betas=(0.9, 0.999),
+               eps: float = 1e-8, weight_decay: float = 0.01, SM: Optional[Sequence] = None,
+               SV: Optional[Sequence] = None, seed: Optional[int] = None, factor=None):
+    """One AdamW step in place on all tensors of the lists; see ``adamw_step`` in ortho.h.  Tensors
+    may have any shape whose rows (the first dimension) lie without gaps inside.  M and V are
+    float32, or e4m3 codes with their scales in SM and SV (lists as long as X, None beside float32
+    states).  ``seed``: stochastic rounding of bf16 weights and of codes.  ``lr`` and ``step`` may be
+    one-element tensors (float32, int64) on the GPU, read when the kernels run; ``factor`` is one
+    such float32 that multiplies the gradients, NaN to leave all as it was."""
+    _run("adamw_step", _first(X), X, G, M, V, SM, SV, lr, step, betas[0], betas[1], eps, weight_decay,
+         seed, factor)
 
 
 # ---------------------------------------------------------------------------
 # Tokens by expert
 # ---------------------------------------------------------------------------
-
-
-def _int32s(t, count, device, what):
-    """Address of an int32 array of `count` elements on the GPU of that number."""
-    if t.dtype is not _INT32 or t.numel() != count or not t.is_contiguous():
-        raise ValueError(f"expected {what} as {count} consecutive int32")
-    if t.get_device() != device:
-        raise ValueError(f"expected {what} on cuda:{device}, got {t.device}")
-    return t.data_ptr()
 
 
 def expert_rows(tokens: int, choices: int, experts: int, align: int = 1) -> int:
@@ -737,64 +643,41 @@ def expert_sort(chosen, experts: int, align: int = 1, slot=None, source=None, of
                 ws=None):
     """Rows by expert for the experts that each token chose (tokens x choices, int32 or int64); see
     ``expert_sort`` in ortho.h.  Returns (slot, source, offsets, counts), allocated where None."""
-    import torch
-    if chosen.dim() != 2 or not chosen.is_contiguous() or chosen.dtype not in (torch.int32, torch.int64):
-        raise ValueError("expected chosen as a contiguous tokens x choices tensor of int32 or int64")
-    device = chosen.get_device()
-    if device < 0:
-        raise ValueError(f"expected tensors on a GPU, got {chosen.device}")
-    _mats_dtypes()
-    tokens, choices = chosen.shape
-    rows = expert_rows(tokens, choices, experts, align)
+    if slot is None or source is None or offsets is None or counts is None or ws is None:
+        import torch
+        if chosen.dim() != 2:
+            raise ValueError("expected chosen as a contiguous tokens x choices tensor of int32 or int64")
+        (tokens, choices), device = chosen.shape, chosen.device
 
-    def ints(*shape):
-        return torch.empty(shape, dtype=torch.int32, device=chosen.device)
+        def ints(*shape):
+            return torch.empty(shape, dtype=torch.int32, device=device)
 
-    slot = ints(tokens, choices) if slot is None else slot
-    source = ints(rows) if source is None else source
-    offsets = ints(max(experts, 0) + 1) if offsets is None else offsets
-    counts = ints(max(experts, 0)) if counts is None else counts
-    if ws is None:
-        ws = workspace(expert_sort_workspace_size(tokens, choices, experts), chosen.device)
-    args = (_int32s(slot, tokens * choices, device, "slot"), _int32s(source, rows, device, "source"),
-            _int32s(offsets, experts + 1, device, "offsets"), _int32s(counts, experts, device, "counts"))
-    _call("expert_sort", chosen, chosen.data_ptr(), chosen.element_size(), tokens, choices, experts, align,
-          *args, *_check_ws(ws, chosen))
+        slot = ints(tokens, choices) if slot is None else slot
+        source = ints(expert_rows(tokens, choices, experts, align)) if source is None else source
+        offsets = ints(max(experts, 0) + 1) if offsets is None else offsets
+        counts = ints(max(experts, 0)) if counts is None else counts
+        if ws is None:
+            ws = workspace(expert_sort_workspace_size(tokens, choices, experts), device)
+    _run("expert_sort", chosen, chosen, experts, align, slot, source, offsets, counts, ws)
     return slot, source, offsets, counts
-
-
-def _slots(slot, tokens, device):
-    shape = slot.shape
-    if len(shape) != 2 or shape[0] != tokens:
-        raise ValueError(f"expected slot with {tokens} rows")
-    return _int32s(slot, tokens * shape[1], device, "slot"), shape[1]
-
-
-def _experts(offsets, counts, device):
-    experts = counts.numel()
-    return (_int32s(offsets, experts + 1, device, "offsets"), _int32s(counts, experts, device, "counts"),
-            experts)
 
 
 def expert_gather(X, slot, offsets, counts, Y=None, S=None, SY=None, rows: Optional[int] = None):
     """X's rows to the rows that ``expert_sort`` gave them; see ``expert_gather`` in ortho.h.  X are
     bf16, float32, or e4m3 codes with scales S.  Without Y, Y (and SY) of `rows` rows are allocated.
     Returns (Y, SY)."""
-    if Y is None:
-        if rows is None:
-            raise ValueError("expected Y, or the number of its rows")
+    if Y is None or (SY is None and S is not None):
         import torch
-        if S is None:
-            Y = torch.empty(rows, X.size(1), dtype=X.dtype, device=X.device)
-        else:
-            Y = fp8_codes(rows, X.size(1), X.device)
-    if S is not None and SY is None:
-        import torch
-        SY = torch.empty(Y.size(0), S.size(1), dtype=S.dtype, device=X.device)
-    x, s, y, sy = _mats(X, S, Y, SY)
-    device = X.get_device()
-    at, choices = _slots(slot, x.rows, device)
-    _call("expert_gather", X, x, _ref(s), at, choices, *_experts(offsets, counts, device), y, _ref(sy))
+        if Y is None:
+            if rows is None:
+                raise ValueError("expected Y, or the number of its rows")
+            if S is None:
+                Y = torch.empty(rows, X.size(1), dtype=X.dtype, device=X.device)
+            else:
+                Y = fp8_codes(rows, X.size(1), X.device)
+        if SY is None and S is not None:
+            SY = torch.empty(Y.size(0), S.size(1), dtype=S.dtype, device=X.device)
+    _run("expert_gather", X, X, S, slot, offsets, counts, Y, SY)
     return Y, SY
 
 
@@ -804,9 +687,7 @@ def expert_combine(Y, slot, weights=None, add=None, out=None):
     if out is None:
         import torch
         out = torch.empty(slot.shape[0], Y.size(1), dtype=Y.dtype, device=Y.device)
-    y, w, ad, o = _mats(Y, weights, add, out)
-    at, choices = _slots(slot, o.rows, Y.get_device())
-    _call("expert_combine", Y, y, at, choices, _ref(w), _ref(ad), o)
+    _run("expert_combine", Y, Y, slot, weights, add, out)
     return out
 
 
@@ -814,17 +695,14 @@ def expert_combine_backward(dOut, slot, weights, offsets, counts, dY=None, Y=Non
                             rows: Optional[int] = None):
     """Gradient of ``expert_combine``; see ortho.h.  Without dY it is allocated, with Y's rows or
     `rows`.  With Y the weights' gradient is formed too.  Returns (dY, dW), dW None without Y."""
-    if dY is None:
-        if rows is None and Y is None:
-            raise ValueError("expected dY, Y or the number of rows")
+    if dY is None or (dW is None and Y is not None):
         import torch
-        dY = torch.empty(Y.size(0) if rows is None else rows, dOut.size(1), dtype=dOut.dtype, device=dOut.device)
-    if Y is not None and dW is None:
-        import torch
-        dW = torch.empty(slot.shape, dtype=torch.float32, device=dOut.device)
-    d, w, dy, y, dw = _mats(dOut, weights, dY, Y, dW)
-    device = dOut.get_device()
-    at, choices = _slots(slot, d.rows, device)
-    _call("expert_combine_backward", dOut, d, at, choices, _ref(w), *_experts(offsets, counts, device), dy,
-          _ref(y), _ref(dw))
+        if dY is None:
+            if rows is None and Y is None:
+                raise ValueError("expected dY, Y or the number of rows")
+            dY = torch.empty(Y.size(0) if rows is None else rows, dOut.size(1), dtype=dOut.dtype,
+                             device=dOut.device)
+        if dW is None and Y is not None:
+            dW = torch.empty(slot.shape, dtype=torch.float32, device=dOut.device)
+    _run("expert_combine_backward", dOut, dOut, slot, weights, offsets, counts, dY, Y, dW)
     return dY, dW

@@ -1,9 +1,10 @@
-"""Build libortho.so in-tree with hipcc for gfx950.
+"""Build libortho.so in-tree with hipcc for gfx950, and with the host compiler the
+binding of its calls over many tensors.
 
     python -m orthonormal_optimizer_update_amd.build
 
-Every call recompiles all sources.  The library lands next to this file, where
-the binding loads it from.
+Every call recompiles all sources.  Both land next to this file, where ``api``
+loads them from.
 """
 
 from __future__ import annotations
@@ -13,11 +14,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libortho.so")
+BINDING = os.path.join(HERE, "_binding.so")
 
 SOURCES = ["kernels_gemm.hip", "kernels_aux.hip", "kernels_stream.hip", "kernels_gram_ns.hip",
            "kernels_sweep.hip", "kernels_dion2.hip", "kernels_fp8_gemm.hip", "kernels_fp8_exact.hip",
@@ -55,18 +58,47 @@ def _compile(src: str) -> str:
     return obj
 
 
-def build(verbose: bool = True) -> str:
-    os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(_compile, SOURCES))
-    tmp = LIB + ".tmp"
-    cmd = [hipcc(), "-shared", "-fPIC", "--offload-arch=gfx950", "-o", tmp, *objs]
+def _run(what: str, cmd) -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"link failed: {' '.join(cmd)}\n{res.stderr}")
+        raise RuntimeError(f"{what} failed: {' '.join(cmd)}\n{res.stderr}")
+
+
+def _compile_binding() -> str:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, "binding.o")
+    _run("compile", [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wno-attributes",
+                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                     "-isystem", os.path.join(root, "include"),
+                     "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                     "-isystem", sysconfig.get_paths()["include"],
+                     "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj])
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    tmp = BINDING + ".tmp"
+    _run("link", [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj,
+                  "-L" + HERE, "-lortho", "-Wl,-rpath,$ORIGIN",
+                  "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
+    os.replace(tmp, BINDING)
+
+
+def build(verbose: bool = True) -> str:
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
+        objs = list(ex.map(_compile, SOURCES))
+        binding = binding.result()
+    tmp = LIB + ".tmp"
+    cmd = [hipcc(), "-shared", "-fPIC", "--offload-arch=gfx950", "-o", tmp, *objs]
+    _run("link", cmd)
     os.replace(tmp, LIB)
+    _link_binding(binding)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB} and {BINDING}")
     return LIB
 
 

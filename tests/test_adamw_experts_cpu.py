@@ -245,17 +245,20 @@ def test_expert_combine_backward_refuses(kw, want):
 
 
 def test_tensors_as_matrices():
-    f = lambda x: api._rows_of(x.shape, x.stride())
+    f = api.binding().matrix
     t = torch.zeros(4, 6, 8)
     assert f(torch.zeros(())) == (1, 1, 1) and f(torch.zeros(7)) == (1, 7, 7) and f(t) == (4, 48, 48)
     assert f(t[:, 0]) == (4, 8, 48) and f(t[1:2]) == (1, 48, 48)
     assert f(torch.zeros(5, 3)[:, 1:]) == (5, 2, 3) and f(torch.zeros(8, 1, 3)) == (8, 3, 3)
-    assert f(torch.zeros(6, 1)[::2]) == (3, 1, 2)
+    assert f(torch.zeros(6, 1)[::2]) == (3, 1, 2) and f(torch.zeros(1, 4, 4)[:, :, 0:]) == (1, 16, 16)
+    assert f(torch.zeros(1)[::3]) == (1, 1, 1) and f(torch.zeros(0)) == (1, 0, 1)
     assert f(t[:, :3]) == (4, 24, 48)   # rows with gaps between them
     for bad in (t[:, 1:, :3], t[:, :, ::2], t.transpose(0, 1), torch.zeros(8)[::2], torch.zeros(1, 8).expand(3, 8), torch.zeros(8, 4).t(),
                 t[:, :, :0]):
         with pytest.raises(ValueError):
             f(bad)
+    with pytest.raises(ValueError):
+        f(3)
 
 
 def test_the_binding_wants_a_gpu():
@@ -267,11 +270,13 @@ def test_the_binding_wants_a_gpu():
                  lambda: api.expert_combine_backward(x, torch.zeros(3, 1, dtype=torch.int32), None, x, x, Y=x)):
         with pytest.raises(ValueError, match="GPU"):
             call()
-    for bad in (torch.zeros(4, dtype=torch.int32), torch.zeros(2, 2), torch.zeros(4, 4, dtype=torch.int64)[:, ::2]):
-        with pytest.raises(ValueError, match="chosen"):
-            api.expert_sort(bad, 4)
-    with pytest.raises(ValueError):
-        api.mats([])
+    with pytest.raises(ValueError, match="chosen"):
+        api.expert_sort(torch.zeros(4, dtype=torch.int32), 4)
+    for empty in ([], [None]):
+        with pytest.raises(ValueError, match="at least one"):
+            api.mats(empty)
+        with pytest.raises(ValueError, match="at least one"):
+            api.grad_norm(empty)
     with pytest.raises(ValueError):
         api.adamw_states([x], 16)
 
@@ -281,5 +286,90 @@ def test_states_of_any_shape():
     M_, V, SM, SV = api.adamw_states([torch.zeros(s) for s in shapes], 8)
     for s, m, v, a, b in zip(shapes, M_, V, SM, SV):
         assert m.shape == v.shape == torch.Size(s) and m.dtype == torch.float8_e4m3fn
-        rows, cols, _ = api._rows_of(s, torch.zeros(s).stride())
+        rows, cols, _ = api.binding().matrix(torch.zeros(s))
         assert a.shape == b.shape == (rows, -(-cols // 128)) and bool((a == 1).all())
+
+
+def test_the_binding_counts_its_arguments():
+    b = api.binding()
+    for name in ("check", "matrix", "grad_norm", "adamw_step", "expert_sort", "expert_gather", "expert_combine", "expert_combine_backward"):
+        with pytest.raises(TypeError):
+            getattr(b, name)(*range(30))
+
+
+@pytest.mark.gpu
+class TestRefusalsOfTensors:
+    """What the binding raises for tensors that no descriptor can stand for."""
+
+    def z(self, *shape, dtype=torch.float32):
+        return torch.zeros(*shape, dtype=dtype, device="cuda")
+
+    def test_lists(self):
+        z = self.z
+        a, cpu = [z(3, 4), z(5)], torch.zeros(3, 4)
+        assert len(api.mats(a)) == 2 and api.mats([None, a[0]])[0] is None
+        for bad, what in (([cpu, a[0]], "GPU"), ([a[0], cpu], "GPU"), ([z(3, 4).half()], "dtype"), ([z(4, 3).t()], "stride"),
+                          ([a[0], 3], "tensor"), ([z(1, 3).expand(4, 3)], "overlap")):
+            with pytest.raises(ValueError, match=what):
+                api.mats(bad)
+            with pytest.raises(ValueError):
+                api.grad_norm(bad)
+        M, V, _, _ = api.adamw_states(a)
+        with pytest.raises(ValueError, match="2 tensors in each list, got 1"):
+            api.adamw_step(a, a[:1], M, V, 0.1, 1)
+        with pytest.raises(ValueError, match="lr"):
+            api.adamw_step(a, [z(3, 4), z(5)], M, V, z(2), 1)
+        with pytest.raises(ValueError, match="step"):
+            api.adamw_step(a, [z(3, 4), z(5)], M, V, 0.1, z(1))
+        with pytest.raises(ValueError, match="factor"):
+            api.adamw_step(a, [z(3, 4), z(5)], M, V, 0.1, 1, factor=z(1, dtype=torch.float64))
+        with pytest.raises(ValueError, match="GPU"):
+            api.adamw_step(a, [z(3, 4), z(5)], M, V, 0.1, 1, factor=torch.ones(1))
+        with pytest.raises(TypeError):
+            api.adamw_step(a, [z(3, 4), z(5)], M, V, "0.1", 1)
+        with pytest.raises(TypeError):
+            api.adamw_step(a, [z(3, 4), z(5)], M, V, 0.1, 1.5)
+        with pytest.raises(api.OrthoError) as e:       # a gradient that is not there
+            api.adamw_step(a, [z(3, 4), None], M, V, 0.1, 1)
+        assert e.value.status == NULL
+        for out in (z(3), z(2, dtype=torch.bfloat16), z(4)[::2]):
+            with pytest.raises(ValueError, match="out"):
+                api.grad_norm(a, out=out)
+        with pytest.raises(api.OrthoError) as e:
+            api.grad_norm(a, ws=z(1).expand(1 << 20))
+        assert e.value.status == WS
+        assert not any(bool(t.any()) for t in a)
+
+    def test_rows(self):
+        z = self.z
+        chosen = z(6, 2, dtype=torch.int32)
+        for bad in (z(6, 2), z(6, 4, dtype=torch.int64)[:, ::2], z(12, dtype=torch.int32)):
+            with pytest.raises(ValueError, match="chosen"):
+                api.expert_sort(bad, 4)
+        slot, source, offsets, counts = api.expert_sort(chosen, 4)
+        for kw in (dict(slot=z(6, 2)), dict(slot=z(5, 2, dtype=torch.int32)), dict(source=z(11, dtype=torch.int32)),
+                   dict(offsets=counts), dict(counts=offsets), dict(slot=slot.cpu())):
+            with pytest.raises(ValueError, match="GPU" if "slot" in kw and not kw["slot"].is_cuda else next(iter(kw))):
+                api.expert_sort(chosen, 4, **kw)
+        with pytest.raises(ValueError, match="align"):
+            api.expert_sort(chosen, 4, 1 << 33, slot, source, offsets, counts, z(256, dtype=torch.uint8))
+        X = z(6, 8)
+        with pytest.raises(ValueError, match="rows"):
+            api.expert_gather(X, slot, offsets, counts)
+        with pytest.raises(ValueError, match="slot"):
+            api.expert_gather(X[:5], slot, offsets, counts, rows=12)
+        with pytest.raises(ValueError, match="offsets"):
+            api.expert_gather(X, slot, counts, counts, rows=12)
+        with pytest.raises(ValueError, match="2-D"):
+            api.expert_gather(X, slot, offsets, counts, Y=z(12, 8, 1))
+        Y, _ = api.expert_gather(X, slot, offsets, counts, rows=12)
+        with pytest.raises(api.OrthoError) as e:
+            api.expert_combine(Y, slot, z(6, 3))
+        assert e.value.status == SHAPE
+        with pytest.raises(ValueError, match="slot"):
+            api.expert_combine(Y, slot.long(), out=X)
+        with pytest.raises(ValueError, match="rows"):
+            api.expert_combine_backward(X, slot, None, offsets, counts)
+        with pytest.raises(api.OrthoError) as e:
+            api.expert_combine_backward(X, slot, None, offsets, counts, rows=12, Y=z(11, 8))
+        assert e.value.status == SHAPE
