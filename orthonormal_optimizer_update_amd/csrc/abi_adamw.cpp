@@ -127,7 +127,10 @@ ortho_status adamw_step(int32_t count, const ortho_mat* X, const ortho_mat* G, c
   auto flush_rows = [&]() -> hipError_t {
     if (rows.count == 0) return hipSuccess;
     rows.close();
-    const hipError_t e = launch_adamw_rows(rows.a, stochastic, as_stream(stream));
+    int kind = rows.a.t[0].kind;
+    for (int i = 0; i < rows.count; ++i)
+      if (rows.a.t[i].kind != kind || rows.a.t[i].sm == nullptr) kind = -1;
+    const hipError_t e = launch_adamw_rows(rows.a, kind, stochastic, as_stream(stream));
     rows.clear();
     return e;
   };

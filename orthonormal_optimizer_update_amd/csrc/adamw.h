@@ -86,7 +86,8 @@ struct NormParts {
 };
 
 hipError_t launch_adamw_flat(const AdamwFlat& a, bool stochastic, hipStream_t s);
-hipError_t launch_adamw_rows(const AdamwRows& a, bool stochastic, hipStream_t s);
+// kind: all tensors', if they have one and their states are codes, else -1.
+hipError_t launch_adamw_rows(const AdamwRows& a, int kind, bool stochastic, hipStream_t s);
 hipError_t launch_grad_norm_parts(const NormParts& a, int groups, hipStream_t s);
 hipError_t launch_grad_norm_join(const double* part, int count, double max_norm, float* out, hipStream_t s);
 

@@ -41,11 +41,17 @@ struct Bits {
     key = tensor + kStride * static_cast<uint32_t>(static_cast<uint64_t>(element) >> 32);
     next = key + kStride;
   }
-  // m's seed, and sqrt(v)'s.
-  __device__ __forceinline__ void at(int j, uint32_t& a, uint32_t& b) const {
-    const uint32_t e = low + j;
-    a = mix(e ^ (e < low ? next : key));
-    b = mix(a + kStride);
+  // m's seeds, and sqrt(v)'s, of eight elements.
+  __device__ __forceinline__ void all(uint32_t (&a)[8], uint32_t (&b)[8]) const {
+    if (__any(low > ~0u - 7)) {   // a multiple of 2^32 among them
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] = mix((low + j) ^ (low + j < low ? next : key));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] = mix((low + j) ^ key);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = mix(a[j] + kStride);
   }
   // The weight's: a's low 12 bits, then b's low 4.
   static __device__ __forceinline__ uint32_t weight(uint32_t a, uint32_t b) {
@@ -102,21 +108,31 @@ __device__ __forceinline__ StepScalars step_scalars(const AdamwScalars& h) {
 }
 
 // m and v are fp32 from here to the next step's start; only storage rounds them.
-// Returns sqrt(v).  The weight takes the reciprocal's rounding (one unit in the last
-// place) in place of a division's.
-//
-// kLimited: v beyond fp32's range is its largest number (NaN stays).
-template <bool kLimited>
-__device__ __forceinline__ float adamw(const AdamwScalars& h, const StepScalars& s, float& x, float g, float& m,
-                                       float& v) {
+__device__ __forceinline__ void moments(const AdamwScalars& h, const StepScalars& s, float g, float& m, float& v) {
   g *= s.factor;
   m = h.b1 * m + h.c1 * g;
   v = h.b2 * v + h.c2 * (g * g);
-  if constexpr (kLimited) v = __builtin_elementwise_minimum(v, __FLT_MAX__);
-  const float root = __builtin_sqrtf(v);
-  x = fmaf(-s.size, m * __builtin_amdgcn_rcpf(fmaf(root, s.root, h.eps)), s.keep * x);
-  return root;
 }
+
+// The weight takes the reciprocal's rounding (one unit in the last place) in place of
+// a division's.
+__device__ __forceinline__ float weight(const AdamwScalars& h, const StepScalars& s, float x, float m, float root) {
+  return fmaf(-s.size, m * __builtin_amdgcn_rcpf(fmaf(root, s.root, h.eps)), s.keep * x);
+}
+
+// sqrt(v), correctly rounded, for v = 0, 2^-100 to the largest number, and NaN: two
+// coupled Newton steps for sqrt(v) and 1 / (2 sqrt(v)) from the reciprocal root, and
+// the residual's correction (nine instructions; the library's function, which takes
+// all of fp32, has seventeen).
+__device__ __forceinline__ float root_of(float v) {
+  const float y = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-126f));
+  float g = v * y, h = 0.5f * y;
+  const float r = fmaf(-h, g, 0.5f);
+  g = fmaf(g, r, g);
+  h = fmaf(h, r, h);
+  return fmaf(fmaf(-g, g, v), h, g);
+}
+constexpr uint32_t kLeastRoot = 0x0d800000u;   // 2^-100
 
 // The tensor of a unit; `first` is this lane's.
 template <typename I>
@@ -150,17 +166,17 @@ __device__ __forceinline__ void flat_unit(const AdamwScalars& h, const StepScala
   unpack8(rm, mv);
   unpack8(rv, vv);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) adamw<false>(h, s, xv[j], gv[j], mv[j], vv[j]);
+  for (int j = 0; j < 8; ++j) {
+    moments(h, s, gv[j], mv[j], vv[j]);
+    xv[j] = weight(h, s, xv[j], mv[j], __builtin_sqrtf(vv[j]));
+  }
   if constexpr (kWhole) limit = kUnit;
   if constexpr (kStochastic && sizeof(TX) == 2) {
     const Bits bits(key, base + c);
-    uint32_t seed[8];
+    uint32_t a[8], b[8], seed[8];
+    bits.all(a, b);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t a, b;
-      bits.at(j, a, b);
-      seed[j] = Bits::weight(a, b);
-    }
+    for (int j = 0; j < 8; ++j) seed[j] = Bits::weight(a[j], b[j]);
     store_weights8(x, c, limit, xv, seed);
   } else {
     store8(x, c, limit, xv);
@@ -290,8 +306,9 @@ __device__ __forceinline__ uint2 unit_load_codes(const uint8_t* row, int c, int 
   return u;
 }
 
-// One thread's eight elements of a row.  kWhole: all inside.
-template <typename TX, typename TG, bool kStochastic, bool kWhole>
+// One thread's eight elements of a row.  kWhole: all inside.  kCodes: states in 8
+// bits, else either.
+template <typename TX, typename TG, bool kStochastic, bool kCodes, bool kWhole>
 __device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScalars& s, const RowTensor& t, int row, int c,
                                           uint32_t key) {
   int cols = t.cols;
@@ -302,7 +319,7 @@ __device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScala
   const auto rg = unit_load<kWhole>(g, c, cols);
   const Bits bits(key, static_cast<int64_t>(row) * cols + c);
   uint32_t seed_m[8] = {}, seed_v[8] = {};
-  if (t.sm == nullptr) {
+  if (!kCodes && t.sm == nullptr) {
     float* const m = static_cast<float*>(t.m) + static_cast<uint64_t>(t.ldm) * row;
     float* const v = static_cast<float*>(t.v) + static_cast<uint64_t>(t.ldv) * row;
     const auto rm = unit_load<kWhole>(m, c, cols);
@@ -312,11 +329,11 @@ __device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScala
     unpack8(rm, mv);
     unpack8(rv, vv);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) adamw<false>(h, s, xv[j], gv[j], mv[j], vv[j]);
-    if constexpr (kStochastic && sizeof(TX) == 2) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) bits.at(j, seed_m[j], seed_v[j]);
+    for (int j = 0; j < 8; ++j) {
+      moments(h, s, gv[j], mv[j], vv[j]);
+      xv[j] = weight(h, s, xv[j], mv[j], __builtin_sqrtf(vv[j]));
     }
+    if constexpr (kStochastic && sizeof(TX) == 2) bits.all(seed_m, seed_v);
     if constexpr (kWhole) cols = c + 8;
     store8(m, c, cols, mv);
     store8(v, c, cols, vv);
@@ -331,15 +348,25 @@ __device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScala
     unpack8(rg, gv);
     values8(qm, ms, mv);
     values8(qv, vs, vv);
+    uint32_t least = ~0u;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       vv[j] *= vv[j];
-      vv[j] = adamw<true>(h, s, xv[j], gv[j], mv[j], vv[j]);
+      moments(h, s, gv[j], mv[j], vv[j]);
+      // (what a code can say ends at fp32's largest number; NaN stays)
+      vv[j] = __builtin_elementwise_minimum(vv[j], __FLT_MAX__);
+      least = min(least, __float_as_uint(vv[j]) - 1);   // (0 counts for nothing)
     }
-    if constexpr (kStochastic) {
+    if (__any(least < kLeastRoot - 1)) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) bits.at(j, seed_m[j], seed_v[j]);
+      for (int j = 0; j < 8; ++j) vv[j] = __builtin_sqrtf(vv[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) vv[j] = root_of(vv[j]);
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) xv[j] = weight(h, s, xv[j], mv[j], vv[j]);
+    if constexpr (kStochastic) bits.all(seed_m, seed_v);
     // past the row's end: zeros, which enter no maximum
     if constexpr (!kWhole) {
 #pragma unroll
@@ -367,7 +394,7 @@ __device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScala
   }
 }
 
-template <typename TX, typename TG, bool kStochastic>
+template <typename TX, typename TG, bool kStochastic, bool kCodes>
 __device__ __forceinline__ void row_unit(const AdamwScalars& h, const StepScalars& s, const RowTensor& t, int at,
                                          uint32_t key) {
   const int lanes = t.lanes, across = t.across, down = at / across;
@@ -375,10 +402,11 @@ __device__ __forceinline__ void row_unit(const AdamwScalars& h, const StepScalar
   const int c = (((at - down * across) << lanes) + (threadIdx.x & ((1 << lanes) - 1))) * 8;
   // (the 16 lanes of a block share the row)
   if (row >= t.rows || (c & ~127) >= t.cols) return;
-  if (__all(c + 8 <= t.cols)) row_piece<TX, TG, kStochastic, true>(h, s, t, row, c, key);
-  else row_piece<TX, TG, kStochastic, false>(h, s, t, row, c, key);
+  if (__all(c + 8 <= t.cols)) row_piece<TX, TG, kStochastic, kCodes, true>(h, s, t, row, c, key);
+  else row_piece<TX, TG, kStochastic, kCodes, false>(h, s, t, row, c, key);
 }
 
+// Tensors of any kind.
 template <bool kStochastic>
 __global__ __launch_bounds__(256, 5) void adamw_rows_kernel(AdamwRows a) {
   const int first = a.first[threadIdx.x & (kLanes - 1)];
@@ -390,11 +418,27 @@ __global__ __launch_bounds__(256, 5) void adamw_rows_kernel(AdamwRows a) {
     const int at = unit - a.first[i];
     const uint32_t key = kStochastic ? tensor_key(a.h, s.step, t.index) : 0;
     switch (t.kind) {
-      case 0: row_unit<float, float, kStochastic>(a.h, s, t, at, key); break;
-      case kBf16Weight: row_unit<uint16_t, float, kStochastic>(a.h, s, t, at, key); break;
-      case kBf16Gradient: row_unit<float, uint16_t, kStochastic>(a.h, s, t, at, key); break;
-      default: row_unit<uint16_t, uint16_t, kStochastic>(a.h, s, t, at, key);
+      case 0: row_unit<float, float, kStochastic, false>(a.h, s, t, at, key); break;
+      case kBf16Weight: row_unit<uint16_t, float, kStochastic, false>(a.h, s, t, at, key); break;
+      case kBf16Gradient: row_unit<float, uint16_t, kStochastic, false>(a.h, s, t, at, key); break;
+      default: row_unit<uint16_t, uint16_t, kStochastic, false>(a.h, s, t, at, key);
     }
+  }
+}
+
+// Tensors with states in 8 bits, all of one kind.  Bound by HBM to nearest: 67 million
+// weights with gradients in bf16 125 us (5.5 TB/s), in fp32 193 (5.6); stochastically
+// the vector unit has as much to do in bf16 (150 us, 160 in the kernel above).
+template <typename TX, typename TG, bool kStochastic>
+__global__ __launch_bounds__(256, 5) void adamw_codes_kernel(AdamwRows a) {
+  const int first = a.first[threadIdx.x & (kLanes - 1)];
+  const StepScalars s = step_scalars(a.h);
+  if (s.skip) return;
+  for (int unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
+    const int i = tensor_of(first, unit);
+    const RowTensor& t = a.t[i];
+    const uint32_t key = kStochastic ? tensor_key(a.h, s.step, t.index) : 0;
+    row_unit<TX, TG, kStochastic, true>(a.h, s, t, unit - a.first[i], key);
   }
 }
 
@@ -508,10 +552,23 @@ hipError_t launch_adamw_flat(const AdamwFlat& a, bool stochastic, hipStream_t s)
   return hipGetLastError();
 }
 
-hipError_t launch_adamw_rows(const AdamwRows& a, bool stochastic, hipStream_t s) {
-  if (stochastic) hipLaunchKernelGGL(adamw_rows_kernel<true>, grid_of(a.units), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(adamw_rows_kernel<false>, grid_of(a.units), dim3(256), 0, s, a);
+template <bool kStochastic>
+static hipError_t rows(const AdamwRows& a, int kind, hipStream_t s) {
+  const dim3 grid = grid_of(a.units), block(256);
+  switch (kind) {
+    case 0: hipLaunchKernelGGL((adamw_codes_kernel<float, float, kStochastic>), grid, block, 0, s, a); break;
+    case kBf16Weight: hipLaunchKernelGGL((adamw_codes_kernel<uint16_t, float, kStochastic>), grid, block, 0, s, a); break;
+    case kBf16Gradient: hipLaunchKernelGGL((adamw_codes_kernel<float, uint16_t, kStochastic>), grid, block, 0, s, a); break;
+    case kBf16Weight | kBf16Gradient:
+      hipLaunchKernelGGL((adamw_codes_kernel<uint16_t, uint16_t, kStochastic>), grid, block, 0, s, a);
+      break;
+    default: hipLaunchKernelGGL(adamw_rows_kernel<kStochastic>, grid, block, 0, s, a);
+  }
   return hipGetLastError();
+}
+
+hipError_t launch_adamw_rows(const AdamwRows& a, int kind, bool stochastic, hipStream_t s) {
+  return stochastic ? rows<true>(a, kind, s) : rows<false>(a, kind, s);
 }
 
 hipError_t launch_grad_norm_parts(const NormParts& a, int groups, hipStream_t s) {
