@@ -22,14 +22,14 @@ def mix(h):
     return h ^ (h >> np.uint32(16))
 
 
-def random_bits(seed, step, tensor, rows, cols):
-    """(weight's 16 bits, m's 20, sqrt(v)'s 20) of a tensor's elements."""
+def random_bits(seed, step, tensor, rows, cols, first_row=0):
+    """(weight's 16 bits, m's 20, sqrt(v)'s 20) of a tensor's elements in `rows` rows."""
     with np.errstate(over="ignore"):
         gold = np.uint32(0x9E3779B9)
         key = mix(np.array([seed & 0xFFFFFFFF], dtype=np.uint32))
         for word in (seed >> 32, step & 0xFFFFFFFF, step >> 32, tensor):
             key = mix(key ^ mix(np.array([word], dtype=np.uint32) + gold))
-        e = np.arange(rows * cols, dtype=np.uint64)
+        e = np.arange(rows * cols, dtype=np.uint64) + np.uint64(first_row * cols)
         low, high = (e & np.uint64(0xFFFFFFFF)).astype(np.uint32), (e >> np.uint64(32)).astype(np.uint32)
         a = mix(low ^ (key + gold * high))
         b = mix(a + gold)
@@ -104,9 +104,12 @@ def check_codes(codes, scales, value, err, bits, least):
     s = scales.cpu().double()
     top, low, high = tops(value), tops((value.abs() - err).clamp(min=0)), tops(value.abs() + err)
     some = top > 0
+    # a value that the error reaches zero from may be zero in 32 bits (a square below 2^-149 is, and the
+    # bound of v' counts it), and where this holds for all of a block, its scale may be 1 as well
+    some &= ~((low == 0) & (s == 1))
     assert bool((s[some] >= (low / TOP * (1 - 2 * U)).clamp(min=2.0 ** -126)[some]).all())
     assert bool((s[some] <= (high / TOP * (1 + 2 * U)).clamp(min=2.0 ** -126)[some]).all())
-    assert bool((s[~some] == 1).all())
+    assert bool((s[top == 0] == 1).all())
     got = e4m3_values(codes)
     finite = torch.isfinite(value)
     assert bool(torch.isnan(got[~finite]).all())

@@ -218,6 +218,23 @@ def test_squares_beyond_fp32_do_not_poison_8_bit_states():
                                                                   bool((x[0, :200] == 2).all()))
 
 
+@pytest.mark.parametrize("std", [1e-22, 1e-20, 1e-18, 1e-16, 1e-13, 1e13, 1e17])
+@pytest.mark.parametrize("seed", [None, 6])
+def test_gradients_at_the_ends_of_the_range(std, seed):
+    """Squares around fp32's smallest numbers, where the root is formed another way, and near its largest."""
+    gen = torch.Generator().manual_seed(12)
+    ts = [Tensor(gen, 4, 1537, F, F, bits) for bits in (32, 8)]
+    for t in ts:
+        t.x.mul_(std)
+        t.g.mul_(std * 1e3)
+        t.m.zero_() if t.bits == 32 else t.m.view(torch.uint8).zero_()
+        t.v.zero_() if t.bits == 32 else t.v.view(torch.uint8).zero_()
+        t.g[1, 5] = 1e-3        # (one block with a gradient of ordinary size)
+        for i, (memory, view, _) in enumerate(t.gaps):
+            t.gaps[i] = (memory, view, memory.clone())
+    step_and_check(ts, seed=seed)
+
+
 def test_a_small_root_never_becomes_zero():
     """Beside a large neighbour sqrt(v) is far below the least code, and gets it all the same."""
     for seed in (None, 1, 2):
@@ -423,7 +440,7 @@ def test_offsets_beyond_32_bits():
     assert api.grad_norm([g])[0].item() == pytest.approx(5 ** 0.5)
     api.adamw_step([x], [g], [m], [v], 0.5, 1)
     assert bool((x.flatten()[-5:] == -0.5).all()) and int((x != 0).sum()) == 5
-    del x, m, v
+    del x, g, m, v
     wide = torch.zeros(3, 1 << 30, dtype=BF, device="cuda")
     for bits in (32, 8):
         X = [wide[:, :200]]
@@ -431,3 +448,47 @@ def test_offsets_beyond_32_bits():
         wide.zero_()
         api.adamw_step(X, [torch.ones(3, 200, dtype=BF, device="cuda")], M, V, 0.5, 1, SM=SM, SV=SV, weight_decay=0.0)
         assert bool((wide[:, :200] == -0.5).all()) and not bool(wide[:, 200:400].any())
+
+
+def test_random_bits_of_more_than_2_to_the_32_elements():
+    """Rows around element 2^32, which lies among a thread's eight."""
+    cols, rows, seed, t = 8191, (1 << 32) // 8191 + 2, 99, 5
+    first = rows - 3
+    X, G = (torch.zeros(rows, cols, dtype=BF, device="cuda") for _ in range(2))
+    gen = torch.Generator().manual_seed(13)
+    x, g = values(gen, 3, cols, 0.02).to(BF), values(gen, 3, cols, 1e-3).to(BF)
+    X[first:].copy_(x)
+    G[first:].copy_(g)
+    M, V, SM, SV = api.adamw_states([X], 8)
+    api.adamw_step([X], [G], M, V, H["lr"], t, betas=H["betas"], eps=H["eps"], weight_decay=H["weight_decay"], SM=SM, SV=SV, seed=seed)
+    zero = torch.zeros(3, cols, dtype=torch.float64)
+    (xn, ex), (mn, em), (vn, ev) = R.step(x.double(), g.double(), zero, zero, H["lr"], t, H["betas"], H["eps"], H["weight_decay"])
+    bits = R.random_bits(seed, t, 0, 3, cols, first)
+    assert R.between(X[first:].cpu().double(), R.round_bf16(xn - ex, bits[0]), R.round_bf16(xn + ex, bits[0]))
+    R.check_codes(M[0][first:], SM[0][first:], mn, em, bits[1], False)
+    root, er = vn.sqrt(), (vn + ev).sqrt() - (vn - ev).clamp(min=0).sqrt()
+    R.check_codes(V[0][first:], SV[0][first:], root, er + R.U * root, bits[2], True)
+    assert not bool(X[:first].any())
+
+
+def test_two_graphs_that_share_a_workspace():
+    """Replayed one after the other, as a program may that runs them on one stream."""
+    ws = api.workspace(api.grad_norm_workspace_size(100), "cuda")
+    gs = [[torch.randn(3, 1000 + i, device="cuda") for i in range(n)] for n in (100, 3)]
+    outs, graphs = [torch.zeros(2, device="cuda") for _ in gs], []
+    for g, out in zip(gs, outs):
+        api.grad_norm(g, 1.0, out=out, ws=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            api.grad_norm(g, 1.0, out=out, ws=ws)
+        graphs.append(graph)
+    for k in range(4):
+        for g in gs:
+            for t in g:
+                t.mul_(1.5)
+        for graph in (graphs if k % 2 else graphs[::-1]):
+            graph.replay()
+        torch.cuda.synchronize()
+        for g, out in zip(gs, outs):
+            assert torch.equal(out, api.grad_norm(g, 1.0))

@@ -237,6 +237,45 @@ def test_one_expert_takes_all_and_the_same_twice():
     assert torch.equal(out, x)
 
 
+@pytest.mark.parametrize("n", [40, 300, 2001])
+def test_tokens_that_all_stay_out(n):
+    chosen = torch.full((33, 3), -1, dtype=torch.int64, device="cuda")
+    slot, source, offsets, counts = api.expert_sort(chosen, 6, 16)
+    assert not bool(counts.any()) and not bool(offsets.any()) and bool((source == -1).all()) and bool((slot == -1).all())
+    x, rows = torch.randn(33, n, dtype=BF, device="cuda"), source.numel()
+    y, _ = api.expert_gather(x, slot, offsets, counts, torch.full((rows, n), 5.0, dtype=BF, device="cuda"))
+    assert bool((y == 5).all())
+    y.fill_(float("nan"))
+    w = torch.full((33, 3), float("inf"), device="cuda")
+    assert not bool(api.expert_combine(y, slot, w).any()) and torch.equal(api.expert_combine(y, slot, w, x), x)
+    dy, dw = api.expert_combine_backward(x, slot, w, offsets, counts, torch.full_like(y, 5.0), Y=y)
+    assert bool((dy == 5).all()) and not bool(dw.any())
+
+
+def test_two_graphs_that_share_a_workspace():
+    cases = [(3000, 4, 60, 16), (900, 8, 7, 1)]
+    ws = api.workspace(max(api.expert_sort_workspace_size(t, k, e) for t, k, e, _ in cases), "cuda")
+    gen, graphs, held = torch.Generator(device="cuda").manual_seed(2), [], []
+    for t, k, e, align in cases:
+        chosen = torch.randint(0, e, (t, k), generator=gen, device="cuda")
+        ints = api.expert_sort(chosen, e, align, ws=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            api.expert_sort(chosen, e, align, *ints, ws=ws)
+        graphs.append(graph)
+        held.append((chosen, ints, e, align))
+    for i in range(4):
+        for chosen, _, e, _ in held:
+            chosen.copy_(torch.randint(-1, e, chosen.shape, generator=gen, device="cuda"))
+        for graph in (graphs if i % 2 else graphs[::-1]):
+            graph.replay()
+        torch.cuda.synchronize()
+        for chosen, ints, e, align in held:
+            for a, b in zip(ints, api.expert_sort(chosen, e, align)):
+                assert torch.equal(a, b)
+
+
 def test_rows_beyond_32_bits():
     """Rows of the sorted matrix more than 2^32 bytes in."""
     n, rows = 1 << 16, (1 << 15) + (1 << 10)
