@@ -429,7 +429,7 @@ ortho_status grad_norm(int32_t count, const ortho_mat* G, double max_norm, float
 typedef struct {
   double lr;
   double beta1, beta2;     /* in [0, 1) */
-  double eps;              /* >= 2^-126 */
+  double eps;              /* 2^-126 to 2^100 */
   double weight_decay;     /* >= 0 */
   int64_t step;            /* t of the bias corrections: 1 at the first step */
   uint64_t seed;           /* of the stochastic rounding */

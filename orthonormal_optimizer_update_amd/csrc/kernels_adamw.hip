@@ -115,7 +115,8 @@ __device__ __forceinline__ void moments(const AdamwScalars& h, const StepScalars
 }
 
 // The weight takes the reciprocal's rounding (one unit in the last place) in place of
-// a division's.
+// a division's.  (eps and the root's bounds keep the divisor from 2^-126 to 2^126,
+// where the instruction's result is a normal number.)
 __device__ __forceinline__ float weight(const AdamwScalars& h, const StepScalars& s, float x, float m, float root) {
   return fmaf(-s.size, m * __builtin_amdgcn_rcpf(fmaf(root, s.root, h.eps)), s.keep * x);
 }

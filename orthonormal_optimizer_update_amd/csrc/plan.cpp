@@ -701,7 +701,7 @@ ortho_status validate_adamw(int32_t count, const ortho_mat* X, const ortho_mat* 
   const float eps = static_cast<float>(h->eps);
   if (!finite(static_cast<float>(h->lr)) || !finite(static_cast<float>(h->weight_decay)) ||
       !(h->weight_decay >= 0.0) || !(h->beta1 >= 0.0 && h->beta1 < 1.0) ||
-      !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !finite(eps) || !(eps >= FLT_MIN) ||
+      !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !(eps >= FLT_MIN && eps <= 0x1p100f) ||
       (h->step < 1 && h->step_dev == nullptr))
     return ORTHO_E_PARAM;
   size_t codes = 0;

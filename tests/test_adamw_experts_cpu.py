@@ -109,6 +109,11 @@ def test_adamw_takes_parameters(kw):
     assert adamw([tensor(0, **OVERLAP)], hyper(**kw)) == LAYOUT   # (gets as far as the overlap)
 
 
+@pytest.mark.parametrize("eps,status", [(2.0 ** 100, LAYOUT), (1.01 * 2.0 ** 100, PARAM), (1e38, PARAM)])
+def test_adamw_largest_eps(eps, status):
+    assert adamw([tensor(0, **OVERLAP)], hyper(eps=eps)) == status
+
+
 def test_adamw_refuses_too_many_elements():
     n = 1 << 30
     assert adamw([tensor(0, rows=n, cols=1025)]) == SHAPE
