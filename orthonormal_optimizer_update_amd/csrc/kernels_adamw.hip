@@ -121,19 +121,52 @@ __device__ __forceinline__ float weight(const AdamwScalars& h, const StepScalars
   return fmaf(-s.size, m * __builtin_amdgcn_rcpf(fmaf(root, s.root, h.eps)), s.keep * x);
 }
 
-// sqrt(v), correctly rounded, for v = 0, 2^-100 to the largest number, and NaN: two
-// coupled Newton steps for sqrt(v) and 1 / (2 sqrt(v)) from the reciprocal root, and
-// the residual's correction (nine instructions; the library's function, which takes
-// all of fp32, has seventeen).
+// sqrt(v), correctly rounded, for v = 2^-100 to the largest number and NaN, with kZero
+// for 0 too: coupled Newton steps for sqrt(v) and 1 / (2 sqrt(v)) from the reciprocal
+// root, and the residual's correction (eight instructions; the library's function,
+// which takes all of fp32, has seventeen).
+template <bool kZero>
 __device__ __forceinline__ float root_of(float v) {
-  const float y = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-126f));
+  const uint32_t bits = __float_as_uint(v);
+  const float y = __builtin_amdgcn_rsqf(__uint_as_float(kZero ? max(bits, 0x00800000u) : bits));
   float g = v * y, h = 0.5f * y;
   const float r = fmaf(-h, g, 0.5f);
   g = fmaf(g, r, g);
   h = fmaf(h, r, h);
   return fmaf(fmaf(-g, g, v), h, g);
 }
-constexpr uint32_t kLeastRoot = 0x0d800000u;   // 2^-100
+constexpr uint32_t kLeastRoot = 0x0d800000u, kInfinity = 0x7f800000u;   // 2^-100's bits
+
+// The roots of eight values that are not negative; what a code can say ends at fp32's
+// largest number (NaN stays).  Most waves hold no zero and nothing tiny or infinite,
+// and one look tells.  Returns whether there may be zeros.
+__device__ __forceinline__ bool roots8(float (&v)[8]) {
+  uint32_t low = ~0u, high = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    low = min(low, __float_as_uint(v[j]));
+    high = max(high, __float_as_uint(v[j]));
+  }
+  if (!__any(low < kLeastRoot || high >= kInfinity)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = root_of<false>(v[j]);
+    return false;
+  }
+  uint32_t least = ~0u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = __builtin_elementwise_minimum(v[j], __FLT_MAX__);
+    least = min(least, __float_as_uint(v[j]) - 1);   // (0 counts for nothing)
+  }
+  if (__any(least < kLeastRoot - 1)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __builtin_sqrtf(v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = root_of<true>(v[j]);
+  }
+  return true;
+}
 
 // The tensor of a unit; `first` is this lane's.
 template <typename I>
@@ -197,6 +230,13 @@ __device__ __forceinline__ void flat_by_kind(const AdamwScalars& h, const StepSc
   }
 }
 
+// Tensors of consecutive elements, states in 32 bits.  Bound by HBM: 470 million weights
+// and gradients in bf16 take 1.89 ms (22 bytes each, 5.5 TB/s; a copy reaches 5.1).
+// Every element is touched once, so nothing is staged: each thread has its 8 elements'
+// loads under way together, and a new workgroup per unit keeps memory busier than
+// workgroups that stay (604 million with clipping 2.72 ms; 2.94 with 2048 that walk
+// the units; 2.73 and 2.75 with two and four units next to each other per workgroup).
+// 100352 fp32 weights in 49 tensors take 4.0 us, a launch's latency.
 template <bool kStochastic>
 __global__ __launch_bounds__(256) void adamw_flat_kernel(AdamwFlat a) {
   const int first = a.first[threadIdx.x & (kLanes - 1)];
@@ -249,37 +289,59 @@ __device__ __forceinline__ float max_of_16_lanes(float v) {
   return __builtin_elementwise_maximum(v, rotated<1>(v));
 }
 
+// 1 / s for s from 2^-126 to 2^126: the reciprocal instruction's result and one
+// correction by the residual, which is the correctly rounded quotient for every such s
+// (all of them tried on the chip).
+__device__ __forceinline__ float inverse(float s) {
+  const float y = __builtin_amdgcn_rcpf(s);
+  return fmaf(fmaf(-s, y, 1.f), y, y);
+}
+
 // Codes of a block's eight elements here, the 16 lanes of a block together.  A block
 // with an infinity or NaN (its largest magnitude says so) looks at its finite
 // elements once more.
+// kPositive: no element is below 0; those above 0 get no code of 0, and `zeros` says
+// whether there may be others.
 template <bool kStochastic, bool kPositive>
-__device__ __forceinline__ uint2 to_codes8(const float (&v)[8], const uint32_t (&seed)[8], float& scale) {
+__device__ __forceinline__ uint2 to_codes8(const float (&v)[8], const uint32_t (&seed)[8], bool zeros, float& scale) {
   float top = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) top = __builtin_elementwise_maximum(top, kPositive ? v[j] : __builtin_fabsf(v[j]));
   top = max_of_16_lanes(top);
-  const bool finite = top < __builtin_inff();
-  if (!finite) {
+  uint32_t lost = 0;   // bit j: element j is no number
+  if (!(top < __builtin_inff())) {
     top = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_abs(v[j]));
+    for (int j = 0; j < 8; ++j) {
+      const bool number = __builtin_fabsf(v[j]) < __builtin_inff();
+      top = fmaxf(top, number ? __builtin_fabsf(v[j]) : 0.f);
+      lost |= number ? 0u : 1u << j;
+    }
     top = max_of_16_lanes(top);
   }
   const float s = fmaxf(top * (1.f / kFp8Top), 0x1p-126f);
   scale = top == 0.f ? 1.f : s;
-  const float f = 1.f / scale;
+  const float f = inverse(scale);
   float q[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    q[j] = v[j] * f;
-    // (the largest may come out a rounding above 448)
-    if constexpr (kPositive) q[j] = __builtin_amdgcn_fmed3f(q[j], q[j] > 0.f ? 0x1p-9f : 0.f, kFp8Top);
-    else if constexpr (kStochastic) q[j] = __builtin_amdgcn_fmed3f(q[j], -kFp8Top, kFp8Top);
+  for (int j = 0; j < 8; ++j) q[j] = v[j] * f;
+  // (the largest may come out a rounding above 448)
+  if constexpr (kPositive) {
+    if (zeros) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = __builtin_amdgcn_fmed3f(q[j], v[j] > 0.f ? 0x1p-9f : 0.f, kFp8Top);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = __builtin_amdgcn_fmed3f(q[j], 0x1p-9f, kFp8Top);
+    }
+  } else if constexpr (kStochastic) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = __builtin_amdgcn_fmed3f(q[j], -kFp8Top, kFp8Top);
   }
-  if (!finite) {
+  if (lost != 0) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (!(__builtin_fabsf(v[j]) < __builtin_inff())) q[j] = __builtin_nanf("");
+      if (lost >> j & 1) q[j] = __builtin_nanf("");
   }
   if constexpr (kStochastic) {
     uint32_t u[2];
@@ -307,22 +369,28 @@ __device__ __forceinline__ uint2 unit_load_codes(const uint8_t* row, int c, int 
   return u;
 }
 
+// (pitch and row as they are, unsigned: the address takes one multiplication)
+template <typename T>
+__device__ __forceinline__ T* row_at(void* base, uint32_t ld, uint32_t row) {
+  return static_cast<T*>(base) + static_cast<uint64_t>(ld) * row;
+}
+
 // One thread's eight elements of a row.  kWhole: all inside.  kCodes: states in 8
 // bits, else either.
 template <typename TX, typename TG, bool kStochastic, bool kCodes, bool kWhole>
-__device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScalars& s, const RowTensor& t, int row, int c,
+__device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScalars& s, const RowTensor& t, uint32_t row, int c,
                                           uint32_t key) {
   int cols = t.cols;
-  TX* const x = static_cast<TX*>(t.x) + static_cast<uint64_t>(t.ldx) * row;
-  const TG* const g = static_cast<const TG*>(t.g) + static_cast<uint64_t>(t.ldg) * row;
+  TX* const x = row_at<TX>(t.x, t.ldx, row);
+  const TG* const g = row_at<const TG>(const_cast<void*>(t.g), t.ldg, row);
   float xv[8], gv[8], mv[8], vv[8];
   const auto rx = unit_load<kWhole>(x, c, cols);
   const auto rg = unit_load<kWhole>(g, c, cols);
-  const Bits bits(key, static_cast<int64_t>(row) * cols + c);
+  const Bits bits(key, static_cast<uint64_t>(row) * static_cast<uint32_t>(cols) + c);
   uint32_t seed_m[8] = {}, seed_v[8] = {};
   if (!kCodes && t.sm == nullptr) {
-    float* const m = static_cast<float*>(t.m) + static_cast<uint64_t>(t.ldm) * row;
-    float* const v = static_cast<float*>(t.v) + static_cast<uint64_t>(t.ldv) * row;
+    float* const m = row_at<float>(t.m, t.ldm, row);
+    float* const v = row_at<float>(t.v, t.ldv, row);
     const auto rm = unit_load<kWhole>(m, c, cols);
     const auto rv = unit_load<kWhole>(v, c, cols);
     unpack8(rx, xv);
@@ -339,32 +407,22 @@ __device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScala
     store8(m, c, cols, mv);
     store8(v, c, cols, vv);
   } else {
-    uint8_t* const m = static_cast<uint8_t*>(t.m) + static_cast<uint64_t>(t.ldm) * row;
-    uint8_t* const v = static_cast<uint8_t*>(t.v) + static_cast<uint64_t>(t.ldv) * row;
-    float* const sm = t.sm + static_cast<uint64_t>(t.ldsm) * row + (c >> 7);
-    float* const sv = t.sv + static_cast<uint64_t>(t.ldsv) * row + (c >> 7);
+    uint8_t* const m = row_at<uint8_t>(t.m, t.ldm, row);
+    uint8_t* const v = row_at<uint8_t>(t.v, t.ldv, row);
+    float* const sm = row_at<float>(t.sm, t.ldsm, row) + (c >> 7);
+    float* const sv = row_at<float>(t.sv, t.ldsv, row) + (c >> 7);
     const uint2 qm = unit_load_codes<kWhole>(m, c, cols), qv = unit_load_codes<kWhole>(v, c, cols);
     const float ms = *sm, vs = *sv;
     unpack8(rx, xv);
     unpack8(rg, gv);
     values8(qm, ms, mv);
     values8(qv, vs, vv);
-    uint32_t least = ~0u;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       vv[j] *= vv[j];
       moments(h, s, gv[j], mv[j], vv[j]);
-      // (what a code can say ends at fp32's largest number; NaN stays)
-      vv[j] = __builtin_elementwise_minimum(vv[j], __FLT_MAX__);
-      least = min(least, __float_as_uint(vv[j]) - 1);   // (0 counts for nothing)
     }
-    if (__any(least < kLeastRoot - 1)) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) vv[j] = __builtin_sqrtf(vv[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) vv[j] = root_of(vv[j]);
-    }
+    const bool zeros = roots8(vv);
 #pragma unroll
     for (int j = 0; j < 8; ++j) xv[j] = weight(h, s, xv[j], mv[j], vv[j]);
     if constexpr (kStochastic) bits.all(seed_m, seed_v);
@@ -375,8 +433,8 @@ __device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScala
         if (c + j >= cols) mv[j] = vv[j] = 0.f;
     }
     float ms2, vs2;
-    const uint2 um = to_codes8<kStochastic, false>(mv, seed_m, ms2);
-    const uint2 uv = to_codes8<kStochastic, true>(vv, seed_v, vs2);
+    const uint2 um = to_codes8<kStochastic, false>(mv, seed_m, false, ms2);
+    const uint2 uv = to_codes8<kStochastic, true>(vv, seed_v, zeros, vs2);
     if constexpr (kWhole) cols = c + 8;
     store_codes8(m, c, cols, um);
     store_codes8(v, c, cols, uv);
@@ -407,7 +465,10 @@ __device__ __forceinline__ void row_unit(const AdamwScalars& h, const StepScalar
   else row_piece<TX, TG, kStochastic, kCodes, false>(h, s, t, row, c, key);
 }
 
-// Tensors of any kind.
+// Tensors of any kind: rows of their own pitch, or states in 8 bits beside other kinds.
+// The states' codes are formed where they lie: 16 lanes hold a block of 128, whose
+// maximum they find with four rotations of the lanes, so m and sqrt(v) meet memory only
+// as codes.  67 million bf16 weights with codes, stochastically, 152 us (4.5 TB/s).
 template <bool kStochastic>
 __global__ __launch_bounds__(256, 5) void adamw_rows_kernel(AdamwRows a) {
   const int first = a.first[threadIdx.x & (kLanes - 1)];
@@ -428,10 +489,12 @@ __global__ __launch_bounds__(256, 5) void adamw_rows_kernel(AdamwRows a) {
 }
 
 // Tensors with states in 8 bits, all of one kind.  Bound by HBM to nearest: 67 million
-// weights with gradients in bf16 125 us (5.5 TB/s), in fp32 193 (5.6); stochastically
-// the vector unit has as much to do in bf16 (150 us, 160 in the kernel above).
+// weights with gradients in bf16 121 us (10.1 bytes each, 5.6 TB/s), in fp32 193 (5.6);
+// stochastically the vector unit has as much to do in bf16 (137 us; 152 in the kernel
+// above), about 20 instructions an element for its random bits.  Six waves per SIMD hide
+// 2% more of it than five; weights in fp32 would not fit their registers.
 template <typename TX, typename TG, bool kStochastic>
-__global__ __launch_bounds__(256, 5) void adamw_codes_kernel(AdamwRows a) {
+__global__ __launch_bounds__(256, sizeof(TX) == 2 ? 6 : 5) void adamw_codes_kernel(AdamwRows a) {
   const int first = a.first[threadIdx.x & (kLanes - 1)];
   const StepScalars s = step_scalars(a.h);
   if (s.skip) return;
@@ -494,7 +557,10 @@ __device__ __forceinline__ double add_square(double sum, uint32_t bits) {
   return fma(d, d, sum);
 }
 
-// The next unit's loads are under way while this one's squares are added.
+// The squares' sum in fp64, where an fp32 square is exact.  The next unit's loads are
+// under way while this one's squares are added.  Bound by HBM: 134 MB take 27 us (5.0
+// TB/s), 1.2 GB 206 (5.9), with the 2048 workgroups that the chip holds at once (1024:
+// 28.5 and 207; 16384: 27.7 and 201, but eight times the sums to join).
 __global__ __launch_bounds__(256) void grad_norm_parts_kernel(NormParts a) {
   __shared__ double red[4];
   const int64_t first = a.first[threadIdx.x & (kLanes - 1)];
@@ -520,6 +586,7 @@ __global__ __launch_bounds__(256) void grad_norm_parts_kernel(NormParts a) {
   if (threadIdx.x == 0) a.part[blockIdx.x] = red[0] + red[1] + red[2] + red[3];
 }
 
+// The workgroups' sums in a fixed order, by a launch of its own: 2 us.
 __global__ __launch_bounds__(1024) void grad_norm_join_kernel(const double* part, int count, double max_norm,
                                                               float* out) {
   __shared__ double red[16];

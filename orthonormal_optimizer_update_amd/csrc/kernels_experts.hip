@@ -229,7 +229,7 @@ __device__ __forceinline__ int64_t row_of(const ExpertRowsArgs& r, int64_t pair)
 
 // A token's row is read once and written `choices` times.  A workgroup's unit is
 // 256 >> lanes tokens by 1 << lanes pieces of 16 bytes.  Bound by the writes: 8192
-// tokens x 2048 codes to 8 of 64 experts (rows padded to 128) take 36.1 us, 4.5 TB/s,
+// tokens x 2048 codes to 8 of 64 experts (rows padded to 128) take 35.7 us, 4.5 TB/s,
 // of which the scales, scattered in pieces of 64 bytes, are 4 us (6 written beside
 // each 128 codes by the thread that has them).  A wave per token with scalar rows
 // took 46 us, a thread row per (token, choice), which reads the token anew, 78.
@@ -451,7 +451,7 @@ __device__ __forceinline__ void grad_chunk(const ExpertCombineGradArgs& a, int64
 
 // kWaves waves per token, kAtOnce choices at a time: their rows of Y are read, the
 // products with dOut summed, their rows of dY written.  Bound by HBM: 8192 tokens x
-// 2048 bf16, 8 choices 115 us (5.0 TB/s).
+// 2048 bf16, 8 choices 116 to 120 us (4.9 TB/s).
 template <typename T, int kAtOnce, int kWaves>
 __global__ __launch_bounds__(256) void expert_combine_grad_kernel(ExpertCombineGradArgs a, int64_t groups) {
   __shared__ float red[2][4][64];
