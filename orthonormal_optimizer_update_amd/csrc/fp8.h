@@ -169,6 +169,46 @@ __device__ __forceinline__ uint4 cut16(uint4 u, int cut) {
                     static_cast<uint32_t>(hi >> 32));
 }
 
+// 16 and 8 bytes at any address; kOnce: such as pass through the chip once, so that the
+// caches need not keep them.
+template <typename V, bool kOnce>
+__device__ __forceinline__ V load_any(const void* p) {
+  typedef uint32_t Words __attribute__((ext_vector_type(sizeof(V) / 4), aligned(1)));
+  const Words* const w = static_cast<const Words*>(p);
+  const Words u = kOnce ? __builtin_nontemporal_load(w) : *w;
+  V v;
+  __builtin_memcpy(&v, &u, sizeof(V));
+  return v;
+}
+template <bool kOnce, typename V>
+__device__ __forceinline__ void store_any(void* p, const V& v) {
+  typedef uint32_t Words __attribute__((ext_vector_type(sizeof(V) / 4), aligned(1)));
+  Words u;
+  __builtin_memcpy(&u, &v, sizeof(V));
+  if constexpr (kOnce) __builtin_nontemporal_store(u, static_cast<Words*>(p));
+  else *static_cast<Words*>(p) = u;
+}
+
+// Eight elements at `row`, all inside.
+template <bool kOnce, typename T>
+__device__ __forceinline__ Raw8<T> load_whole8(const T* row) {
+  Raw8<T> r;
+  r.a = load_any<uint4, kOnce>(row);
+  if constexpr (sizeof(T) == 4) r.b = load_any<uint4, kOnce>(row + 4);
+  return r;
+}
+template <bool kOnce>
+__device__ __forceinline__ void store_whole8(uint16_t* row, const float (&v)[8]) {
+  const uint2 lo = pack_bf16x4(floatx4{v[0], v[1], v[2], v[3]});
+  const uint2 hi = pack_bf16x4(floatx4{v[4], v[5], v[6], v[7]});
+  store_any<kOnce>(row, make_uint4(lo.x, lo.y, hi.x, hi.y));
+}
+template <bool kOnce>
+__device__ __forceinline__ void store_whole8(float* row, const float (&v)[8]) {
+  store_any<kOnce>(row, floatx4{v[0], v[1], v[2], v[3]});
+  store_any<kOnce>(row + 4, floatx4{v[4], v[5], v[6], v[7]});
+}
+
 // 16 bytes' worth of elements from column c of a row of `limit` columns; zeros
 // past its end.  The row may start at any element (the accesses need no
 // alignment); what its end cuts is loaded from further left and shifted, so

@@ -41,17 +41,18 @@ struct Bits {
     key = tensor + kStride * static_cast<uint32_t>(static_cast<uint64_t>(element) >> 32);
     next = key + kStride;
   }
-  // m's seeds, and sqrt(v)'s, of eight elements.
-  __device__ __forceinline__ void all(uint32_t (&a)[8], uint32_t (&b)[8]) const {
-    if (__any(low > ~0u - 7)) {   // a multiple of 2^32 among them
+  // m's seeds, and sqrt(v)'s, of kN elements.
+  template <int kN>
+  __device__ __forceinline__ void all(uint32_t (&a)[kN], uint32_t (&b)[kN]) const {
+    if (__any(low > ~0u - (kN - 1))) {   // a multiple of 2^32 among them
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] = mix((low + j) ^ (low + j < low ? next : key));
+      for (int j = 0; j < kN; ++j) a[j] = mix((low + j) ^ (low + j < low ? next : key));
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] = mix((low + j) ^ key);
+      for (int j = 0; j < kN; ++j) a[j] = mix((low + j) ^ key);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) b[j] = mix(a[j] + kStride);
+    for (int j = 0; j < kN; ++j) b[j] = mix(a[j] + kStride);
   }
   // The weight's: a's low 12 bits, then b's low 4.
   static __device__ __forceinline__ uint32_t weight(uint32_t a, uint32_t b) {
@@ -61,20 +62,24 @@ struct Bits {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
+// Two weights, rounded by their seeds.
+__device__ __forceinline__ uint32_t weights2(float x0, float x1, uint32_t seed0, uint32_t seed1) {
+  bf16x2 p = {0, 0};
+  p = __builtin_amdgcn_cvt_sr_bf16_f32(p, x0, seed0, false);
+  p = __builtin_amdgcn_cvt_sr_bf16_f32(p, x1, seed1, true);
+  return __builtin_bit_cast(uint32_t, p);
+}
+
 // Eight weights to column c of a row of `limit`, rounded by their seeds.
+template <bool kOnce>
 __device__ __forceinline__ void store_weights8(uint16_t* row, int c, int limit, const float (&x)[8],
                                                const uint32_t (&seed)[8]) {
   uint32_t w[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    bf16x2 p = {0, 0};
-    p = __builtin_amdgcn_cvt_sr_bf16_f32(p, x[2 * j], seed[2 * j], false);
-    p = __builtin_amdgcn_cvt_sr_bf16_f32(p, x[2 * j + 1], seed[2 * j + 1], true);
-    w[j] = __builtin_bit_cast(uint32_t, p);
-  }
+  for (int j = 0; j < 4; ++j) w[j] = weights2(x[2 * j], x[2 * j + 1], seed[2 * j], seed[2 * j + 1]);
   if (c + 8 <= limit) {
     const uint4 u = make_uint4(w[0], w[1], w[2], w[3]);
-    __builtin_memcpy(row + c, &u, 16);
+    store_any<kOnce>(row + c, u);
     return;
   }
 #pragma unroll
@@ -174,27 +179,79 @@ __device__ __forceinline__ int tensor_of(I first, I unit) {
   return __builtin_amdgcn_readfirstlane(__popcll(__ballot(first <= unit)) - 1);
 }
 
-// Eight elements at c of a unit's `limit`; a whole unit needs no look at its end.
-template <bool kWhole, typename T>
-__device__ __forceinline__ Raw8<T> unit_load(const T* p, int c, int limit) {
-  if constexpr (!kWhole) return load_raw8(p, c, limit);
-  Raw8<T> r;
-  __builtin_memcpy(&r, p + c, sizeof(r));
-  return r;
+
+// Four elements at p.
+template <bool kOnce>
+__device__ __forceinline__ void load4(const float* p, float* v) {
+  const uint4 u = load_any<uint4, kOnce>(p);
+  v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y); v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+}
+template <bool kOnce>
+__device__ __forceinline__ void load4(const uint16_t* p, float* v) {
+  const uint2 u = load_any<uint2, kOnce>(p);
+  v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+  v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+template <bool kOnce>
+__device__ __forceinline__ void store4(float* p, const float* v) {
+  store_any<kOnce>(p, floatx4{v[0], v[1], v[2], v[3]});
+}
+template <bool kOnce>
+__device__ __forceinline__ void store4(uint16_t* p, const float* v) {
+  store_any<kOnce>(p, pack_bf16x4(floatx4{v[0], v[1], v[2], v[3]}));
 }
 
-template <typename TX, typename TG, bool kStochastic, bool kWhole>
-__device__ __forceinline__ void flat_unit(const AdamwScalars& h, const StepScalars& s, const FlatTensor& t,
+// A whole unit: a thread has four elements in each half of it, so that every access of
+// a wave covers whole lines whatever the type.
+template <typename TX, typename TG, bool kStochastic, bool kOnce>
+__device__ __forceinline__ void flat_whole(const AdamwScalars& h, const StepScalars& s, const FlatTensor& t,
+                                           int64_t base, uint32_t key) {
+  constexpr int kHalf = kUnit / 2;
+  base += threadIdx.x * 4;
+  TX* const x = static_cast<TX*>(t.x) + base;
+  const TG* const g = static_cast<const TG*>(t.g) + base;
+  float *const m = t.m + base, *const v = t.v + base;
+  float xv[8], gv[8], mv[8], vv[8];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    load4<kOnce>(x + q * kHalf, xv + 4 * q);
+    load4<kOnce>(g + q * kHalf, gv + 4 * q);
+    load4<kOnce>(m + q * kHalf, mv + 4 * q);
+    load4<kOnce>(v + q * kHalf, vv + 4 * q);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    moments(h, s, gv[j], mv[j], vv[j]);
+    xv[j] = weight(h, s, xv[j], mv[j], __builtin_sqrtf(vv[j]));
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    if constexpr (kStochastic && sizeof(TX) == 2) {
+      uint32_t a[4], b[4];
+      Bits(key, base + q * kHalf).all(a, b);
+      store_any<kOnce>(x + q * kHalf, make_uint2(weights2(xv[4 * q], xv[4 * q + 1], Bits::weight(a[0], b[0]), Bits::weight(a[1], b[1])),
+                                                 weights2(xv[4 * q + 2], xv[4 * q + 3], Bits::weight(a[2], b[2]), Bits::weight(a[3], b[3]))));
+    } else {
+      store4<kOnce>(x + q * kHalf, xv + 4 * q);
+    }
+    store4<kOnce>(m + q * kHalf, mv + 4 * q);
+    store4<kOnce>(v + q * kHalf, vv + 4 * q);
+  }
+}
+
+// A tensor's last unit, of `limit` elements.
+template <typename TX, typename TG, bool kStochastic>
+__device__ __forceinline__ void flat_part(const AdamwScalars& h, const StepScalars& s, const FlatTensor& t,
                                           int64_t base, int limit, uint32_t key) {
   TX* const x = static_cast<TX*>(t.x) + base;
   const TG* const g = static_cast<const TG*>(t.g) + base;
   float *const m = t.m + base, *const v = t.v + base;
   const int c = threadIdx.x * 8;
   float xv[8], gv[8], mv[8], vv[8];
-  const auto rx = unit_load<kWhole>(x, c, limit);
-  const auto rg = unit_load<kWhole>(g, c, limit);
-  const auto rm = unit_load<kWhole>(m, c, limit);
-  const auto rv = unit_load<kWhole>(v, c, limit);
+  const auto rx = load_raw8(x, c, limit);
+  const auto rg = load_raw8(g, c, limit);
+  const auto rm = load_raw8(m, c, limit);
+  const auto rv = load_raw8(v, c, limit);
   unpack8(rx, xv);
   unpack8(rg, gv);
   unpack8(rm, mv);
@@ -204,14 +261,13 @@ __device__ __forceinline__ void flat_unit(const AdamwScalars& h, const StepScala
     moments(h, s, gv[j], mv[j], vv[j]);
     xv[j] = weight(h, s, xv[j], mv[j], __builtin_sqrtf(vv[j]));
   }
-  if constexpr (kWhole) limit = kUnit;
   if constexpr (kStochastic && sizeof(TX) == 2) {
     const Bits bits(key, base + c);
     uint32_t a[8], b[8], seed[8];
     bits.all(a, b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) seed[j] = Bits::weight(a[j], b[j]);
-    store_weights8(x, c, limit, xv, seed);
+    store_weights8<false>(x, c, limit, xv, seed);
   } else {
     store8(x, c, limit, xv);
   }
@@ -219,25 +275,22 @@ __device__ __forceinline__ void flat_unit(const AdamwScalars& h, const StepScala
   store8(v, c, limit, vv);
 }
 
-template <bool kStochastic, bool kWhole>
-__device__ __forceinline__ void flat_by_kind(const AdamwScalars& h, const StepScalars& s, const FlatTensor& t,
-                                             int64_t base, int limit, uint32_t key) {
-  switch (t.kind) {
-    case 0: flat_unit<float, float, kStochastic, kWhole>(h, s, t, base, limit, key); break;
-    case kBf16Weight: flat_unit<uint16_t, float, kStochastic, kWhole>(h, s, t, base, limit, key); break;
-    case kBf16Gradient: flat_unit<float, uint16_t, kStochastic, kWhole>(h, s, t, base, limit, key); break;
-    default: flat_unit<uint16_t, uint16_t, kStochastic, kWhole>(h, s, t, base, limit, key);
-  }
+template <typename TX, typename TG, bool kStochastic, bool kOnce>
+__device__ __forceinline__ void flat_unit(const AdamwScalars& h, const StepScalars& s, const FlatTensor& t,
+                                          int64_t base, int64_t left, uint32_t key) {
+  if (left >= kUnit) flat_whole<TX, TG, kStochastic, kOnce>(h, s, t, base, key);
+  else flat_part<TX, TG, kStochastic>(h, s, t, base, static_cast<int>(left), key);
 }
 
-// Tensors of consecutive elements, states in 32 bits.  Bound by HBM: 470 million weights
-// and gradients in bf16 take 1.89 ms (22 bytes each, 5.5 TB/s; a copy reaches 5.1).
-// Every element is touched once, so nothing is staged: each thread has its 8 elements'
-// loads under way together, and a new workgroup per unit keeps memory busier than
-// workgroups that stay (604 million with clipping 2.72 ms; 2.94 with 2048 that walk
-// the units; 2.73 and 2.75 with two and four units next to each other per workgroup).
+// Tensors of consecutive elements, states in 32 bits.  Bound by HBM: 134 million weights
+// and gradients in bf16 take 501 us (22 bytes each, 5.9 TB/s; a copy reaches 5.1).  Every
+// element is touched once, so nothing is staged: each thread has its 8 elements' loads
+// under way together, a new workgroup per unit keeps memory busier than workgroups that
+// stay (8% on 604 million; two and four units per workgroup: no gain), and what is large
+// goes past the caches, in whole lines and both ways (551 us through them; 545 past them
+// with lines in halves, 541 with only the loads, 551 with only the stores past them).
 // 100352 fp32 weights in 49 tensors take 4.0 us, a launch's latency.
-template <bool kStochastic>
+template <bool kStochastic, bool kOnce>
 __global__ __launch_bounds__(256) void adamw_flat_kernel(AdamwFlat a) {
   const int first = a.first[threadIdx.x & (kLanes - 1)];
   const StepScalars s = step_scalars(a.h);
@@ -247,8 +300,12 @@ __global__ __launch_bounds__(256) void adamw_flat_kernel(AdamwFlat a) {
     const FlatTensor& t = a.t[i];
     const int64_t base = (int64_t)(unit - a.first[i]) * kUnit, left = t.n - base;
     const uint32_t key = kStochastic ? tensor_key(a.h, s.step, t.index) : 0;
-    if (left >= kUnit) flat_by_kind<kStochastic, true>(a.h, s, t, base, kUnit, key);
-    else flat_by_kind<kStochastic, false>(a.h, s, t, base, static_cast<int>(left), key);
+    switch (t.kind) {
+      case 0: flat_unit<float, float, kStochastic, kOnce>(a.h, s, t, base, left, key); break;
+      case kBf16Weight: flat_unit<uint16_t, float, kStochastic, kOnce>(a.h, s, t, base, left, key); break;
+      case kBf16Gradient: flat_unit<float, uint16_t, kStochastic, kOnce>(a.h, s, t, base, left, key); break;
+      default: flat_unit<uint16_t, uint16_t, kStochastic, kOnce>(a.h, s, t, base, left, key);
+    }
   }
 }
 
@@ -361,12 +418,19 @@ __device__ __forceinline__ uint2 to_codes8(const float (&v)[8], const uint32_t (
 }
 
 // Eight codes at c of a row of `cols`.
-template <bool kWhole>
+template <bool kWhole, bool kOnce>
 __device__ __forceinline__ uint2 unit_load_codes(const uint8_t* row, int c, int cols) {
-  if constexpr (!kWhole) return load_codes8(row, c, cols);
-  uint2 u;
-  __builtin_memcpy(&u, row + c, 8);
-  return u;
+  if constexpr (kWhole) return load_any<uint2, kOnce>(row + c);
+  else return load_codes8(row, c, cols);
+}
+
+// Eight elements at c of a row of `cols`.  fp32, of which a wave's 16-byte accesses take
+// every other 16, does not go past the caches, which join the halves of a line (67
+// million weights with gradients in fp32: 184 us, 197 past them).
+template <bool kWhole, bool kOnce, typename T>
+__device__ __forceinline__ Raw8<T> unit_load(const T* p, int c, int limit) {
+  if constexpr (kWhole) return load_whole8<kOnce && sizeof(T) == 2>(p + c);
+  else return load_raw8(p, c, limit);
 }
 
 // (pitch and row as they are, unsigned: the address takes one multiplication)
@@ -377,22 +441,22 @@ __device__ __forceinline__ T* row_at(void* base, uint32_t ld, uint32_t row) {
 
 // One thread's eight elements of a row.  kWhole: all inside.  kCodes: states in 8
 // bits, else either.
-template <typename TX, typename TG, bool kStochastic, bool kCodes, bool kWhole>
+template <typename TX, typename TG, bool kStochastic, bool kCodes, bool kOnce, bool kWhole>
 __device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScalars& s, const RowTensor& t, uint32_t row, int c,
                                           uint32_t key) {
   int cols = t.cols;
   TX* const x = row_at<TX>(t.x, t.ldx, row);
   const TG* const g = row_at<const TG>(const_cast<void*>(t.g), t.ldg, row);
   float xv[8], gv[8], mv[8], vv[8];
-  const auto rx = unit_load<kWhole>(x, c, cols);
-  const auto rg = unit_load<kWhole>(g, c, cols);
+  const auto rx = unit_load<kWhole, kOnce>(x, c, cols);
+  const auto rg = unit_load<kWhole, kOnce>(g, c, cols);
   const Bits bits(key, static_cast<uint64_t>(row) * static_cast<uint32_t>(cols) + c);
   uint32_t seed_m[8] = {}, seed_v[8] = {};
   if (!kCodes && t.sm == nullptr) {
     float* const m = row_at<float>(t.m, t.ldm, row);
     float* const v = row_at<float>(t.v, t.ldv, row);
-    const auto rm = unit_load<kWhole>(m, c, cols);
-    const auto rv = unit_load<kWhole>(v, c, cols);
+    const auto rm = unit_load<kWhole, kOnce>(m, c, cols);
+    const auto rv = unit_load<kWhole, kOnce>(v, c, cols);
     unpack8(rx, xv);
     unpack8(rg, gv);
     unpack8(rm, mv);
@@ -411,7 +475,7 @@ __device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScala
     uint8_t* const v = row_at<uint8_t>(t.v, t.ldv, row);
     float* const sm = row_at<float>(t.sm, t.ldsm, row) + (c >> 7);
     float* const sv = row_at<float>(t.sv, t.ldsv, row) + (c >> 7);
-    const uint2 qm = unit_load_codes<kWhole>(m, c, cols), qv = unit_load_codes<kWhole>(v, c, cols);
+    const uint2 qm = unit_load_codes<kWhole, kOnce>(m, c, cols), qv = unit_load_codes<kWhole, kOnce>(v, c, cols);
     const float ms = *sm, vs = *sv;
     unpack8(rx, xv);
     unpack8(rg, gv);
@@ -436,8 +500,13 @@ __device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScala
     const uint2 um = to_codes8<kStochastic, false>(mv, seed_m, false, ms2);
     const uint2 uv = to_codes8<kStochastic, true>(vv, seed_v, zeros, vs2);
     if constexpr (kWhole) cols = c + 8;
-    store_codes8(m, c, cols, um);
-    store_codes8(v, c, cols, uv);
+    if constexpr (kWhole) {
+      store_any<kOnce>(m + c, um);
+      store_any<kOnce>(v + c, uv);
+    } else {
+      store_codes8(m, c, cols, um);
+      store_codes8(v, c, cols, uv);
+    }
     if ((threadIdx.x & 15) == 0) {
       *sm = ms2;
       *sv = vs2;
@@ -447,13 +516,15 @@ __device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScala
     uint32_t seed[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) seed[j] = Bits::weight(seed_m[j], seed_v[j]);
-    store_weights8(x, c, cols, xv, seed);
+    store_weights8<kOnce>(x, c, cols, xv, seed);
+  } else if constexpr (kWhole) {
+    store_whole8<kOnce && sizeof(TX) == 2>(x + c, xv);
   } else {
     store8(x, c, cols, xv);
   }
 }
 
-template <typename TX, typename TG, bool kStochastic, bool kCodes>
+template <typename TX, typename TG, bool kStochastic, bool kCodes, bool kOnce>
 __device__ __forceinline__ void row_unit(const AdamwScalars& h, const StepScalars& s, const RowTensor& t, int at,
                                          uint32_t key) {
   const int lanes = t.lanes, across = t.across, down = at / across;
@@ -461,8 +532,8 @@ __device__ __forceinline__ void row_unit(const AdamwScalars& h, const StepScalar
   const int c = (((at - down * across) << lanes) + (threadIdx.x & ((1 << lanes) - 1))) * 8;
   // (the 16 lanes of a block share the row)
   if (row >= t.rows || (c & ~127) >= t.cols) return;
-  if (__all(c + 8 <= t.cols)) row_piece<TX, TG, kStochastic, kCodes, true>(h, s, t, row, c, key);
-  else row_piece<TX, TG, kStochastic, kCodes, false>(h, s, t, row, c, key);
+  if (__all(c + 8 <= t.cols)) row_piece<TX, TG, kStochastic, kCodes, kOnce, true>(h, s, t, row, c, key);
+  else row_piece<TX, TG, kStochastic, kCodes, kOnce, false>(h, s, t, row, c, key);
 }
 
 // Tensors of any kind: rows of their own pitch, or states in 8 bits beside other kinds.
@@ -480,20 +551,21 @@ __global__ __launch_bounds__(256, 5) void adamw_rows_kernel(AdamwRows a) {
     const int at = unit - a.first[i];
     const uint32_t key = kStochastic ? tensor_key(a.h, s.step, t.index) : 0;
     switch (t.kind) {
-      case 0: row_unit<float, float, kStochastic, false>(a.h, s, t, at, key); break;
-      case kBf16Weight: row_unit<uint16_t, float, kStochastic, false>(a.h, s, t, at, key); break;
-      case kBf16Gradient: row_unit<float, uint16_t, kStochastic, false>(a.h, s, t, at, key); break;
-      default: row_unit<uint16_t, uint16_t, kStochastic, false>(a.h, s, t, at, key);
+      case 0: row_unit<float, float, kStochastic, false, false>(a.h, s, t, at, key); break;
+      case kBf16Weight: row_unit<uint16_t, float, kStochastic, false, false>(a.h, s, t, at, key); break;
+      case kBf16Gradient: row_unit<float, uint16_t, kStochastic, false, false>(a.h, s, t, at, key); break;
+      default: row_unit<uint16_t, uint16_t, kStochastic, false, false>(a.h, s, t, at, key);
     }
   }
 }
 
 // Tensors with states in 8 bits, all of one kind.  Bound by HBM to nearest: 67 million
-// weights with gradients in bf16 121 us (10.1 bytes each, 5.6 TB/s), in fp32 193 (5.6);
-// stochastically the vector unit has as much to do in bf16 (137 us; 152 in the kernel
-// above), about 20 instructions an element for its random bits.  Six waves per SIMD hide
-// 2% more of it than five; weights in fp32 would not fit their registers.
-template <typename TX, typename TG, bool kStochastic>
+// weights with gradients in bf16 115 us (10.1 bytes each, 5.9 TB/s; 123 through the
+// caches), in fp32 184 (5.9); stochastically the vector unit has as much to do in bf16
+// (136 us; 152 in the kernel above), about 20 instructions an element for its random
+// bits.  Six waves per SIMD hide 2% more of it than five; weights in fp32 would not fit
+// their registers.
+template <typename TX, typename TG, bool kStochastic, bool kOnce>
 __global__ __launch_bounds__(256, sizeof(TX) == 2 ? 6 : 5) void adamw_codes_kernel(AdamwRows a) {
   const int first = a.first[threadIdx.x & (kLanes - 1)];
   const StepScalars s = step_scalars(a.h);
@@ -502,7 +574,7 @@ __global__ __launch_bounds__(256, sizeof(TX) == 2 ? 6 : 5) void adamw_codes_kern
     const int i = tensor_of(first, unit);
     const RowTensor& t = a.t[i];
     const uint32_t key = kStochastic ? tensor_key(a.h, s.step, t.index) : 0;
-    row_unit<TX, TG, kStochastic, true>(a.h, s, t, unit - a.first[i], key);
+    row_unit<TX, TG, kStochastic, true, kOnce>(a.h, s, t, unit - a.first[i], key);
   }
 }
 
@@ -610,33 +682,42 @@ __global__ __launch_bounds__(1024) void grad_norm_join_kernel(const double* part
 // A workgroup per unit, as far as a launch goes (2^32 threads); more are walked.
 constexpr int kMostGroups = (1 << 24) - 1;
 
+// Units from which on a launch goes past the caches, which would keep too little of it
+// until the next step (bf16 weights and gradients, states in 32 bits: 8192 units 61.4 us
+// past the caches and 71.4 through them, 4096 32.3 both ways, 2048 17.5 and 15.4; in 8
+// bits: 16384 units 59.9 and 64.4, 8192 32 both ways).
+constexpr int kPastUnits = 1 << 13;
+
 inline dim3 grid_of(int units) { return dim3(units < kMostGroups ? units : kMostGroups); }
 
 }  // namespace
 
 hipError_t launch_adamw_flat(const AdamwFlat& a, bool stochastic, hipStream_t s) {
-  if (stochastic) hipLaunchKernelGGL(adamw_flat_kernel<true>, grid_of(a.units), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(adamw_flat_kernel<false>, grid_of(a.units), dim3(256), 0, s, a);
+  const bool once = a.units >= kPastUnits;
+  const auto kernel = stochastic ? (once ? adamw_flat_kernel<true, true> : adamw_flat_kernel<true, false>)
+                                 : (once ? adamw_flat_kernel<false, true> : adamw_flat_kernel<false, false>);
+  hipLaunchKernelGGL(kernel, grid_of(a.units), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
-template <bool kStochastic>
-static hipError_t rows(const AdamwRows& a, int kind, hipStream_t s) {
-  const dim3 grid = grid_of(a.units), block(256);
-  switch (kind) {
-    case 0: hipLaunchKernelGGL((adamw_codes_kernel<float, float, kStochastic>), grid, block, 0, s, a); break;
-    case kBf16Weight: hipLaunchKernelGGL((adamw_codes_kernel<uint16_t, float, kStochastic>), grid, block, 0, s, a); break;
-    case kBf16Gradient: hipLaunchKernelGGL((adamw_codes_kernel<float, uint16_t, kStochastic>), grid, block, 0, s, a); break;
-    case kBf16Weight | kBf16Gradient:
-      hipLaunchKernelGGL((adamw_codes_kernel<uint16_t, uint16_t, kStochastic>), grid, block, 0, s, a);
-      break;
-    default: hipLaunchKernelGGL(adamw_rows_kernel<kStochastic>, grid, block, 0, s, a);
-  }
+template <bool kStochastic, bool kOnce>
+static hipError_t codes(const AdamwRows& a, int kind, hipStream_t s) {
+  const auto kernel = kind == 0               ? adamw_codes_kernel<float, float, kStochastic, kOnce>
+                      : kind == kBf16Weight   ? adamw_codes_kernel<uint16_t, float, kStochastic, kOnce>
+                      : kind == kBf16Gradient ? adamw_codes_kernel<float, uint16_t, kStochastic, kOnce>
+                                              : adamw_codes_kernel<uint16_t, uint16_t, kStochastic, kOnce>;
+  hipLaunchKernelGGL(kernel, grid_of(a.units), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_adamw_rows(const AdamwRows& a, int kind, bool stochastic, hipStream_t s) {
-  return stochastic ? rows<true>(a, kind, s) : rows<false>(a, kind, s);
+  if (kind < 0) {
+    const auto kernel = stochastic ? adamw_rows_kernel<true> : adamw_rows_kernel<false>;
+    hipLaunchKernelGGL(kernel, grid_of(a.units), dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  if (a.units >= kPastUnits) return stochastic ? codes<true, true>(a, kind, s) : codes<false, true>(a, kind, s);
+  return stochastic ? codes<true, false>(a, kind, s) : codes<false, false>(a, kind, s);
 }
 
 hipError_t launch_grad_norm_parts(const NormParts& a, int groups, hipStream_t s) {

@@ -177,9 +177,10 @@ __device__ __forceinline__ int64_t piece_at(int64_t p, int64_t bytes) {
   return p * 16 + 16 <= bytes ? p * 16 : bytes - 16;
 }
 
+template <bool kOnce>
 __device__ __forceinline__ void copy_piece(uint8_t* dst, const uint4& u, int64_t p, int64_t bytes) {
   if (bytes >= 16) {
-    __builtin_memcpy(dst + piece_at(p, bytes), &u, 16);
+    store_any<kOnce>(dst + piece_at(p, bytes), u);
     return;
   }
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -203,6 +204,7 @@ __device__ __forceinline__ uint4 load_piece(const uint8_t* src, int64_t p, int64
 
 // Zeros in the rows of padding of expert e's part `part` of `parts`, `pieces` of
 // `bytes` each.
+template <bool kOnce>
 __device__ __forceinline__ void clear_padding(const ExpertRowsArgs& r, int e, int part, int parts, uint8_t* y,
                                               int64_t pitch, int64_t bytes, uint8_t* s, int64_t pitch_s, int blocks,
                                               int scale_bytes) {
@@ -210,7 +212,8 @@ __device__ __forceinline__ void clear_padding(const ExpertRowsArgs& r, int e, in
   const int64_t to = min(static_cast<int64_t>(r.offsets[e + 1]), r.rows);
   const int64_t pieces = (bytes + 15) >> 4;
   for (int64_t row = from + part; row < to; row += parts) {
-    for (int64_t p = threadIdx.x; p < pieces; p += 256) copy_piece(y + row * pitch, make_uint4(0, 0, 0, 0), p, bytes);
+    for (int64_t p = threadIdx.x; p < pieces; p += 256)
+      copy_piece<kOnce>(y + row * pitch, make_uint4(0, 0, 0, 0), p, bytes);
     if (s)
       for (int i = threadIdx.x; i < blocks; i += 256) {
         if (scale_bytes == 4) reinterpret_cast<float*>(s + row * pitch_s)[i] = 1.f;
@@ -229,14 +232,16 @@ __device__ __forceinline__ int64_t row_of(const ExpertRowsArgs& r, int64_t pair)
 
 // A token's row is read once and written `choices` times.  A workgroup's unit is
 // 256 >> lanes tokens by 1 << lanes pieces of 16 bytes.  Bound by the writes: 8192
-// tokens x 2048 codes to 8 of 64 experts (rows padded to 128) take 35.7 us, 4.5 TB/s,
-// of which the scales, scattered in pieces of 64 bytes, are 4 us (6 written beside
-// each 128 codes by the thread that has them).  A wave per token with scalar rows
-// took 46 us, a thread row per (token, choice), which reads the token anew, 78.
+// tokens x 2048 codes to 8 of 64 experts (rows padded to 128) take 32 us, 4.9 TB/s, with
+// rows written past the caches (36 through them; reading past them too 35).  The scales,
+// scattered in pieces of 64 bytes, are 4 us of it (6 written beside each 128 codes by the
+// thread that has them).  A wave per token with scalar rows took a quarter more, a thread
+// row per (token, choice), which reads the token anew, twice as long.
+template <bool kOnce>
 __global__ __launch_bounds__(256) void expert_gather_kernel(ExpertGatherArgs a, int lanes, int across, int64_t units) {
   if (blockIdx.x >= gridDim.x - a.r.experts * kPadParts) {
     const int at = blockIdx.x - (gridDim.x - a.r.experts * kPadParts);
-    clear_padding(a.r, at / kPadParts, at % kPadParts, kPadParts, a.y, a.pitch_y, a.bytes, a.sy, a.pitch_sy, a.blocks,
+    clear_padding<kOnce>(a.r, at / kPadParts, at % kPadParts, kPadParts, a.y, a.pitch_y, a.bytes, a.sy, a.pitch_sy, a.blocks,
                   a.scale_bytes);
     return;
   }
@@ -253,7 +258,7 @@ __global__ __launch_bounds__(256) void expert_gather_kernel(ExpertGatherArgs a, 
 #pragma unroll 4
     for (int j = 0; j < a.r.choices; ++j) {
       const int64_t row = row_of(a.r, pair + j);
-      if (row >= 0) copy_piece(a.y + row * a.pitch_y, u, p, a.bytes);
+      if (row >= 0) copy_piece<kOnce>(a.y + row * a.pitch_y, u, p, a.bytes);
     }
   }
   if (a.s == nullptr) return;
@@ -352,17 +357,44 @@ __device__ __forceinline__ float scalar_weight(const Choices& c, int j) {
 
 constexpr int kWaveColumns = 512;
 
-// Eight elements at c of a row of n; kWhole: inside.
-template <bool kWhole, typename T>
+// This lane's eight elements of the 512 of a row of n from column c on; kWhole: all
+// inside.  Where rows are fp32 (kHalves) a lane of a whole 512 has four elements in each
+// half, so that every access of a wave covers whole lines.
+template <bool kWhole, bool kHalves, bool kOnce, typename T>
 __device__ __forceinline__ Raw8<T> piece8(const T* row, int c, int n) {
-  if constexpr (!kWhole) return load_raw8(row, c, n);
+  const int lane = threadIdx.x & 63;
   Raw8<T> r;
-  __builtin_memcpy(&r, row + c, sizeof(r));
+  if constexpr (!kWhole) {
+    r = load_raw8(row, c + lane * 8, n);
+  } else if constexpr (!kHalves) {
+    r = load_whole8<kOnce>(row + c + lane * 8);
+  } else if constexpr (sizeof(T) == 4) {
+    r.a = load_any<uint4, kOnce>(row + c + lane * 4);
+    r.b = load_any<uint4, kOnce>(row + c + kWaveColumns / 2 + lane * 4);
+  } else {
+    const uint2 lo = load_any<uint2, kOnce>(row + c + lane * 4);
+    const uint2 hi = load_any<uint2, kOnce>(row + c + kWaveColumns / 2 + lane * 4);
+    r.a = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
   return r;
 }
+template <bool kWhole, bool kHalves, bool kOnce, typename T>
+__device__ __forceinline__ void store_piece8(T* row, int c, int n, const float (&v)[8]) {
+  const int lane = threadIdx.x & 63;
+  if constexpr (!kWhole) {
+    store8(row, c + lane * 8, n, v);
+  } else if constexpr (!kHalves) {
+    store_whole8<kOnce>(row + c + lane * 8, v);
+  } else {
+    static_assert(sizeof(T) == 4, "");
+    store_any<kOnce>(row + c + lane * 4, floatx4{v[0], v[1], v[2], v[3]});
+    store_any<kOnce>(row + c + kWaveColumns / 2 + lane * 4, floatx4{v[4], v[5], v[6], v[7]});
+  }
+}
 
-template <typename T, int kAtOnce, bool kWhole>
+template <typename T, int kAtOnce, bool kWhole, bool kOnce>
 __device__ __forceinline__ void combine_chunk(const ExpertCombineArgs& a, int64_t token, const Choices& ch, int c) {
+  constexpr bool kHalves = sizeof(T) == 4;
   float sum[8] = {};
   for (int j0 = 0; j0 < a.r.choices; j0 += kAtOnce) {
     Raw8<T> y[kAtOnce];
@@ -370,7 +402,7 @@ __device__ __forceinline__ void combine_chunk(const ExpertCombineArgs& a, int64_
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
       row[j] = j0 + j < a.r.choices ? scalar_row(ch, j0 + j) : -1;
-      y[j] = piece8<kWhole>(static_cast<const T*>(a.y) + max(row[j], 0) * a.ldy, c, a.n);
+      y[j] = piece8<kWhole, kHalves, kOnce>(static_cast<const T*>(a.y) + max(row[j], 0) * a.ldy, c, a.n);
     }
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
@@ -384,25 +416,25 @@ __device__ __forceinline__ void combine_chunk(const ExpertCombineArgs& a, int64_
   }
   if (a.add) {
     float v[8];
-    if (a.add_bf) unpack8(piece8<kWhole>(static_cast<const uint16_t*>(a.add) + token * a.ldadd, c, a.n), v);
-    else unpack8(piece8<kWhole>(static_cast<const float*>(a.add) + token * a.ldadd, c, a.n), v);
+    if (a.add_bf) unpack8(piece8<kWhole, kHalves, kOnce>(static_cast<const uint16_t*>(a.add) + token * a.ldadd, c, a.n), v);
+    else unpack8(piece8<kWhole, kHalves, kOnce>(static_cast<const float*>(a.add) + token * a.ldadd, c, a.n), v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] += v[e];
   }
-  store8(static_cast<T*>(a.out) + token * a.ldout, c, kWhole ? c + 8 : a.n, sum);
+  store_piece8<kWhole, kHalves, kOnce>(static_cast<T*>(a.out) + token * a.ldout, c, a.n, sum);
 }
 
-// Bound by HBM: 8192 tokens x 2048 bf16 from 8 experts each 59.4 us (5.1 TB/s), 66.9
-// with the rows' addresses in vector registers.
-template <typename T, int kAtOnce>
+// Bound by HBM: 8192 tokens x 2048 bf16 from 8 experts each 50 us (6.0 TB/s), 59 through
+// the caches, 67 with the rows' addresses in vector registers.
+template <typename T, int kAtOnce, bool kOnce>
 __global__ __launch_bounds__(256) void expert_combine_kernel(ExpertCombineArgs a, int chunks, int64_t tasks) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int64_t task = (int64_t)blockIdx.x * 4 + wave; task < tasks; task += 4 * (int64_t)gridDim.x) {
     const int64_t token = task / chunks;
-    const int c0 = static_cast<int>(task - token * chunks) * kWaveColumns, c = c0 + lane * 8;
+    const int c = static_cast<int>(task - token * chunks) * kWaveColumns;
     const Choices ch = lane_choices(a.r, token, a.w, a.w_bf, a.ldw);
-    if (c0 + kWaveColumns <= a.n) combine_chunk<T, kAtOnce, true>(a, token, ch, c);
-    else combine_chunk<T, kAtOnce, false>(a, token, ch, c);
+    if (c + kWaveColumns <= a.n) combine_chunk<T, kAtOnce, true, kOnce>(a, token, ch, c);
+    else combine_chunk<T, kAtOnce, false, kOnce>(a, token, ch, c);
   }
 }
 
@@ -419,15 +451,16 @@ __device__ __forceinline__ float sum_of_wave(float v) {
   return v + __shfl_xor(v, 32, 64);
 }
 
-template <typename T, int kAtOnce, bool kWhole>
+template <typename T, int kAtOnce, bool kWhole, bool kOnce>
 __device__ __forceinline__ void grad_chunk(const ExpertCombineGradArgs& a, int64_t token, const int (&row)[kAtOnce],
                                            const float (&w)[kAtOnce], float (&dot)[kAtOnce], int c) {
-  const Raw8<T> rd = piece8<kWhole>(static_cast<const T*>(a.dout) + token * a.lddout, c, a.n);
+  constexpr bool kHalves = sizeof(T) == 4;
+  const Raw8<T> rd = piece8<kWhole, kHalves, kOnce>(static_cast<const T*>(a.dout) + token * a.lddout, c, a.n);
   float d[8];
   if (a.y) {
     Raw8<T> y[kAtOnce];
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) y[j] = piece8<kWhole>(static_cast<const T*>(a.y) + max(row[j], 0) * a.ldy, c, a.n);
+    for (int j = 0; j < kAtOnce; ++j) y[j] = piece8<kWhole, kHalves, kOnce>(static_cast<const T*>(a.y) + max(row[j], 0) * a.ldy, c, a.n);
     unpack8(rd, d);
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
@@ -445,19 +478,19 @@ __device__ __forceinline__ void grad_chunk(const ExpertCombineGradArgs& a, int64
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = w[j] * d[e];
-    store8(static_cast<T*>(a.dy) + row[j] * a.lddy, c, kWhole ? c + 8 : a.n, v);
+    store_piece8<kWhole, kHalves, kOnce>(static_cast<T*>(a.dy) + row[j] * a.lddy, c, a.n, v);
   }
 }
 
 // kWaves waves per token, kAtOnce choices at a time: their rows of Y are read, the
 // products with dOut summed, their rows of dY written.  Bound by HBM: 8192 tokens x
-// 2048 bf16, 8 choices 116 to 120 us (4.9 TB/s).
-template <typename T, int kAtOnce, int kWaves>
+// 2048 bf16, 8 choices 107 to 113 us (5.2 TB/s), 114 to 119 through the caches.
+template <typename T, int kAtOnce, int kWaves, bool kOnce>
 __global__ __launch_bounds__(256) void expert_combine_grad_kernel(ExpertCombineGradArgs a, int64_t groups) {
   __shared__ float red[2][4][64];
   if (blockIdx.x >= gridDim.x - a.r.experts * kPadParts) {
     const int at = blockIdx.x - (gridDim.x - a.r.experts * kPadParts);
-    clear_padding(a.r, at / kPadParts, at % kPadParts, kPadParts, static_cast<uint8_t*>(a.dy), a.lddy * sizeof(T),
+    clear_padding<kOnce>(a.r, at / kPadParts, at % kPadParts, kPadParts, static_cast<uint8_t*>(a.dy), a.lddy * sizeof(T),
                   (int64_t)a.n * sizeof(T), nullptr, 0, 0, 0);
     return;
   }
@@ -477,10 +510,9 @@ __global__ __launch_bounds__(256) void expert_combine_grad_kernel(ExpertCombineG
         w[j] = scalar_weight(ch, min(j0 + j, 63));
         dot[j] = 0.f;
       }
-      for (int c0 = kWaves == 1 ? 0 : wave * kWaveColumns; c0 < a.n; c0 += kWaves * kWaveColumns) {
-        const int c = c0 + lane * 8;
-        if (c0 + kWaveColumns <= a.n) grad_chunk<T, kAtOnce, true>(a, token, row, w, dot, c);
-        else grad_chunk<T, kAtOnce, false>(a, token, row, w, dot, c);
+      for (int c = kWaves == 1 ? 0 : wave * kWaveColumns; c < a.n; c += kWaves * kWaveColumns) {
+        if (c + kWaveColumns <= a.n) grad_chunk<T, kAtOnce, true, kOnce>(a, token, row, w, dot, c);
+        else grad_chunk<T, kAtOnce, false, kOnce>(a, token, row, w, dot, c);
       }
       if (a.y == nullptr) continue;
 #pragma unroll
@@ -503,6 +535,15 @@ __global__ __launch_bounds__(256) void expert_combine_grad_kernel(ExpertCombineG
 
 constexpr int64_t kMostGroups = 1 << 20;   // workgroups of a launch; more units are walked
 
+// Whether the rows by expert that a call reads and writes, `row_bytes` for a pair, are
+// more than the last-level cache of 256 MB would keep (bf16, 8 choices x 2048, past the
+// caches and through them: combine of 2048 tokens, 67 MB, 14.6 and 13.3 us, of 4096 28.7
+// and 33.2, of 8192 55.5 and 63.0; its gradient, of 1024, 67 MB, 15.0 and 13.2 us, of 2048
+// 29.7 and 34.8; codes gathered for 4096, 67 MB, 19.6 and 19.7, for 8192 32.4 and 36.7).
+bool passes_once(const ExpertRowsArgs& r, int64_t row_bytes) {
+  return static_cast<int64_t>(r.tokens) * r.choices * row_bytes >= int64_t{1} << 27;
+}
+
 }  // namespace
 
 hipError_t launch_expert_sort(const ExpertSortArgs& a, hipStream_t s) {
@@ -518,7 +559,8 @@ hipError_t launch_expert_sort(const ExpertSortArgs& a, hipStream_t s) {
 hipError_t launch_expert_gather(const ExpertGatherArgs& a, int lanes, int64_t across, int64_t units, hipStream_t s) {
   const int64_t groups = units < kMostGroups ? units : kMostGroups;
   const dim3 grid(static_cast<uint32_t>(groups + a.r.experts * kPadParts));
-  hipLaunchKernelGGL(expert_gather_kernel, grid, dim3(256), 0, s, a, lanes, static_cast<int>(across), units);
+  const auto kernel = passes_once(a.r, a.bytes) ? expert_gather_kernel<true> : expert_gather_kernel<false>;
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, lanes, static_cast<int>(across), units);
   return hipGetLastError();
 }
 
@@ -545,18 +587,20 @@ template <typename T>
 static hipError_t combine_wide(const ExpertCombineArgs& a, hipStream_t s) {
   const int64_t chunks = cdiv(a.n, kWaveColumns), tasks = chunks * a.r.tokens, groups = cdiv(tasks, 4);
   const dim3 grid(static_cast<uint32_t>(groups < kMostGroups ? groups : kMostGroups));
+  const bool once = passes_once(a.r, static_cast<int64_t>(a.n) * sizeof(T));
   return by_choices(a.r.choices, [&](auto k) {
-    hipLaunchKernelGGL((expert_combine_kernel<T, decltype(k)::value>), grid, dim3(256), 0, s, a,
-                       static_cast<int>(chunks), tasks);
+    constexpr int kAtOnce = decltype(k)::value;
+    const auto kernel = once ? expert_combine_kernel<T, kAtOnce, true> : expert_combine_kernel<T, kAtOnce, false>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, static_cast<int>(chunks), tasks);
   });
 }
 
-template <typename T, int kWaves>
+template <typename T, int kWaves, bool kOnce>
 static hipError_t combine_grad(const ExpertCombineGradArgs& a, hipStream_t s) {
   const int64_t units = cdiv(a.r.tokens, 4 / kWaves);
   const dim3 grid(static_cast<uint32_t>((units < kMostGroups ? units : kMostGroups) + a.r.experts * kPadParts));
   return by_choices(a.r.choices, [&](auto k) {
-    hipLaunchKernelGGL((expert_combine_grad_kernel<T, decltype(k)::value, kWaves>), grid, dim3(256), 0, s, a, units);
+    hipLaunchKernelGGL((expert_combine_grad_kernel<T, decltype(k)::value, kWaves, kOnce>), grid, dim3(256), 0, s, a, units);
   });
 }
 
@@ -573,8 +617,10 @@ hipError_t launch_expert_combine_grad(const ExpertCombineGradArgs& a, bool bf, h
   // one wave per token below 1024 columns (bf16, 8 choices: 16384 x 512 60 us, 78 with
   // four; x 768 89 and 94; x 1024 117 and 113; 8192 x 2048 131 and 115; 64 x 8192 26
   // and 11)
-  if (a.n < 1024) return bf ? combine_grad<uint16_t, 1>(a, s) : combine_grad<float, 1>(a, s);
-  return bf ? combine_grad<uint16_t, 4>(a, s) : combine_grad<float, 4>(a, s);
+  if (a.n < 1024) return bf ? combine_grad<uint16_t, 1, false>(a, s) : combine_grad<float, 1, false>(a, s);
+  if (passes_once(a.r, static_cast<int64_t>(a.n) * (bf ? 2 : 4) * (a.y ? 2 : 1)))
+    return bf ? combine_grad<uint16_t, 4, true>(a, s) : combine_grad<float, 4, true>(a, s);
+  return bf ? combine_grad<uint16_t, 4, false>(a, s) : combine_grad<float, 4, false>(a, s);
 }
 
 }  // namespace ortho
