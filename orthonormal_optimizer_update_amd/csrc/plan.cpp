@@ -747,14 +747,14 @@ ortho_status validate_adamw(int32_t count, const ortho_mat* X, const ortho_mat* 
   return ok ? ORTHO_OK : ORTHO_E_LAYOUT;
 }
 
-Deal deal(int64_t rows, int64_t cols, int64_t piece) {
-  // The widest that pads rows by at most an eighth more than the narrowest does.
+Deal deal(int64_t rows, int64_t cols, int64_t piece, int64_t slack) {
+  // The widest that pads rows by at most 1 / slack more than the narrowest does.
   Deal best{};
   int64_t least = 0;
   for (int lanes = 4; lanes <= 8; ++lanes) {
     const int64_t wide = piece << lanes, across = cdiv(cols, wide);
     if (lanes == 4) least = across * wide;
-    if (across * wide > least + least / 8) continue;
+    if (across * wide > least + least / slack) continue;
     best = {lanes, across, across * cdiv(rows, 256 >> lanes)};
   }
   return best;

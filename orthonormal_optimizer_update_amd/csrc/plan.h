@@ -205,12 +205,13 @@ ortho_status validate_adamw(int32_t count, const ortho_mat* X, const ortho_mat* 
                             const ortho_adamw* h);
 
 // How a kernel deals a rows x cols matrix to workgroups of 256 threads: 1 << lanes
-// threads (16 to 256) side by side in a row, `piece` elements each.
+// threads (16 to 256) side by side in a row, `piece` elements each, padding rows by at
+// most 1 / slack more than 16 would.
 struct Deal {
   int lanes;
   int64_t across, units;     // units along the columns, and in all
 };
-Deal deal(int64_t rows, int64_t cols, int64_t piece);
+Deal deal(int64_t rows, int64_t cols, int64_t piece, int64_t slack = 8);
 
 // Tokens by expert.  The pairs are cut into `tiles` of `tile` pairs, one workgroup
 // each; a tile's counts (one per expert) meet in the workspace.

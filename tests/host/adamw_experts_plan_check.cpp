@@ -26,14 +26,14 @@ static int failures = 0;
   } while (0)
 
 // Every element of a matrix belongs to one thread's piece, none to two.
-static void check_deal(int64_t rows, int64_t cols, int64_t piece) {
-  const Deal d = deal(rows, cols, piece);
+static void check_deal(int64_t rows, int64_t cols, int64_t piece, int64_t slack = 8) {
+  const Deal d = deal(rows, cols, piece, slack);
   EXPECT(d.lanes >= 4 && d.lanes <= 8, "%lld x %lld", (long long)rows, (long long)cols);
   const int64_t wide = piece << d.lanes, high = 256 >> d.lanes;
   EXPECT(d.across * wide >= cols && (d.across - 1) * wide < cols, "%lld", (long long)cols);
   EXPECT(d.units == d.across * ((rows + high - 1) / high), "%lld", (long long)rows);
   const int64_t least = (cols + 16 * piece - 1) / (16 * piece) * 16 * piece;
-  EXPECT(d.across * wide <= least + least / 8, "%lld", (long long)cols);
+  EXPECT(d.across * wide <= least + least / slack, "%lld", (long long)cols);
   // (32-bit numbers in the kernels on up to 2^40 elements; pieces of bytes count in 64)
   if (piece >= 8 && rows <= kMaxElements / cols) EXPECT(d.units < int64_t{1} << 31 && d.across < int64_t{1} << 31, "units");
 }
@@ -63,7 +63,10 @@ int main() {
                                       8193, 1 << 20, (1 << 20) + 1, 1 << 30};
   for (int64_t r : sizes)
     for (int64_t c : sizes)
-      for (int64_t p : {1, 8, 32}) check_deal(r, c, p);
+      for (int64_t p : {1, 8, 32}) {
+        check_deal(r, c, p);
+        check_deal(r, c, p, 4);
+      }
   check_deal(1, kMaxElements, 8);
   check_deal(1, kMaxElements, 32);
 
