@@ -584,6 +584,7 @@ def grad_norm_workspace_size(count: int) -> int:
 def grad_norm(G: Sequence, max_norm: float = float("inf"), out=None, ws=None):
     """The norm of all gradients together and the factor that clips it to max_norm (``grad_norm``
     of ortho.h), as the two elements of a float32 tensor: ``out[1:]`` is ``adamw_step``'s factor."""
+    G = tuple(G)   # (what can be gone through only once is looked at twice)
     first = _first(G)
     if out is None:
         import torch
@@ -621,6 +622,7 @@ def adamw_step(X: Sequence, G: Sequence, M: Sequence, V: Sequence, lr, step, bet
     states).  ``seed``: stochastic rounding of bf16 weights and of codes.  ``lr`` and ``step`` may be
     one-element tensors (float32, int64) on the GPU, read when the kernels run; ``factor`` is one
     such float32 that multiplies the gradients, NaN to leave all as it was."""
+    X = tuple(X)
     _run("adamw_step", _first(X), X, G, M, V, SM, SV, lr, step, betas[0], betas[1], eps, weight_decay,
          seed, factor)
 
