@@ -599,6 +599,7 @@ def adamw_states(X: Sequence, bits: int = 32):
     """States of ``adamw_step`` for the tensors X, at the start: (M, V, SM, SV), lists of float32
     zeros (bits 32; SM and SV are None), or of e4m3 codes of 0 with scales of 1 (bits 8)."""
     import torch
+    X = tuple(X)
     if bits == 32:
         return ([torch.zeros(x.shape, dtype=torch.float32, device=x.device) for x in X],
                 [torch.zeros(x.shape, dtype=torch.float32, device=x.device) for x in X], None, None)

@@ -66,3 +66,12 @@ def test_norm_and_step_of_iterators():
     api.adamw_step(iter(y), iter(g), iter(b[0]), iter(b[1]), 0.1, 1)
     for p, q in zip(x + a[0] + a[1], y + b[0] + b[1]):
         assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_states_for_an_iterator(bits):
+    shapes = [(3,), (4, 5), (2, 3, 64)]
+    want = api.adamw_states([torch.zeros(s) for s in shapes], bits)
+    got = api.adamw_states((torch.zeros(s) for s in shapes), bits)
+    for a, b in zip(got, want):
+        assert (a is None) == (b is None) and (a is None or [t.shape for t in a] == [t.shape for t in b])
