@@ -91,12 +91,17 @@ def build(verbose: bool = True) -> str:
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
-        binding = binding.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", "--offload-arch=gfx950", "-o", tmp, *objs]
     _run("link", cmd)
     os.replace(tmp, LIB)
-    _link_binding(binding)
+    # (callers of the C-ABI need neither torch nor Python's headers nor the host compiler)
+    try:
+        _link_binding(binding.result())
+    except Exception as e:
+        if os.path.exists(BINDING):   # an older one may not fit this library
+            os.remove(BINDING)
+        raise RuntimeError(f"built {LIB}, but not its binding for Python: {e}") from e
     if verbose:
         print(f"built {LIB} and {BINDING}")
     return LIB
