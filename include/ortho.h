@@ -463,10 +463,10 @@ typedef struct {
  *
  * The step uses m and v as computed; only what is kept for the next one is rounded.
  * A block's scale is its largest finite |m| (or sqrt(v)) / 448, at least 2^-126, and
- * 1 for a block of zeros; infinite and NaN values get the NaN code, but a v beyond
- * fp32's range counts as its largest number.  A v above 0 never gets the code of 0
- * (the least code, 2^-9, in its place), so that no later step divides by nothing but
- * eps.
+ * 1 for a block of zeros; infinite and NaN values get the NaN code.  A v above 0 never
+ * gets the code of 0 (the least code, 2^-9, in its place), so that no later step divides
+ * by nothing but eps.  Beside codes v itself may pass fp32's range, since its root does
+ * not; kept in fp32 such a v is infinite, and from then on its weight only decays.
  *
  * Stochastic rounding of bf16 weights and of codes: with u random bits out of
  * 2^n, a value that lies a part p of the way from one number of the type to the

@@ -142,10 +142,14 @@ __device__ __forceinline__ float root_of(float v) {
 }
 constexpr uint32_t kLeastRoot = 0x0d800000u, kInfinity = 0x7f800000u;   // 2^-100's bits
 
-// The roots of eight values that are not negative; what a code can say ends at fp32's
-// largest number (NaN stays).  Most waves hold no zero and nothing tiny or infinite,
-// and one look tells.  Returns whether there may be zeros.
-__device__ __forceinline__ bool roots8(float (&v)[8]) {
+// What a wave's values may be beside ordinary ones.
+struct Among {
+  bool zeros, far;   // far: infinite or NaN
+};
+
+// The roots of eight values that are not negative.  Most waves hold no zero and nothing
+// tiny, infinite or NaN, and one look tells.
+__device__ __forceinline__ Among roots8(float (&v)[8]) {
   uint32_t low = ~0u, high = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -155,22 +159,43 @@ __device__ __forceinline__ bool roots8(float (&v)[8]) {
   if (!__any(low < kLeastRoot || high >= kInfinity)) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = root_of<false>(v[j]);
-    return false;
+    return {false, false};
   }
+  const bool far = __any(high >= kInfinity);
   uint32_t least = ~0u;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v[j] = __builtin_elementwise_minimum(v[j], __FLT_MAX__);
-    least = min(least, __float_as_uint(v[j]) - 1);   // (0 counts for nothing)
-  }
-  if (__any(least < kLeastRoot - 1)) {
+  for (int j = 0; j < 8; ++j) least = min(least, __float_as_uint(v[j]) - 1);   // (0 counts for nothing)
+  if (far || __any(least < kLeastRoot - 1)) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = __builtin_sqrtf(v[j]);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = root_of<true>(v[j]);
   }
-  return true;
+  return {true, far};
+}
+
+__device__ __forceinline__ float value_of(float g) { return g; }
+__device__ __forceinline__ float value_of(uint16_t g) { return bf16_bits_to_f32(g); }
+__device__ __forceinline__ float value_of(uint8_t code, float scale) {
+  return __builtin_amdgcn_cvt_f32_fp8(code, 0) * scale;
+}
+
+// The weight of an element whose v came out infinite or NaN in fp32, and sqrt(v) in
+// place of it.  A root kept as a code, or a gradient, may have a square beyond fp32's
+// range; scaled by a power of two it has not, and the root is back within the range.
+// (Formed so where nothing is far, a square would be lost at the other end.)
+__device__ __forceinline__ float far_weight(const AdamwScalars& h, const StepScalars& s, float x, float g, float m,
+                                            float kept, float& root) {
+  g *= s.factor;
+  kept = h.b2 == 0.f ? 0.f * kept : kept;
+  const int e = max(0, __builtin_amdgcn_frexp_expf(fmaxf(__builtin_fabsf(kept), __builtin_fabsf(g))));
+  g = __builtin_ldexpf(g, -e);
+  kept = __builtin_ldexpf(kept, -e);
+  const float r = __builtin_sqrtf(h.b2 * (kept * kept) + h.c2 * (g * g));
+  root = r < __builtin_inff() ? fminf(__builtin_ldexpf(r, e), __FLT_MAX__) : r;
+  const float down = fmaf(r, s.root, __builtin_ldexpf(h.eps, -e));
+  return fmaf(-s.size, __builtin_ldexpf(m, -e) * __builtin_amdgcn_rcpf(down), s.keep * x);
 }
 
 // The tensor of a unit; `first` is this lane's.
@@ -486,9 +511,15 @@ __device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScala
       vv[j] *= vv[j];
       moments(h, s, gv[j], mv[j], vv[j]);
     }
-    const bool zeros = roots8(vv);
+    const Among among = roots8(vv);
 #pragma unroll
     for (int j = 0; j < 8; ++j) xv[j] = weight(h, s, xv[j], mv[j], vv[j]);
+    if (__builtin_expect(among.far, false)) {   // (read anew: kept until here it would cost every launch registers)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!(vv[j] < __builtin_inff()) && c + j < cols)
+          xv[j] = far_weight(h, s, value_of(x[c + j]), value_of(g[c + j]), mv[j], value_of(v[c + j], *sv), vv[j]);
+    }
     if constexpr (kStochastic) bits.all(seed_m, seed_v);
     // past the row's end: zeros, which enter no maximum
     if constexpr (!kWhole) {
@@ -498,7 +529,7 @@ __device__ __forceinline__ void row_piece(const AdamwScalars& h, const StepScala
     }
     float ms2, vs2;
     const uint2 um = to_codes8<kStochastic, false>(mv, seed_m, false, ms2);
-    const uint2 uv = to_codes8<kStochastic, true>(vv, seed_v, zeros, vs2);
+    const uint2 uv = to_codes8<kStochastic, true>(vv, seed_v, among.zeros, vs2);
     if constexpr (kWhole) cols = c + 8;
     if constexpr (kWhole) {
       store_any<kOnce>(m + c, um);
@@ -563,10 +594,13 @@ __global__ __launch_bounds__(256, 5) void adamw_rows_kernel(AdamwRows a) {
 // weights with gradients in bf16 115 us (10.1 bytes each, 5.9 TB/s; 123 through the
 // caches), in fp32 184 (5.9); stochastically the vector unit has as much to do in bf16
 // (136 us; 152 in the kernel above), about 20 instructions an element for its random
-// bits.  Six waves per SIMD hide 2% more of it than five; weights in fp32 would not fit
-// their registers.
+// bits.  Six waves per SIMD hide 2% more of it than five; weights in fp32 take five and
+// no more (with gradients in fp32, stochastically, 183 us, to nearest 184; with as many
+// as fit, 187 and 188).
 template <typename TX, typename TG, bool kStochastic, bool kOnce>
-__global__ __launch_bounds__(256, sizeof(TX) == 2 ? 6 : 5) void adamw_codes_kernel(AdamwRows a) {
+__global__ __launch_bounds__(256)
+    __attribute__((amdgpu_waves_per_eu(sizeof(TX) == 4 ? 5 : 6, sizeof(TX) == 4 ? 5 : 8))) void adamw_codes_kernel(
+        AdamwRows a) {
   const int first = a.first[threadIdx.x & (kLanes - 1)];
   const StepScalars s = step_scalars(a.h);
   if (s.skip) return;
