@@ -2,6 +2,8 @@
 // (internal to libortho.so).  gfx950 only.
 #pragma once
 
+#include <stddef.h>
+
 #include "common.h"
 
 namespace ortho {
@@ -13,7 +15,8 @@ namespace ortho {
 // count).  What is not used of `first` is the type's largest value.
 //
 // A tensor's entry is read by scalar loads, which drop the two low bits of both
-// parts of an address: entries hold no type of less than four bytes.
+// parts of an address: entries hold no type of less than four bytes.  The assertions
+// below add up their members, so that another member has to be looked at there.
 constexpr int kUnit = 2048;
 constexpr int kLanes = 64;
 
@@ -42,6 +45,8 @@ struct FlatTensor {
   int32_t index;                 // of the tensor in the call
   int32_t kind;
 };
+static_assert(sizeof(FlatTensor) == 4 * 8 + 8 + 2 * 4 && alignof(FlatTensor) == 8 && offsetof(FlatTensor, n) == 4 * 8,
+              "pointers at multiples of 8, nothing below four bytes, no gap");
 struct AdamwFlat {
   static constexpr int kMost = 64;
   AdamwScalars h;
@@ -63,6 +68,8 @@ struct RowTensor {
   int32_t lanes;
   int32_t index, kind;
 };
+static_assert(sizeof(RowTensor) == 6 * 8 + 12 * 4 && alignof(RowTensor) == 8 && offsetof(RowTensor, ldx) == 6 * 8,
+              "pointers at multiples of 8, nothing below four bytes, no gap");
 struct AdamwRows {
   static constexpr int kMost = 38;   // 96 bytes each
   AdamwScalars h;
@@ -77,6 +84,8 @@ struct NormTensor {
   int64_t ld, cols;
   int32_t rows, across, lanes, bf;
 };
+static_assert(sizeof(NormTensor) == 3 * 8 + 4 * 4 && alignof(NormTensor) == 8 && offsetof(NormTensor, rows) == 3 * 8,
+              "pointers at multiples of 8, nothing below four bytes, no gap");
 struct NormParts {
   static constexpr int kMost = 64;
   NormTensor t[kMost];
@@ -84,6 +93,11 @@ struct NormParts {
   int64_t units;
   double* part;                  // one sum per workgroup
 };
+
+static_assert(offsetof(AdamwFlat, t) % 8 == 0 && offsetof(AdamwRows, t) % 8 == 0 && offsetof(NormParts, t) % 8 == 0 &&
+                  offsetof(AdamwFlat, first) % 4 == 0 && offsetof(AdamwRows, first) % 4 == 0 &&
+                  offsetof(NormParts, first) % 8 == 0,
+              "the tables' places in a launch's arguments");
 
 hipError_t launch_adamw_flat(const AdamwFlat& a, bool stochastic, hipStream_t s);
 // kind: all tensors', if they have one and their states are codes, else -1.
