@@ -44,13 +44,13 @@
  *   - Every matrix is an ortho_mat: a DEVICE pointer to a row-major matrix with
  *     `rows` x `cols` elements and leading dimension `ld` (elements, >= cols).
  *     The caller allocates and owns all device memory, including the
- *     workspace; the library never allocates or frees memory inside a call.
+ *     workspace; the library never allocates or frees any inside a call.
  *   - All work is enqueued on `stream` (a hipStream_t, NULL = the default
  *     stream) and the calls return without synchronising.  Argument errors are
  *     reported synchronously, before anything is enqueued.
  *   - A call keeps no state between calls: everything it needs is in the
  *     caller's buffers.  Concurrent calls must use different workspaces.
- *   - No call performs host synchronisation or allocation, so a sequence of
+ *   - No call synchronises the host or allocates device memory, so a sequence of
  *     calls can be captured into a HIP graph.
  *   - Numerical breakdown cannot be reported synchronously; when `dev_status`
  *     is non-NULL the kernels OR these bits into the device int32 it points to
@@ -458,8 +458,9 @@ typedef struct {
  * have memory of their own, apart from each other, from those of every other tensor
  * and from every G (else ORTHO_E_LAYOUT; rows between another matrix's rows of the
  * same pitch are apart), from lr_dev, step_dev and factor too: a weight that is
- * listed twice is refused.  So is a leading dimension from 2^32 on.  (Where the host
- * has no memory left to look: ORTHO_E_WORKSPACE.)
+ * listed twice is refused.  So is a leading dimension from 2^32 on.  (To look for
+ * overlaps among more than 61 matrices the call takes host memory, 32 bytes for each,
+ * and frees it before it returns; where there is none left: ORTHO_E_WORKSPACE.)
  *
  * The step uses m and v as computed; only what is kept for the next one is rounded.
  * A block's scale is its largest finite |m| (or sqrt(v)) / 448, at least 2^-126, and
