@@ -477,7 +477,7 @@ typedef struct {
  * bits come from (seed, t, index of the tensor in the call, index of the element
  * row * cols + column) alone:
  *     mix(h): h ^= h >> 16, h *= 0x7feb352d, h ^= h >> 15, h *= 0x846ca68b,
- *             h ^= h >> 16                                          (32 bits)
+ *             h ^= h >> 16                 (32 bits; a published hash, lowbias32)
  *     key = mix(low word of seed); then key = mix(key ^ mix(word + 0x9e3779b9))
  *           for the words seed's high, t's low, t's high, tensor
  *     a = mix(element's low word ^ (key + 0x9e3779b9 * its high word))
