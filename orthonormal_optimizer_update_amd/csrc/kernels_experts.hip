@@ -16,7 +16,9 @@ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // workgroup adds what it needs of them itself (64 tiles of 128 experts are 32 KB
 // from L2, less than another launch takes), and its 16 waves place their pairs, 64 at
 // a time, in order.  One tile needs no other's counts and no first launch.  Bound by
-// latency: 16384 x 8 pairs, 128 experts take 2.8 and 6.8 us, 33 x 8 pairs 4.2.
+// latency: 16384 x 8 pairs, 128 experts take 2.0 and 6.6 us, 33 x 8 pairs 4.2.  (What the
+// workgroups add up grows with the square of the tiles: 131072 x 8 pairs of 256 experts
+// take 32 us in all, 262144 x 8 of 512 160.)
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kExperts = 1024;
 
 __device__ __forceinline__ int expert_of(const ExpertSortArgs& a, int pair) {
@@ -484,7 +486,9 @@ __device__ __forceinline__ void grad_chunk(const ExpertCombineGradArgs& a, int64
 
 // kWaves waves per token, kAtOnce choices at a time: their rows of Y are read, the
 // products with dOut summed, their rows of dY written.  Bound by HBM: 8192 tokens x
-// 2048 bf16, 8 choices 107 to 113 us (5.2 TB/s), 114 to 119 through the caches.
+// 2048 bf16, 8 choices 107 to 113 us (5.2 TB/s), 114 to 119 through the caches; fp32 228
+// (5.0).  Columns that the four waves' chunks do not share evenly, or rows that begin
+// inside a line, take longer: bf16 x 1100 131 us (2.3 TB/s), x 2001 170, x 2100 186.
 template <typename T, int kAtOnce, int kWaves, bool kOnce>
 __global__ __launch_bounds__(256) void expert_combine_grad_kernel(ExpertCombineGradArgs a, int64_t groups) {
   __shared__ float red[2][4][64];
@@ -540,6 +544,7 @@ constexpr int64_t kMostGroups = 1 << 20;   // workgroups of a launch; more units
 // caches and through them: combine of 2048 tokens, 67 MB, 14.6 and 13.3 us, of 4096 28.7
 // and 33.2, of 8192 55.5 and 63.0; its gradient, of 1024, 67 MB, 15.0 and 13.2 us, of 2048
 // 29.7 and 34.8; codes gathered for 4096, 67 MB, 19.6 and 19.7, for 8192 32.4 and 36.7).
+// Each was timed alone, without the call that reads what it writes.
 bool passes_once(const ExpertRowsArgs& r, int64_t row_bytes) {
   return static_cast<int64_t>(r.tokens) * r.choices * row_bytes >= int64_t{1} << 27;
 }
