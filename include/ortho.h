@@ -467,7 +467,8 @@ typedef struct {
  * 1 for a block of zeros; infinite and NaN values get the NaN code.  A v above 0 never
  * gets the code of 0 (the least code, 2^-9, in its place), so that no later step divides
  * by nothing but eps.  Beside codes v itself may pass fp32's range, since its root does
- * not; kept in fp32 such a v is infinite, and from then on its weight only decays.
+ * not; kept in fp32 such a v is infinite, and from then on its weight only decays (with
+ * beta2 = 0 v and then the weight become NaN).
  *
  * Stochastic rounding of bf16 weights and of codes: with u random bits out of
  * 2^n, a value that lies a part p of the way from one number of the type to the
